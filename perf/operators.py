@@ -190,9 +190,9 @@ def prepare(case, seed):
         if own:
             from w8a8_int8_dynamic_amd import W8A8Linear, ops
             if case["codes"]:
-                s["packed"], s["packed_scale"] = ops.mxfp4_prepack_weight(s["wq"], s["ws"])
+                s["packed"], s["packed_scale"] = ops.fp4_prepack_weight(s["wq"], s["ws"])
             else:
-                s["layer"] = W8A8Linear.from_quantized(s["wq"], s["ws"], s["bias"], scheme="mxfp4")
+                s["layer"] = W8A8Linear.from_quantized(s["wq"], s["ws"], s["bias"], scheme="fp4")
         return s
     batch, m = case["batch"], case["batch"] * case["tokens"]
     vec = DTYPES[case["vectors"]]
@@ -304,11 +304,11 @@ def _own(s):
     case = s["case"]
     dtype = DTYPES[case["dtype"]]
     if case["op"] == "quant":
-        return ops.mxfp4_dequant(*ops.mxfp4_quant(s["x"]), dtype=dtype)
+        return ops.fp4_dequant(*ops.fp4_quant_per_block(s["x"]), dtype=dtype)
     if case["op"] == "linear":
         if not case["codes"]:
             return s["layer"](s["x"])
-        return ops.mxfp4_scaled_mm(s["xq"], s["xs"], s["packed"], s["packed_scale"], case["n"], s["bias"],
+        return ops.fp4_scaled_mm(s["xq"], s["xs"], s["packed"], s["packed_scale"], case["n"], s["bias"],
                                    out_dtype=dtype)
     out = case["out"]
     if case["op"] == "norm":
