@@ -421,6 +421,130 @@ w8a8_status_t fp8_quant_scaled_mm_tile(const uint16_t *x, int64_t ldx, uint8_t *
 int w8a8_fp8_tile_count(void);
 int w8a8_fp8_tile_auto(int64_t M, int64_t N, int64_t K);
 
+/*
+ * ---- The microscaled 4-bit (MX FP4) layer ----
+ * Weights and activations in blocks of 32 along K: e2m1 elements with one
+ * power-of-two (e8m0) scale byte per block, as the published OCP
+ * Microscaling Formats specification v1.0 defines MXFP4. Half the weight
+ * bytes of the 8-bit layers, and the fastest matrix instructions of gfx950
+ * take both operands as they are.
+ *
+ * The quant rule, for each block of 32 elements x of a row (widened to fp32
+ * exactly):
+ *   a = max |x|;  e = clamp(floor(log2 a) - 2, -127, 127), -127 for a = 0
+ *   scale byte = e + 127;  code = e2m1(x / 2^e): nearest of 0, .5, 1, 1.5, 2,
+ *   3, 4, 6 (ties to the even code, larger values to 6), sign in bit 3
+ *   A block that holds NaN or an infinity: scale byte 255, codes 0; the
+ *   block stands for NaN, and so does every output that it takes part in.
+ * Two codes to a byte, the even element in the low nibble: a row of K
+ * elements is K/2 code bytes and K/32 scale bytes. K is a multiple of 32
+ * everywhere.
+ */
+
+/* Largest K accepted by fp4_scaled_mm. */
+#define W8A8_FP4_MAX_K 262144
+
+/* Element type of a 16- or 32-bit float tensor. */
+typedef enum w8a8_dtype {
+    W8A8_T_BF16 = 0,
+    W8A8_T_F32 = 1,
+    W8A8_T_F16 = 2
+} w8a8_dtype_t;
+
+/*
+ * fp4_quant_per_block - rows x [M, ldx] of x_dtype to codes xq [M, ldq] and
+ * scale bytes x_scale [M, lds].
+ * Requirements: M >= 0 (0 is a no-op), K a multiple of 32, ldx >= K, ldq >=
+ * K/2, lds >= K/32; x 16-byte aligned and ldx a multiple of 8 (fp32: 4); xq
+ * 4-byte aligned and ldq a multiple of 4. Bytes past K/2 and K/32 of a row
+ * are not touched.
+ */
+w8a8_status_t fp4_quant_per_block(const void *x, int x_dtype, int64_t M, int64_t K, int64_t ldx,
+                                  uint8_t *xq, int64_t ldq, uint8_t *x_scale, int64_t lds,
+                                  void *stream);
+
+/* The values that codes and scales stand for, rounded once to out_dtype
+ * (exact in bf16 and fp32 while they stay in range; NaN for scale byte
+ * 255). Requirements as above, with out in x's place. */
+w8a8_status_t fp4_dequant(const uint8_t *xq, int64_t ldq, const uint8_t *x_scale, int64_t lds,
+                          int64_t M, int64_t K, int out_dtype, void *out, int64_t ldo,
+                          void *stream);
+
+/* Bytes of the two packed buffers of a weight [N, K]: the codes in the
+ * layout of int8_prepack_weight over code bytes (int8_prepack_weight_bytes
+ * (N, K/2)), and the scales, round_up(N, 16) * round_up(K, 512) / 32 bytes:
+ * byte 256*(nb*chunks + c) + 16*r + j is block 16*c + j of channel 16*nb + r
+ * (chunks = ceil(K / 512)), 127 outside the weight. 0 for sizes out of
+ * range. */
+size_t fp4_prepack_weight_bytes(int64_t N, int64_t K);
+size_t fp4_prepack_scale_bytes(int64_t N, int64_t K);
+
+/*
+ * fp4_prepack_weight - load-time repack of a weight quantized before: codes
+ * wq [N, ldq] and scale bytes w_scale [N, lds] (no alignment rule).
+ * fp4_quant_prepack_weight - the quant rule applied to a bf16 or fp32 weight
+ * w [N, ldw] (w_dtype: W8A8_W_*), written straight into the packed buffers.
+ * Requirements: N >= 1; both packed buffers 16-byte aligned and as long as
+ * the functions above say; w as x of fp4_quant_per_block.
+ * fp4_unpack_weight - the inverse of both repacks.
+ */
+w8a8_status_t fp4_prepack_weight(const uint8_t *wq, int64_t ldq, const uint8_t *w_scale,
+                                 int64_t lds, int64_t N, int64_t K, void *w_packed,
+                                 void *s_packed, void *stream);
+w8a8_status_t fp4_quant_prepack_weight(const void *w, int w_dtype, int64_t N, int64_t K,
+                                       int64_t ldw, void *w_packed, void *s_packed, void *stream);
+w8a8_status_t fp4_unpack_weight(const void *w_packed, const void *s_packed, int64_t N, int64_t K,
+                                uint8_t *wq, int64_t ldq, uint8_t *w_scale, int64_t lds,
+                                void *stream);
+
+/*
+ * fp4_scaled_mm - the product of quantized rows with a packed weight:
+ *   acc[m,n] = sum over blocks b of 2^(ex[m,b] + ew[n,b]) *
+ *              sum over k in b of e2m1(xq[m,k]) * e2m1(wq[n,k])
+ * with fp32 sums (exact within a block; sums below fp32's normal range may
+ * be flushed to zero);
+ *   W8A8_OUT_BF16 / W8A8_OUT_F16: acc + bias[n] (bias in the output's type,
+ *   or NULL) in fp32, rounded to nearest even;  W8A8_OUT_I32: acc as fp32.
+ * Requirements: M >= 0 (0 is a no-op), N >= 1, K <= W8A8_FP4_MAX_K, K/2 <=
+ * ldq <= W8A8_MAX_LDQ, K/32 <= lds <= W8A8_MAX_LDQ, ldo >= N; xq, w_packed
+ * and s_packed 16-byte aligned, ldq a multiple of 16; x_scale 16-byte
+ * aligned, lds a multiple of 16 and M * lds bytes readable (what lies past
+ * K/32 of a row has no effect); out aligned to its element size.
+ * fp4_scaled_mm_tile: with an explicit tile (0 <= tile <
+ * w8a8_fp4_tile_count()) or -1. Tiles may differ in the order of their fp32
+ * sums.
+ */
+w8a8_status_t fp4_scaled_mm(const uint8_t *xq, int64_t ldq, const uint8_t *x_scale, int64_t lds,
+                            const void *w_packed, const void *s_packed, const uint16_t *bias,
+                            int64_t M, int64_t N, int64_t K, int mode, void *out, int64_t ldo,
+                            void *stream);
+w8a8_status_t fp4_scaled_mm_tile(const uint8_t *xq, int64_t ldq, const uint8_t *x_scale,
+                                 int64_t lds, const void *w_packed, const void *s_packed,
+                                 const uint16_t *bias, int64_t M, int64_t N, int64_t K, int mode,
+                                 void *out, int64_t ldo, void *stream, int tile);
+
+/*
+ * fp4_quant_scaled_mm - fp4_quant_per_block of x [M, ldx], then
+ * fp4_scaled_mm of the result, in one call; xq and x_scale are written.
+ * Requirements: those of the two.
+ */
+w8a8_status_t fp4_quant_scaled_mm(const void *x, int x_dtype, int64_t ldx, uint8_t *xq,
+                                  int64_t ldq, uint8_t *x_scale, int64_t lds,
+                                  const void *w_packed, const void *s_packed,
+                                  const uint16_t *bias, int64_t M, int64_t N, int64_t K, int mode,
+                                  void *out, int64_t ldo, void *stream);
+w8a8_status_t fp4_quant_scaled_mm_tile(const void *x, int x_dtype, int64_t ldx, uint8_t *xq,
+                                       int64_t ldq, uint8_t *x_scale, int64_t lds,
+                                       const void *w_packed, const void *s_packed,
+                                       const uint16_t *bias, int64_t M, int64_t N, int64_t K,
+                                       int mode, void *out, int64_t ldo, void *stream, int tile);
+
+/* Tiles of the 4-bit matmul: their number, a name of each, and the automatic
+ * choice. */
+int w8a8_fp4_tile_count(void);
+const char *w8a8_fp4_tile_name(int tile);
+int w8a8_fp4_tile_auto(int64_t M, int64_t N, int64_t K);
+
 /* Number of tile configurations, a short name of one, and the tile the
  * automatic choice picks for a shape. Main kernel: "128x192/m1n2k2/l33" is
  * tile rows x columns / wave row groups, column groups and k-groups / token

@@ -23,6 +23,10 @@ W8A8_OUT_I32 = 1
 W8A8_OUT_F16 = 2
 W8A8_MAX_K = 131056
 W8A8_MAX_LDQ = 4194304
+W8A8_FP4_MAX_K = 262144
+W8A8_T_BF16 = 0
+W8A8_T_F32 = 1
+W8A8_T_F16 = 2
 
 # name -> (restype, argtypes), in the order of include/w8a8.h
 _i64, _vp, _int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
@@ -67,6 +71,24 @@ SIGNATURES = {
     "w8a8_fp8_tile_count": (_int, []),
     "w8a8_fused_wait_limit": (_int, [_int]),
     "w8a8_fp8_tile_auto": (_int, [_i64, _i64, _i64]),
+    "fp4_quant_per_block": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "fp4_dequant": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _int, _vp, _i64, _vp]),
+    "fp4_prepack_weight_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "fp4_prepack_scale_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "fp4_prepack_weight": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "fp4_quant_prepack_weight": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "fp4_unpack_weight": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "fp4_scaled_mm": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _i64,
+                             _vp]),
+    "fp4_scaled_mm_tile": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp,
+                                  _i64, _vp, _int]),
+    "fp4_quant_scaled_mm": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
+                                   _i64, _int, _vp, _i64, _vp]),
+    "fp4_quant_scaled_mm_tile": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
+                                        _i64, _i64, _int, _vp, _i64, _vp, _int]),
+    "w8a8_fp4_tile_count": (_int, []),
+    "w8a8_fp4_tile_name": (ctypes.c_char_p, [_int]),
+    "w8a8_fp4_tile_auto": (_int, [_i64, _i64, _i64]),
     "w8a8_mm_tile_count": (_int, []),
     "w8a8_mm_tile_name": (ctypes.c_char_p, [_int]),
     "w8a8_mm_tile_auto": (_int, [_i64, _i64, _i64]),

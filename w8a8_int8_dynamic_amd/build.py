@@ -32,7 +32,8 @@ LIBRARY = os.path.join(HERE, "libw8a8.so")
 # W8A8_TIMELINE (per-workgroup phase stamps of the main kernel, timeline.hpp).
 TIMELINE_LIBRARY = os.path.join(HERE, "libw8a8_timeline.so")
 TIMELINE_SOURCE = "scaled_mm.hip"
-SOURCES = ["quant.hip", "prepack.hip", "scaled_mm.hip", "scaled_mm_fp8.hip", "skinny_mm.hip", "api.cpp"]
+SOURCES = ["quant.hip", "prepack.hip", "scaled_mm.hip", "scaled_mm_fp8.hip", "skinny_mm.hip",
+           "quant_fp4.hip", "scaled_mm_fp4.hip", "api.cpp", "api_fp4.cpp"]
 ARCH = "gfx950"
 
 FLAGS = [

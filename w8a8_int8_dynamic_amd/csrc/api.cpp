@@ -9,16 +9,19 @@
 #include <limits>
 #include <string>
 
-#include "w8a8.h"   // include/ is on the include path
-#include "internal.hpp"
+#include "api.hpp"
 
-#define W8A8_API extern "C" __attribute__((visibility("default")))
+using namespace w8a8::api;
 
 namespace {
 
 thread_local std::string g_last_error;
 
-w8a8_status_t fail(w8a8_status_t s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+}  // namespace
+
+namespace w8a8 {
+namespace api {
+
 w8a8_status_t fail(w8a8_status_t s, const char *fmt, ...)
 {
     char buf[256];
@@ -36,9 +39,10 @@ w8a8_status_t ok()
     return W8A8_OK;
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace api
+}  // namespace w8a8
 
-constexpr int64_t kMaxRows = std::numeric_limits<int32_t>::max();
+namespace {
 
 // Per-device cache of "is gfx950": 0 unknown, 1 yes, 2 no.
 constexpr int kMaxDevices = 64;
@@ -66,6 +70,11 @@ int query_supported(int device)
     return c == 1;
 }
 
+}  // namespace
+
+namespace w8a8 {
+namespace api {
+
 w8a8_status_t check_device()
 {
     int dev = -1;
@@ -83,6 +92,11 @@ w8a8_status_t launched(hipError_t e, const char *what)
         return fail(W8A8_ERR_HIP, "%s launch failed: %s", what, hipGetErrorString(e));
     return ok();
 }
+
+}  // namespace api
+}  // namespace w8a8
+
+namespace {
 
 w8a8_status_t quant_common(const void *x, int kind, int64_t M, int64_t K, int64_t ldx, int8_t *q,
                            int64_t ldq, float *s, void *stream, const char *what, bool fp8 = false)

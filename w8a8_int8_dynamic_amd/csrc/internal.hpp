@@ -49,6 +49,19 @@ hipError_t launch_quant_prepack(const void *w, bool w_f32, int64_t N, int64_t K,
                                 void *packed, float *w_scale, hipStream_t stream,
                                 bool fp8 = false);
 
+// ---- microscaled 4-bit rows and weights (quant_fp4.hip) ----
+// K is a multiple of 32. kind: the element kind of x / out. launch_prepack_fp4
+// takes codes and scale bytes made before (kind -1: w holds code bytes, ldw
+// bytes apart) or a bf16 or fp32 weight to quantize (ws unused).
+hipError_t launch_quant_fp4(const void *x, int kind, int64_t rows, int64_t K, int64_t ldx, uint8_t *q, int64_t ldq,
+                            uint8_t *s, int64_t lds, hipStream_t stream);
+hipError_t launch_dequant_fp4(const uint8_t *q, int64_t ldq, const uint8_t *s, int64_t lds, int64_t rows, int64_t K,
+                              int kind, void *out, int64_t ldo, hipStream_t stream);
+hipError_t launch_prepack_fp4(const void *w, int kind, const uint8_t *ws, int64_t N, int64_t K, int64_t ldw,
+                              int64_t lds, void *packed, void *spacked, hipStream_t stream);
+hipError_t launch_unpack_fp4(const void *packed, const void *spacked, int64_t N, int64_t K, uint8_t *wq, int64_t ldw,
+                             uint8_t *ws, int64_t lds, hipStream_t stream);
+
 // ---- scaled matmul (scaled_mm.hip) ----
 struct MmArgs {
     const int8_t *xq;
@@ -80,6 +93,14 @@ struct MmArgs {
     int kbs;
     unsigned *split_count;
     int *split_part;
+    // Microscaled 4-bit operands: xq and wp hold code bytes (two codes each)
+    // and K, ldq and kblocks count those; sx [M, lds] are the token scale
+    // bytes, sw the packed weight scales (launch_prepack_fp4) and blocks the
+    // scales per row (K / 16 of the bytes). xs and ws are unused.
+    const uint8_t *sx;
+    const uint8_t *sw;
+    int64_t lds;
+    int blocks;
 };
 
 // Split of K for the small-M kernel: how many workgroups share a tile's K
@@ -142,6 +163,14 @@ int mm_tile_auto(int64_t M, int64_t N, int64_t K);
 // (mm_grid_fits); fp8_launch_fits is the same for the e4m3 twin's tiles.
 bool mm_launch_fits(int tile, int64_t M, int64_t N);
 bool fp8_launch_fits(int tile, int64_t M, int64_t N);
+
+// ---- the microscaled 4-bit matmul (scaled_mm_fp4.hip) ----
+// mode kOutI32 stores the raw fp32 sums.
+int fp4_tile_count();
+const char *fp4_tile_name(int tile);
+int fp4_tile_auto(int64_t M, int64_t N, int64_t K);
+bool fp4_launch_fits(int tile, int64_t M, int64_t N);
+hipError_t launch_scaled_mm_fp4(const MmArgs &a, int mode, int tile, hipStream_t stream);
 
 // ---- the e4m3 twin of the matmul (scaled_mm_fp8.hip) ----
 // Tiles are numbered as the int8 ones (main, then small-M); mode kOutI32

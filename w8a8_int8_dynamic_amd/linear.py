@@ -24,17 +24,21 @@ class W8A8Linear(torch.nn.Module):
     scheme "int8" (the default): int8 codes, bf16 or fp16 activations.
     scheme "fp8": the e4m3 twin (page "Online Quantization": FP8 W8A8 with
     dynamic per-token activation scales), bf16 activations.
+    scheme "fp4": weights and activations in microscaled 4-bit floating point
+    (MX FP4: e2m1 codes, a power-of-two scale per 32 elements along K), bf16 or
+    fp16 activations; in_features a multiple of 32.
 
-    Build with ``from_float`` (online per-channel weight quantization on the
-    GPU, written straight into the load-time layout) or ``from_quantized``
-    (int8 weights and fp32 scales already made offline).
+    Build with ``from_float`` (online weight quantization on the GPU, written
+    straight into the load-time layout) or ``from_quantized`` (weights and
+    scales already made offline: int8 and fp32, or for "fp4" the uint8 codes
+    [N, K/2] and scale bytes [N, K/32] of ops.fp4_quant_per_block).
     """
 
     def __init__(self, w_packed: torch.Tensor, w_scale: torch.Tensor, out_features: int,
                  in_features: int, bias: Optional[torch.Tensor] = None, scheme: str = "int8"):
         super().__init__()
-        if scheme not in ("int8", "fp8"):
-            raise ValueError(f"scheme must be 'int8' or 'fp8', got {scheme!r}")
+        if scheme not in ("int8", "fp8", "fp4"):
+            raise ValueError(f"scheme must be 'int8', 'fp8' or 'fp4', got {scheme!r}")
         self.scheme = scheme
         self.in_features = in_features
         self.out_features = out_features
@@ -54,8 +58,14 @@ class W8A8Linear(torch.nn.Module):
 
     @classmethod
     def from_quantized(cls, wq: torch.Tensor, w_scale: torch.Tensor,
-                       bias: Optional[torch.Tensor] = None) -> "W8A8Linear":
+                       bias: Optional[torch.Tensor] = None, scheme: str = "int8") -> "W8A8Linear":
+        if scheme not in ("int8", "fp4"):
+            raise ValueError(f"scheme must be 'int8' or 'fp4', got {scheme!r}")
         N, K = wq.shape
+        if scheme == "fp4":
+            if (w_scale == 255).any():
+                raise ValueError("weight scales must be finite")
+            return cls(*ops.fp4_prepack_weight(wq, w_scale), N, 2 * K, bias, scheme)
         if not torch.isfinite(w_scale).all():
             raise ValueError("weight scales must be finite")
         packed = ops.prepack_weight(wq.contiguous())
@@ -69,6 +79,11 @@ class W8A8Linear(torch.nn.Module):
         quant rule works on fp32 values)."""
         w = weight if weight.dtype in (torch.bfloat16, torch.float32) else weight.to(torch.float32)
         N, K = w.shape
+        if scheme == "fp4":
+            packed, ws = ops.fp4_quant_prepack_weight(w.contiguous())
+            if (ws == 255).any():
+                raise ValueError("weight scales must be finite")
+            return cls(packed, ws, N, K, bias, scheme)
         quant = ops.fp8_quant_prepack_weight if scheme == "fp8" else ops.quant_prepack_weight
         packed, ws = quant(w.contiguous())
         if not torch.isfinite(ws).all():
@@ -90,6 +105,10 @@ class W8A8Linear(torch.nn.Module):
                 raise TypeError(f"the fp8 scheme takes bfloat16 activations, got {x2.dtype}")
             out, _, _ = ops.fp8_quant_scaled_mm(x2, self.w_packed, self.w_scale,
                                                 self.out_features, bias)
+        elif self.scheme == "fp4":
+            if x2.dtype not in (torch.bfloat16, torch.float16):
+                raise TypeError(f"the fp4 scheme takes bfloat16 or float16 activations, got {x2.dtype}")
+            out, _, _ = ops.fp4_quant_scaled_mm(x2, self.w_packed, self.w_scale, self.out_features, bias)
         else:
             wsp = self.workspace if x2.dtype == torch.bfloat16 else None
             out, _, _ = ops.quant_scaled_mm(x2, self.w_packed, self.w_scale, self.out_features,
@@ -107,20 +126,20 @@ def quantize_linear_layers(module: torch.nn.Module, method: str = "int8",
     """Replace the torch.nn.Linear layers of `module` by W8A8Linear layers.
 
     The selection follows the page "Online Quantization" (Parameters table):
-    `method` is "int8" or "fp8"; `activation_scheme` must be "dynamic"
-    (activation scales computed per token at run time, the only scheme
-    implemented); `ignored_layers` holds name patterns of layers to keep in
+    `method` is "int8", "fp8" or "fp4"; `activation_scheme` must be "dynamic"
+    (activation scales computed at run time, the only scheme implemented); `ignored_layers` holds name patterns of layers to keep in
     their float type. A layer is kept when its qualified name (as in
     module.named_modules()) matches a pattern by fnmatch or contains it.
     Weights are quantized online on their device (W8A8Linear.from_float).
     Anything the path cannot run raises ValueError naming the layer: a layer
-    on the CPU, or in_features not a multiple of 16. Returns `module`, or the
+    on the CPU, or in_features not a multiple of 16 (32 for "fp4"). Returns `module`, or the
     replacement when `module` is itself a Linear."""
-    if method not in ("int8", "fp8"):
-        raise ValueError(f"method must be 'int8' or 'fp8', got {method!r}")
+    if method not in ("int8", "fp8", "fp4"):
+        raise ValueError(f"method must be 'int8', 'fp8' or 'fp4', got {method!r}")
     if activation_scheme != "dynamic":
         raise ValueError(f"only activation_scheme='dynamic' is implemented, got {activation_scheme!r}")
     patterns = [p for p in ignored_layers if p]
+    step = 32 if method == "fp4" else 16
 
     def kept(name: str) -> bool:
         return any(fnmatch.fnmatchcase(name, p) or p in name for p in patterns)
@@ -128,8 +147,8 @@ def quantize_linear_layers(module: torch.nn.Module, method: str = "int8",
     def convert(name: str, lin: torch.nn.Linear) -> W8A8Linear:
         if not lin.weight.is_cuda:
             raise ValueError(f"layer {name!r} is on {lin.weight.device}; move the model to the GPU first")
-        if lin.in_features % 16 != 0:
-            raise ValueError(f"layer {name!r}: in_features {lin.in_features} is not a multiple of 16")
+        if lin.in_features % step != 0:
+            raise ValueError(f"layer {name!r}: in_features {lin.in_features} is not a multiple of {step}")
         bias = None if lin.bias is None else lin.bias.detach()
         return W8A8Linear.from_float(lin.weight.detach(), bias, scheme=method)
 

@@ -19,7 +19,10 @@ __all__ = ["quant_per_token", "quant_per_channel", "prepack_weight", "quant_prep
            "prepack_weight_bytes", "scaled_mm", "quant_scaled_mm", "tile_count", "tile_name",
            "workspace_bytes", "new_workspace",
            "tile_auto", "device_supported", "fp8_quant_per_token", "fp8_quant_per_channel",
-           "fp8_quant_prepack_weight", "fp8_scaled_mm", "fp8_quant_scaled_mm", "fp8_tile_count"]
+           "fp8_quant_prepack_weight", "fp8_scaled_mm", "fp8_quant_scaled_mm", "fp8_tile_count",
+           "fp4_quant_per_block", "fp4_dequant", "fp4_prepack_weight", "fp4_quant_prepack_weight",
+           "fp4_unpack_weight", "fp4_scaled_mm", "fp4_quant_scaled_mm", "fp4_tile_count", "fp4_tile_name",
+           "fp4_tile_auto"]
 
 
 def _stream(t: torch.Tensor) -> int:
@@ -427,6 +430,213 @@ def fp8_quant_scaled_mm(x: torch.Tensor, w_packed: torch.Tensor, ws: Optional[to
              xs.data_ptr(), w_packed.data_ptr(), ptr(ws), ptr(bias), M, N, K, mode,
              out.data_ptr(), _ld(out), _stream(x), tile)
     return out, xq, xs
+
+
+# ---- the microscaled 4-bit (MX FP4) layer ---------------------------------
+_DTYPE = {torch.bfloat16: _lib.W8A8_T_BF16, torch.float16: _lib.W8A8_T_F16, torch.float32: _lib.W8A8_T_F32}
+_FP4_BLOCK = 32
+
+
+def _fp4_k(K: int) -> int:
+    if K < _FP4_BLOCK or K % _FP4_BLOCK != 0:
+        raise ValueError(f"K must be a multiple of {_FP4_BLOCK}, got {K}")
+    return K
+
+
+def _bytes_rows(M: int, n: int, device) -> torch.Tensor:
+    """uint8 [M, n] view of a buffer whose rows are padded to 16 bytes."""
+    return torch.empty((M, _round_up(n, 16)), dtype=torch.uint8, device=device)[:, :n]
+
+
+def _fp4_rows(xq: torch.Tensor, xs: torch.Tensor) -> Tuple[int, int]:
+    """(M, K) of 4-bit codes [M, K/2] and their scale bytes [M, K/32]."""
+    _matrix(xq, "xq", torch.uint8)
+    _matrix(xs, "xs", torch.uint8)
+    M, K = xq.shape[0], _fp4_k(2 * xq.shape[1])
+    if xs.shape != (M, K // _FP4_BLOCK):
+        raise ValueError(f"xs must have shape {(M, K // _FP4_BLOCK)}, got {tuple(xs.shape)}")
+    _same_device(xq, xs)
+    return M, K
+
+
+def _scale_rows(xs: torch.Tensor) -> torch.Tensor:
+    """xs itself when its rows start on 16-byte boundaries and the last one can
+    be read to a whole 16 bytes, else a copy into a row-padded buffer."""
+    M, n = xs.shape
+    ld = _ld(xs)
+    if xs.data_ptr() % 16 == 0 and ld % 16 == 0 and \
+            xs.untyped_storage().nbytes() - xs.storage_offset() >= M * ld:
+        return xs
+    buf = _bytes_rows(M, n, xs.device)
+    buf.copy_(xs)
+    return buf
+
+
+def _ldp(t: torch.Tensor) -> int:
+    """Row pitch of a row-padded byte buffer (one row: its padded length)."""
+    return t.stride(0) if t.shape[0] > 1 else _round_up(t.shape[1], 16)
+
+
+def fp4_quant_per_block(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
+                        xs: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """MX FP4 quantization of bf16, fp16 or fp32 x [M, K] (K a multiple of 32):
+    (uint8 codes [M, K/2], the even element in the low nibble; uint8 scale
+    bytes [M, K/32], one power of two per 32 elements)."""
+    if x.dtype not in _DTYPE:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    _matrix(x, "x", x.dtype)
+    M, K = x.shape[0], _fp4_k(x.shape[1])
+    x = _rows_aligned(x, 4 if x.dtype == torch.float32 else 8)
+    xq = _bytes_rows(M, K // 2, x.device) if xq is None else xq
+    xs = _bytes_rows(M, K // _FP4_BLOCK, x.device) if xs is None else xs
+    if _fp4_rows(xq, xs) != (M, K):
+        raise ValueError(f"xq must have shape {(M, K // 2)}")
+    _same_device(x, xq)
+    with torch.cuda.device(x.device):
+        call("fp4_quant_per_block", x.data_ptr(), _DTYPE[x.dtype], M, K, _ld(x), xq.data_ptr(), _ld(xq),
+             xs.data_ptr(), _ld(xs), _stream(x))
+    return xq, xs
+
+
+def fp4_dequant(xq: torch.Tensor, xs: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The values [M, K] that 4-bit codes and scale bytes stand for, rounded
+    once to dtype (bf16 and fp32: exact)."""
+    if dtype not in _DTYPE:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    M, K = _fp4_rows(xq, xs)
+    if xq.data_ptr() % 4 != 0 or _ld(xq) % 4 != 0:
+        xq = _rows_aligned(xq, 16)
+    out = torch.empty((M, K), dtype=dtype, device=xq.device)
+    with torch.cuda.device(xq.device):
+        call("fp4_dequant", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), M, K, _DTYPE[dtype],
+             out.data_ptr(), K, _stream(xq))
+    return out
+
+
+def _fp4_packed(N: int, K: int, device) -> Tuple[torch.Tensor, torch.Tensor]:
+    L = _lib.lib()
+    w, s = L.fp4_prepack_weight_bytes(N, K), L.fp4_prepack_scale_bytes(N, K)
+    if w == 0 or s == 0:
+        raise ValueError(f"no packed size for N={N}, K={K}")
+    return (torch.empty((w,), dtype=torch.uint8, device=device),
+            torch.empty((s,), dtype=torch.uint8, device=device))
+
+
+def _check_fp4_packed(w_packed: torch.Tensor, s_packed: torch.Tensor, N: int, K: int) -> None:
+    L = _lib.lib()
+    for t, n, name in ((w_packed, L.fp4_prepack_weight_bytes(N, K), "w_packed"),
+                       (s_packed, L.fp4_prepack_scale_bytes(N, K), "s_packed")):
+        if not t.is_cuda or t.dtype != torch.uint8 or not t.is_contiguous() or n == 0 or t.numel() < n:
+            raise ValueError(f"{name} must be a uint8 device buffer of the packed layout (N, K)")
+
+
+def fp4_prepack_weight(wq: torch.Tensor, ws: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Repack a weight quantized before, codes [N, K/2] and scale bytes
+    [N, K/32], into the two buffers that fp4_scaled_mm reads."""
+    N, K = _fp4_rows(wq, ws)
+    packed, spacked = _fp4_packed(N, K, wq.device)
+    with torch.cuda.device(wq.device):
+        call("fp4_prepack_weight", wq.data_ptr(), _ld(wq), ws.data_ptr(), _ld(ws), N, K, packed.data_ptr(),
+             spacked.data_ptr(), _stream(wq))
+    return packed, spacked
+
+
+def fp4_quant_prepack_weight(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Online MX FP4 quantization of a bf16 or fp32 weight [N, K] into the packed
+    buffers: the same bytes as fp4_prepack_weight(*fp4_quant_per_block(w))."""
+    if w.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"w must be bfloat16 or float32, got {w.dtype}")
+    _matrix(w, "w", w.dtype)
+    N, K = w.shape[0], _fp4_k(w.shape[1])
+    f32 = w.dtype == torch.float32
+    w = _rows_aligned(w, 4 if f32 else 8)
+    packed, spacked = _fp4_packed(N, K, w.device)
+    with torch.cuda.device(w.device):
+        call("fp4_quant_prepack_weight", w.data_ptr(), 0 if f32 else 1, N, K, _ld(w), packed.data_ptr(),
+             spacked.data_ptr(), _stream(w))
+    return packed, spacked
+
+
+def fp4_unpack_weight(w_packed: torch.Tensor, s_packed: torch.Tensor, N: int, K: int
+                      ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Inverse of fp4_prepack_weight: codes [N, K/2] and scale bytes [N, K/32]."""
+    _check_fp4_packed(w_packed, s_packed, N, _fp4_k(K))
+    _same_device(w_packed, s_packed)
+    wq = torch.empty((N, K // 2), dtype=torch.uint8, device=w_packed.device)
+    ws = torch.empty((N, K // _FP4_BLOCK), dtype=torch.uint8, device=w_packed.device)
+    with torch.cuda.device(w_packed.device):
+        call("fp4_unpack_weight", w_packed.data_ptr(), s_packed.data_ptr(), N, K, wq.data_ptr(), K // 2,
+             ws.data_ptr(), K // _FP4_BLOCK, _stream(w_packed))
+    return wq, ws
+
+
+def _fp4_out(M: int, N: int, bias, out_dtype, out, device):
+    if out_dtype not in _FP8_OUT_MODE:
+        raise TypeError("out_dtype must be torch.bfloat16, torch.float16 or torch.float32")
+    mode = _FP8_OUT_MODE[out_dtype]
+    if mode != W8A8_OUT_I32:
+        _vector(bias, N, "bias", out_dtype)
+    elif bias is not None:
+        raise ValueError("out_dtype=torch.float32 gives the raw sums: bias must be None")
+    out = torch.empty((M, N), dtype=out_dtype, device=device) if out is None else out
+    _matrix(out, "out", out_dtype)
+    if out.shape != (M, N):
+        raise ValueError(f"out must have shape {(M, N)}")
+    return mode, out
+
+
+def fp4_scaled_mm(xq: torch.Tensor, xs: torch.Tensor, w_packed: torch.Tensor, s_packed: torch.Tensor,
+                  N: int, bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                  out: Optional[torch.Tensor] = None, tile: int = -1) -> torch.Tensor:
+    """The product [M, N] of MX FP4 rows (codes xq [M, K/2], scale bytes xs
+    [M, K/32]) with a packed weight, plus bias, rounded to out_dtype (bf16 or
+    fp16; the bias in the same type), or the raw fp32 sums."""
+    M, K = _fp4_rows(xq, xs)
+    _check_fp4_packed(w_packed, s_packed, N, K)
+    mode, out = _fp4_out(M, N, bias, out_dtype, out, xq.device)
+    _same_device(xq, w_packed, s_packed, bias, out)
+    xq, xs = _rows_aligned(xq, 16), _scale_rows(xs)
+    with torch.cuda.device(xq.device):
+        call("fp4_scaled_mm_tile", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ldp(xs), w_packed.data_ptr(),
+             s_packed.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, mode, out.data_ptr(),
+             _ld(out), _stream(xq), tile)
+    return out
+
+
+def fp4_quant_scaled_mm(x: torch.Tensor, w_packed: torch.Tensor, s_packed: torch.Tensor, N: int,
+                        bias: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                        out: Optional[torch.Tensor] = None, tile: int = -1
+                        ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """fp4_quant_per_block of x [M, K] and fp4_scaled_mm in one call: (out, xq,
+    xs). out_dtype defaults to x's type, bf16 for fp32 x."""
+    if x.dtype not in _DTYPE:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    _matrix(x, "x", x.dtype)
+    M, K = x.shape[0], _fp4_k(x.shape[1])
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
+    _check_fp4_packed(w_packed, s_packed, N, K)
+    mode, out = _fp4_out(M, N, bias, out_dtype, out, x.device)
+    _same_device(x, w_packed, s_packed, bias, out)
+    x = _rows_aligned(x, 4 if x.dtype == torch.float32 else 8)
+    xq, xs = _bytes_rows(M, K // 2, x.device), _bytes_rows(M, K // _FP4_BLOCK, x.device)
+    with torch.cuda.device(x.device):
+        call("fp4_quant_scaled_mm_tile", x.data_ptr(), _DTYPE[x.dtype], _ld(x), xq.data_ptr(), _ldp(xq),
+             xs.data_ptr(), _ldp(xs), w_packed.data_ptr(), s_packed.data_ptr(),
+             None if bias is None else bias.data_ptr(), M, N, K, mode, out.data_ptr(), _ld(out), _stream(x), tile)
+    return out, xq, xs
+
+
+def fp4_tile_count() -> int:
+    return _lib.lib().w8a8_fp4_tile_count()
+
+
+def fp4_tile_name(tile: int) -> str:
+    return _lib.lib().w8a8_fp4_tile_name(tile).decode()
+
+
+def fp4_tile_auto(M: int, N: int, K: int) -> int:
+    return _lib.lib().w8a8_fp4_tile_auto(M, N, K)
 
 
 def fp8_tile_count() -> int:
