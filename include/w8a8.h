@@ -545,6 +545,94 @@ int w8a8_fp4_tile_count(void);
 const char *w8a8_fp4_tile_name(int tile);
 int w8a8_fp4_tile_auto(int64_t M, int64_t N, int64_t K);
 
+/*
+ * ---- Norms around a layer ----
+ * The modulated norm in front of a block, whose result a layer takes as
+ * 16-bit values or as codes, and the gate, residual scale and norm behind it.
+ *   rms:   n(v) = v / sqrt(mean(v^2) + eps)
+ *   layer: n(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps)
+ *   norm(v) = (n(v) * weight + bias) * (1 + scale) + shift
+ * in fp32 over the K elements of a row; every result is rounded once. Where
+ * the squares or sums leave fp32's range the result is what they give.
+ */
+typedef enum w8a8_norm_kind {
+    W8A8_NORM_RMS = 0,
+    W8A8_NORM_LAYER = 1
+} w8a8_norm_kind_t;
+
+/* A norm and its vectors. weight and bias [K] in vec_dtype, or NULL (1 and
+ * 0). scale and shift [groups, ld] in mod_dtype, or NULL (0): row m takes
+ * their row m / (M / groups), so M is a multiple of groups (1: one vector for
+ * all rows; M: one per row). Vectors are aligned to their element size. */
+typedef struct w8a8_norm {
+    int kind;               /* w8a8_norm_kind_t */
+    float eps;              /* finite, >= 0 */
+    const void *weight;
+    const void *bias;
+    const void *scale;
+    const void *shift;
+    int64_t ld_scale;
+    int64_t ld_shift;
+    int64_t groups;
+    int vec_dtype;          /* w8a8_dtype_t */
+    int mod_dtype;
+} w8a8_norm_t;
+
+/* How a norm's result is written: 16-bit floats, or the codes and row scales
+ * that int8_quant_per_token / fp8_quant_per_token would give for the fp32
+ * result (with no rounding in between). A row whose result is not finite
+ * gets a scale that is not finite. */
+typedef enum w8a8_norm_out {
+    W8A8_NORM_OUT_16 = 0,
+    W8A8_NORM_OUT_INT8 = 1,
+    W8A8_NORM_OUT_FP8 = 2
+} w8a8_norm_out_t;
+
+/*
+ * norm_rows - the norm of each row of x [M, ldx] (x_dtype) to out [M, ldo]:
+ * act_dtype (bf16 or fp16, and x_dtype itself unless that is fp32), or codes
+ * with out_scale fp32 [M].
+ * Requirements: M >= 0 (0 is a no-op), K >= 1, ldx >= K, ldo >= K; tensors
+ * aligned to their element size, codes 8-byte aligned with ldo a multiple of
+ * 8. Rows may have any pitch and start.
+ */
+w8a8_status_t norm_rows(const void *x, int x_dtype, int64_t M, int64_t K, int64_t ldx,
+                        const w8a8_norm_t *norm, int act_dtype, int out_kind, void *out,
+                        int64_t ldo, float *out_scale, void *stream);
+
+/* A block's way back into the residual stream x [M, ldx] (bf16, fp16, or fp32
+ * with a 16-bit y):
+ *   r = residual_scale * x + branch_scale * gate * post(y)
+ * y [M, ldy]; post: a norm with weight and bias only, or NULL (y itself);
+ * gate [gate_groups, ld_gate] with rows as a norm's scale, or NULL (1); r
+ * [M, ldr] in x's type. r may be x itself (same pointer and pitch). */
+typedef struct w8a8_residual {
+    const void *x;
+    const void *y;
+    void *r;
+    int64_t ldx;
+    int64_t ldy;
+    int64_t ldr;
+    const void *gate;
+    int64_t ld_gate;
+    int64_t gate_groups;
+    const w8a8_norm_t *post;
+    float residual_scale;
+    float branch_scale;
+    int x_dtype;
+    int y_dtype;            /* bf16 or fp16 */
+    int gate_dtype;
+} w8a8_residual_t;
+
+/*
+ * gated_residual_rows - r, and with a norm (or NULL) also norm(r) to out as
+ * norm_rows writes it (16-bit: in y's type), taken from r before its
+ * rounding to the stored type. Requirements: those of norm_rows.
+ */
+w8a8_status_t gated_residual_rows(const w8a8_residual_t *res, int64_t M, int64_t K,
+                                  const w8a8_norm_t *norm, int out_kind, void *out, int64_t ldo,
+                                  float *out_scale, void *stream);
+
 /* Number of tile configurations, a short name of one, and the tile the
  * automatic choice picks for a shape. Main kernel: "128x192/m1n2k2/l33" is
  * tile rows x columns / wave row groups, column groups and k-groups / token

@@ -28,6 +28,31 @@ W8A8_T_BF16 = 0
 W8A8_T_F32 = 1
 W8A8_T_F16 = 2
 
+W8A8_NORM_RMS = 0
+W8A8_NORM_LAYER = 1
+W8A8_NORM_OUT_16 = 0
+W8A8_NORM_OUT_INT8 = 1
+W8A8_NORM_OUT_FP8 = 2
+
+
+class NormStruct(ctypes.Structure):
+    """w8a8_norm_t"""
+    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p),
+                ("ld_scale", ctypes.c_int64), ("ld_shift", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("vec_dtype", ctypes.c_int), ("mod_dtype", ctypes.c_int)]
+
+
+class ResidualStruct(ctypes.Structure):
+    """w8a8_residual_t"""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("r", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64), ("gate_groups", ctypes.c_int64),
+                ("post", ctypes.POINTER(NormStruct)), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("x_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int),
+                ("gate_dtype", ctypes.c_int)]
+
+
 # name -> (restype, argtypes), in the order of include/w8a8.h
 _i64, _vp, _int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
 SIGNATURES = {
@@ -86,6 +111,8 @@ SIGNATURES = {
                                    _i64, _int, _vp, _i64, _vp]),
     "fp4_quant_scaled_mm_tile": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
                                         _i64, _i64, _int, _vp, _i64, _vp, _int]),
+    "norm_rows": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _int, _vp, _i64, _vp, _vp]),
+    "gated_residual_rows": (_int, [_vp, _i64, _i64, _vp, _int, _vp, _i64, _vp, _vp]),
     "w8a8_fp4_tile_count": (_int, []),
     "w8a8_fp4_tile_name": (ctypes.c_char_p, [_int]),
     "w8a8_fp4_tile_auto": (_int, [_i64, _i64, _i64]),

@@ -62,6 +62,38 @@ hipError_t launch_prepack_fp4(const void *w, int kind, const uint8_t *ws, int64_
 hipError_t launch_unpack_fp4(const void *packed, const void *spacked, int64_t N, int64_t K, uint8_t *wq, int64_t ldw,
                              uint8_t *ws, int64_t lds, hipStream_t stream);
 
+// ---- norms before a block, gate, residual and norm after it (norm_rows.hip) ----
+// One pass over rows of K elements:
+//   v = x, or with y: v = residual_scale * x + branch_scale * gate * post(y),
+//       stored to r in x's type;
+//   h = next(v) to out (16-bit floats, or codes with a scale per row).
+// Element kinds: x_kind of x and r, act_kind of y and a 16-bit out.
+constexpr int kNormNone = -1, kNormRms = 0, kNormLayer = 1;
+constexpr int kNormOut16 = 0, kNormOutInt8 = 1, kNormOutFp8 = 2;
+struct NormVectors {
+    int kind;                    // kNorm*
+    float eps;
+    int vec_kind, mod_kind;      // element kinds of weight and bias, scale and shift
+    const void *weight, *bias;   // [K] or null (1, 0)
+    const void *scale, *shift;   // [groups, ld] or null (0, 0): h * (1 + scale) + shift
+    int64_t ld_scale, ld_shift;
+    int64_t group_rows;          // rows per group of scale and shift
+};
+struct NormRowsArgs {
+    const void *x, *y;
+    void *r, *out;
+    float *out_scale;
+    int64_t ldx, ldy, ldr, ldo;
+    int64_t rows, K;
+    int x_kind, act_kind, out_kind;
+    const void *gate;            // [groups, ld_gate] or null (1)
+    int gate_kind;
+    int64_t ld_gate, gate_rows;
+    float residual_scale, branch_scale;
+    NormVectors post, next;
+};
+hipError_t launch_norm_rows(const NormRowsArgs &a, hipStream_t stream);
+
 // ---- scaled matmul (scaled_mm.hip) ----
 struct MmArgs {
     const int8_t *xq;

@@ -115,6 +115,25 @@ class W8A8Linear(torch.nn.Module):
                                             bias, workspace=wsp)
         return out.reshape(*lead, self.out_features)
 
+    def forward_quantized(self, xq: torch.Tensor, xs: torch.Tensor,
+                          out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+        """The layer's product alone, for activations quantized elsewhere (by the
+        ops that end in quant_per_token for "int8" and "fp8", by
+        fp4_quant_per_block for "fp4"): codes [M, K] (fp4: [M, K/2]) and their
+        scales to [M, N] in out_dtype (bf16 or fp16)."""
+        if out_dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"out_dtype must be bfloat16 or float16, got {out_dtype}")
+        K = xq.shape[-1] * (2 if self.scheme == "fp4" else 1)
+        if K != self.in_features:
+            raise ValueError(f"expected codes of {self.in_features} elements, got {K}")
+        bias = self.bias_f16 if out_dtype == torch.float16 else self.bias
+        if self.scheme == "fp4":
+            return ops.fp4_scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype)
+        if self.scheme == "fp8":
+            return ops.fp8_scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype)
+        return ops.scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype,
+                             workspace=self.workspace)
+
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
                 f"bias={self.bias is not None}, scheme={self.scheme}")

@@ -8,6 +8,8 @@ contiguous (stride 1); the row stride becomes the leading dimension.
 """
 from __future__ import annotations
 
+import ctypes
+from dataclasses import dataclass
 from typing import Optional, Tuple
 
 import torch
@@ -22,7 +24,8 @@ __all__ = ["quant_per_token", "quant_per_channel", "prepack_weight", "quant_prep
            "fp8_quant_prepack_weight", "fp8_scaled_mm", "fp8_quant_scaled_mm", "fp8_tile_count",
            "fp4_quant_per_block", "fp4_dequant", "fp4_prepack_weight", "fp4_quant_prepack_weight",
            "fp4_unpack_weight", "fp4_scaled_mm", "fp4_quant_scaled_mm", "fp4_tile_count", "fp4_tile_name",
-           "fp4_tile_auto"]
+           "fp4_tile_auto", "Norm", "norm", "norm_quant_per_token", "fp8_norm_quant_per_token", "gated_residual",
+           "gated_residual_norm", "gated_residual_norm_quant", "fp8_gated_residual_norm_quant"]
 
 
 def _stream(t: torch.Tensor) -> int:
@@ -657,3 +660,187 @@ def tile_auto(M: int, N: int, K: int) -> int:
 
 def device_supported(device: int = 0) -> bool:
     return bool(_lib.lib().w8a8_device_supported(device))
+
+
+# ---- norms around a layer -------------------------------------------------
+@dataclass(frozen=True)
+class Norm:
+    """A norm over the last dimension and its vectors:
+
+        n(v) = v / sqrt(mean(v^2) + eps)                        kind "rms"
+        n(v) = (v - mean(v)) / sqrt(var(v) + eps)               kind "layer"
+        (n(v) * weight + bias) * (1 + scale) + shift
+
+    weight, bias: [K]. scale, shift: [K], or [G, K] for rows in G equal groups
+    (row m of M takes vector m // (M // G): images of a batch, or tokens with
+    a vector each). bf16, fp16 or fp32, weight and bias in one type, scale and
+    shift in one type; the last dimension contiguous."""
+    kind: str = "rms"
+    weight: Optional[torch.Tensor] = None
+    bias: Optional[torch.Tensor] = None
+    scale: Optional[torch.Tensor] = None
+    shift: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+
+
+_NORM_KIND = {"rms": _lib.W8A8_NORM_RMS, "layer": _lib.W8A8_NORM_LAYER}
+_CODE_TYPE = {_lib.W8A8_NORM_OUT_INT8: torch.int8, _lib.W8A8_NORM_OUT_FP8: torch.uint8}
+
+
+def _groups(t: torch.Tensor, M: int, K: int, ref: torch.Tensor, name: str) -> Tuple[int, int]:
+    """(groups, leading dimension) of a vector per group, [K] or [G, K]."""
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    shape = t.shape
+    if t.device != ref.device or len(shape) not in (1, 2) or shape[-1] != K or (K > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be [{K}] or [G, {K}] on {ref.device} with a contiguous last dimension")
+    if len(shape) == 1:
+        return 1, K
+    G = shape[0]
+    if G < 1 or M % G != 0:
+        raise ValueError(f"{M} rows do not split into the {G} rows of {name}")
+    return G, (t.stride(0) if G > 1 else K)
+
+
+def _norm_struct(n: Norm, M: int, K: int, ref: torch.Tensor) -> _lib.NormStruct:
+    if n.kind not in _NORM_KIND:
+        raise ValueError(f"kind must be 'rms' or 'layer', got {n.kind!r}")
+    s = _lib.NormStruct(kind=_NORM_KIND[n.kind], eps=n.eps)
+    for name, t in (("weight", n.weight), ("bias", n.bias)):
+        if t is not None:
+            if t.dim() != 1:
+                raise ValueError(f"{name} must be [{K}], got shape {tuple(t.shape)}")
+            _groups(t, M, K, ref, name)
+            setattr(s, name, t.data_ptr())
+            s.vec_dtype = _DTYPE[t.dtype]
+    if n.weight is not None and n.bias is not None and n.weight.dtype != n.bias.dtype:
+        raise TypeError("weight and bias must have one type")
+    for name, t in (("scale", n.scale), ("shift", n.shift)):
+        if t is not None:
+            G, ld = _groups(t, M, K, ref, name)
+            if s.groups not in (0, G):
+                raise ValueError("scale and shift must have the same number of rows")
+            s.groups = G
+            setattr(s, name, t.data_ptr())
+            setattr(s, "ld_" + name, ld)
+            s.mod_dtype = _DTYPE[t.dtype]
+    if n.scale is not None and n.shift is not None and n.scale.dtype != n.shift.dtype:
+        raise TypeError("scale and shift must have one type")
+    return s
+
+
+def _norm_out(M: int, K: int, act: torch.dtype, kind: int, device):
+    """(out, scales or None) of a norm."""
+    if kind == _lib.W8A8_NORM_OUT_16:
+        return torch.empty((M, K), dtype=act, device=device), None
+    codes = torch.empty((M, _round_up(K, 16)), dtype=_CODE_TYPE[kind], device=device)[:, :K]
+    return codes, torch.empty((M,), dtype=torch.float32, device=device)
+
+
+def _norm_call(x: torch.Tensor, norm: Norm, kind: int, out_dtype: Optional[torch.dtype]):
+    if x.dtype not in _DTYPE:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    _matrix(x, "x", x.dtype)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
+    if out_dtype not in _ACT_ENTRY or (x.dtype != torch.float32 and out_dtype != x.dtype):
+        raise TypeError(f"out_dtype must be {'bfloat16 or float16' if x.dtype == torch.float32 else x.dtype}")
+    M, K = x.shape
+    n = _norm_struct(norm, M, K, x)
+    out, scales = _norm_out(M, K, out_dtype, kind, x.device)
+    with torch.cuda.device(x.device):
+        call("norm_rows", x.data_ptr(), _DTYPE[x.dtype], M, K, _ld(x), ctypes.byref(n), _DTYPE[out_dtype], kind,
+             out.data_ptr(), _ldp(out) if scales is not None else _ld(out),
+             None if scales is None else scales.data_ptr(), _stream(x))
+    return out, scales
+
+
+def norm(x: torch.Tensor, norm: Norm, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """The norm of each row of x [M, K] (bf16, fp16 or fp32) in x's type; of fp32
+    x in out_dtype (bf16, the default, or fp16)."""
+    return _norm_call(x, norm, _lib.W8A8_NORM_OUT_16, out_dtype)[0]
+
+
+def norm_quant_per_token(x: torch.Tensor, norm: Norm) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The norm of each row of x [M, K] as int8 codes and fp32 scales [M], the
+    operands of scaled_mm: quant_per_token's rule on the fp32 norm."""
+    return _norm_call(x, norm, _lib.W8A8_NORM_OUT_INT8, None)
+
+
+def fp8_norm_quant_per_token(x: torch.Tensor, norm: Norm) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The e4m3 twin of norm_quant_per_token: uint8 e4m3 codes and fp32 scales."""
+    return _norm_call(x, norm, _lib.W8A8_NORM_OUT_FP8, None)
+
+
+def _residual_call(x: torch.Tensor, y: torch.Tensor, norm: Optional[Norm], kind: int,
+                   gate: Optional[torch.Tensor], post: Optional[Norm], residual_scale: float,
+                   branch_scale: float, out: Optional[torch.Tensor]):
+    _matrix(y, "y", _act_dtype(y))
+    if x.dtype not in (y.dtype, torch.float32):
+        raise TypeError(f"x must be {y.dtype} (y's type) or float32, got {x.dtype}")
+    _matrix(x, "x", x.dtype)
+    M, K = x.shape
+    if y.shape != (M, K):
+        raise ValueError(f"y must have shape {(M, K)}, got {tuple(y.shape)}")
+    r = torch.empty((M, K), dtype=x.dtype, device=x.device) if out is None else out
+    _matrix(r, "out", x.dtype)
+    if r.shape != (M, K):
+        raise ValueError(f"out must have shape {(M, K)}")
+    _same_device(x, y, r)
+    s = _lib.ResidualStruct(x=x.data_ptr(), y=y.data_ptr(), r=r.data_ptr(), ldx=_ld(x), ldy=_ld(y), ldr=_ld(r),
+                            residual_scale=residual_scale, branch_scale=branch_scale, x_dtype=_DTYPE[x.dtype],
+                            y_dtype=_DTYPE[y.dtype])
+    if gate is not None:
+        s.gate_groups, s.ld_gate = _groups(gate, M, K, x, "gate")
+        s.gate, s.gate_dtype = gate.data_ptr(), _DTYPE[gate.dtype]
+    if post is not None:
+        if post.scale is not None or post.shift is not None:
+            raise ValueError("post takes no scale or shift: the gate multiplies its result")
+        p = _norm_struct(post, M, K, x)
+        s.post = ctypes.pointer(p)
+    n, h, hs = None, None, None
+    if norm is not None:
+        n = _norm_struct(norm, M, K, x)
+        h, hs = _norm_out(M, K, y.dtype, kind, x.device)
+    with torch.cuda.device(x.device):
+        call("gated_residual_rows", ctypes.byref(s), M, K, None if n is None else ctypes.byref(n), kind,
+             None if h is None else h.data_ptr(), 0 if h is None else _ldp(h) if hs is not None else _ld(h),
+             None if hs is None else hs.data_ptr(), _stream(x))
+    return r, h, hs
+
+
+def gated_residual(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                   post: Optional[Norm] = None, residual_scale: float = 1.0, branch_scale: float = 1.0,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A block's output y [M, K] (bf16 or fp16) back into the residual stream x
+    (y's type or fp32): residual_scale * x + branch_scale * gate * post(y), in
+    x's type. gate: [K] or [G, K] as a Norm's scale (None: 1). post: a Norm
+    with weight and bias, or None (y itself). out may be x itself."""
+    return _residual_call(x, y, None, _lib.W8A8_NORM_OUT_16, gate, post, residual_scale, branch_scale, out)[0]
+
+
+def gated_residual_norm(x: torch.Tensor, y: torch.Tensor, norm: Norm, gate: Optional[torch.Tensor] = None,
+                        post: Optional[Norm] = None, residual_scale: float = 1.0, branch_scale: float = 1.0,
+                        out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """gated_residual and the next block's norm in one pass: (r, norm(r) in y's
+    type). The norm sees r before its rounding to x's type."""
+    return _residual_call(x, y, norm, _lib.W8A8_NORM_OUT_16, gate, post, residual_scale, branch_scale, out)[:2]
+
+
+def gated_residual_norm_quant(x: torch.Tensor, y: torch.Tensor, norm: Norm,
+                              gate: Optional[torch.Tensor] = None, post: Optional[Norm] = None,
+                              residual_scale: float = 1.0, branch_scale: float = 1.0,
+                              out: Optional[torch.Tensor] = None
+                              ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """gated_residual_norm with the norm as int8 codes and fp32 scales, the
+    operands of scaled_mm: (r, codes, scales)."""
+    return _residual_call(x, y, norm, _lib.W8A8_NORM_OUT_INT8, gate, post, residual_scale, branch_scale, out)
+
+
+def fp8_gated_residual_norm_quant(x: torch.Tensor, y: torch.Tensor, norm: Norm,
+                                  gate: Optional[torch.Tensor] = None, post: Optional[Norm] = None,
+                                  residual_scale: float = 1.0, branch_scale: float = 1.0,
+                                  out: Optional[torch.Tensor] = None
+                                  ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The e4m3 twin of gated_residual_norm_quant: (r, uint8 e4m3 codes, scales)."""
+    return _residual_call(x, y, norm, _lib.W8A8_NORM_OUT_FP8, gate, post, residual_scale, branch_scale, out)
