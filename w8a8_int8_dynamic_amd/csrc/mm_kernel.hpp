@@ -218,6 +218,17 @@ struct Tile {
     static constexpr int SIDE_PER_THREAD = (SIDE + THREADS - 1) / THREADS;
     static constexpr int FLAG = MAIN + SIDE * 4;        // one word: fused-path decision
     static constexpr int LDS = FLAG + 16;
+    // The 4-bit kernel's block scales: a ring of SC_SLOTS LDS slots behind the
+    // image ring, each the 16 scale bytes of SC_STAGES stages (4 k-blocks) for
+    // every token and channel of the tile, loaded in units of 64 rows (one
+    // wave's 16 bytes a lane) SC_LEAD slots ahead.
+    static constexpr int SC_STAGES = 4 / WK;
+    static constexpr int SC_LEAD = WK, SC_SLOTS = 2 * WK;
+    static constexpr int SC_UNITS = (BM + BN) / 64;
+    static constexpr int SC_LPW = (SC_UNITS + NW - 1) / NW;   // loads per wave per slot
+    static constexpr int SC_SLOT = (BM + BN) * 16;            // bytes
+    static constexpr int SIDE4 = cmax(MAIN, RING + SC_SLOTS * SC_SLOT);
+    static constexpr int LDS4 = SIDE4 + BN * 4;               // then the bias of the tile
     static_assert(NW == 4 || NW == 8, "four or eight wavefronts per workgroup");
     static_assert(BM % (32 * WM) == 0 && BN % (32 * WN) == 0, "tile/wave mismatch");
     static_assert(AIMG % NW == 0, "token loads must split evenly over waves");
@@ -225,7 +236,21 @@ struct Tile {
     static_assert(LT >= 1 && (NS & (NS - 1)) == 0, "LDS ring of a power-of-two stages");
     static_assert(WLDS || LW >= LT, "weight lead >= token lead");
     static_assert(VM < 64 && (LT + 1) * LPW < 64 && (LW + 1) * LPW < 64, "vmcnt range");
-    static_assert(LDS <= 160 * 1024, "LDS budget");
+    static_assert(LDS <= 160 * 1024 && LDS4 <= 160 * 1024, "LDS budget");
+    static_assert(LT <= 3 && GROUP % SC_STAGES == 0, "scales land a slot's stages before their use");
+    // Loads that step v issues for the scales.
+    static constexpr int scale_loads(int v) { return (v + 1 + 64) % SC_STAGES == 0 ? SC_LPW : 0; }
+    // VM for the 4-bit kernel at step u (modulo GROUP): the same wait with the
+    // scale loads counted (a step issues images, scales, weights).
+    static constexpr int vm_fp4(int u)
+    {
+        int a = LB + scale_loads(u - LT), b = 0;
+        for (int d = 1; d < LT; ++d)
+            a += LPW + scale_loads(u - d);
+        for (int d = 1; d < (WLDS ? LT : LW); ++d)
+            b += LPW + scale_loads(u - d);
+        return WLDS || b < a ? b : a;
+    }
     static_assert(FM * FN * 16 <= 1024 / NW, "accumulators must leave room for operands");
     static_assert(WK <= 2 && FM % WK == 0, "k-groups split the row tiles evenly");
 };
@@ -236,13 +261,19 @@ struct Tile {
 // v_mfma_scale_f32_32x32x64_f8f6f4 per k-block with unit block scales,
 // fp32 accumulators; kOutI32 then stores the raw fp32 accumulators; the
 // fused form writes e4m3 codes).
-template <class T, int OUT, bool FUSED, bool FP8 = false>
+// FP4: microscaled 4-bit operands (scaled_mm_fp4.hip): the same images with
+// two e2m1 codes in each byte, so a k-block is 128 elements, and one
+// v_mfma_scale_f32_32x32x64_f8f6f4 where int8 has a 32x32x32 one. Each lane
+// hands the instruction the scale bytes of its row and block; kOutI32 stores
+// the raw fp32 accumulators.
+template <class T, int OUT, bool FUSED, bool FP8 = false, bool FP4 = false>
 __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args)
 {
     constexpr bool OUT_I32 = OUT == kOutI32, OUT_F16 = OUT == kOutF16;
-    using Acc = std::conditional_t<FP8, v16f, v16i>;
+    constexpr bool FLT = FP8 || FP4;                   // fp32 accumulators
+    using Acc = std::conditional_t<FLT, v16f, v16i>;
     constexpr int IN = OUT_F16 ? kElemF16 : kElemBF16;
-    __shared__ uint4 lds[T::LDS / 16];
+    __shared__ uint4 lds[(FP4 ? T::LDS4 : T::LDS) / 16];
     W8A8_STAMP(0);
 
     MmArgs a;
@@ -261,6 +292,12 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
     a.nblocks = pinned(args.nblocks);
     a.vec_store = pinned(args.vec_store);
     a.vec16 = pinned(args.vec16);
+    if (FP4) {
+        a.sx = pinned_ptr(args.sx);
+        a.sw = pinned_ptr(args.sw);
+        a.lds = pinned(args.lds);
+        a.blocks = pinned(args.blocks);
+    }
     if (FUSED) {
         a.x = pinned_ptr(args.x);
         a.ldx = pinned(args.ldx);
@@ -320,13 +357,13 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
     // k-group's partial (raw bits) as fp32: an exact int32 sum converted
     // once, or an fp32 sum.
     auto quad_bits = [](const Acc &c, int q) __attribute__((always_inline)) {
-        if constexpr (FP8)
+        if constexpr (FLT)
             return __builtin_bit_cast(v4i, f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]});
         else
             return v4i{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
     };
     auto acc_plus = [](const Acc &c, int k, int other) __attribute__((always_inline)) {
-        if constexpr (FP8)
+        if constexpr (FLT)
             return c[k] + __int_as_float(other);
         else
             return (float)(c[k] + other);
@@ -339,6 +376,8 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
     v4i bq[T::NB][T::FN][2];                           // weight operand ring (direct path)
     v4i xf[2][T::FM][2];                               // token operands, this and next stage
     v4i bf[T::WLDS ? 2 : 1][T::FN][2];                 // weight operands from LDS, this and next
+    int sxf[FP4 ? 2 : 1][FP4 ? T::FM : 1];             // 4-bit: scale bytes of the token operands
+    int swf[FP4 ? 2 : 1][FP4 ? T::FN : 1];             // ... and of the weight operands
 
     // Weights of stage t into ring set t % NB. Addresses are clamped into
     // the operands, so a load of a stage past the end is harmless.
@@ -403,10 +442,73 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
             for (int i = 0; i < T::FM; ++i)
                 x[i][h] = st[(2 * i) * 64 + xslot[h]];
     };
+    // 4-bit: the scale bytes of slot c (k-blocks 4c .. 4c+3 of the tile's
+    // tokens, then channels) into LDS slot c % SC_SLOTS. Unit g is rows 64*g ..
+    // of them, lane l row 64*g + l; with fewer units than loads the last unit
+    // is loaded twice (the same bytes to the same place).
+    // Where each load starts, and how far it moves with c, is settled before
+    // the loop: a choice inside it would cut a step in pieces.
+    const int chunks = (a.kblocks + 3) / 4;
+    const uint8_t *sc_base[FP4 ? T::SC_LPW : 1];
+    int sc_off[FP4 ? T::SC_LPW : 1], sc_step[FP4 ? T::SC_LPW : 1], sc_dst[FP4 ? T::SC_LPW : 1];
+    if constexpr (FP4) {
+#pragma unroll
+        for (int i = 0; i < T::SC_LPW; ++i) {
+            const int g = min(i * T::NW + wave, T::SC_UNITS - 1);
+            const int tok = (g - T::BM / 64) >> 31;    // all ones for token rows
+            const int row = g * 64 + lane;             // token row, or channel BM + n, of the tile
+            const int nb = min(n0 / 16 + ((row - T::BM) >> 4), a.nblocks - 1) - n0 / 16;
+            const int off_tok = (min(m0 + row, a.M - 1) - m0) * (int)a.lds;
+            const int off_ch = nb * chunks * 256 + (lane & 15) * 16;
+            const uintptr_t base_tok = reinterpret_cast<uintptr_t>(a.sx + (int64_t)m0 * a.lds);
+            const uintptr_t base_ch = reinterpret_cast<uintptr_t>(a.sw + (int64_t)(n0 / 16) * chunks * 256);
+            sc_off[i] = (off_tok & tok) | (off_ch & ~tok);
+            sc_step[i] = pinned((16 & tok) | (256 & ~tok));
+            sc_dst[i] = pinned(T::RING + g * 1024);
+            sc_base[i] = pinned_ptr(reinterpret_cast<const uint8_t *>((base_tok & (intptr_t)tok) |
+                                                                      (base_ch & ~(intptr_t)tok)));
+        }
+    }
+    auto scale_dma = [&](int c) __attribute__((always_inline)) {
+        const int cc = min(c, chunks - 1);
+#pragma unroll
+        for (int i = 0; i < T::SC_LPW; ++i)
+            dma16(sc_base[i], sc_off[i] + cc * sc_step[i],
+                  reinterpret_cast<char *>(lds) + sc_dst[i] + (c & (T::SC_SLOTS - 1)) * T::SC_SLOT);
+    };
+    // 4-bit: this wave's scale bytes of stage t: lane l takes the four blocks
+    // of its token (channel) l%32 of each 32-row group, shifted so that bytes 0
+    // and 2 are blocks l/32 and 2 + l/32, those of the two halves of a k-block.
+    // Past the row's last block (in the last k-block, never in the steady
+    // state) the byte is 1.0: it meets zero weights, and must not be NaN.
+    auto scale_read = [&](auto full, int t, auto u_c, int (&sx)[FP4 ? T::FM : 1],
+                          int (&sw)[FP4 ? T::FN : 1]) __attribute__((always_inline)) {
+        constexpr int u = decltype(u_c)::value;        // t modulo SC_STAGES
+        const int c = t / T::SC_STAGES;
+        const int word = T::WK == 1 ? u % 4 : (u % 2) * 2 + wk;
+        const int *slot = reinterpret_cast<const int *>(reinterpret_cast<const char *>(lds) + T::RING +
+                                                        (c & (T::SC_SLOTS - 1)) * T::SC_SLOT) + word;
+        unsigned keep = ~0u;
+        if constexpr (!decltype(full)::value)
+            keep = t * T::WK + wk == kblast && (a.blocks & 3) ? (1u << (8 * (a.blocks & 3))) - 1u : ~0u;
+        auto one = [&](int row) __attribute__((always_inline)) {
+            unsigned v = (unsigned)slot[(row + (lane & 31)) * 4];
+            if constexpr (!decltype(full)::value)
+                v = (v & keep) | (0x7f7f7f7fu & ~keep);
+            return (int)(v >> (8 * (lane >> 5)));
+        };
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+            sx[i] = one(wm * (T::BM / T::WM) + i * 32);
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+            sw[j] = one(T::BM + (wn * T::FN + j) * 32);
+    };
     // MFMAs number q0 .. q1-1 of a stage, in the order (h, j, i): a wave's 2*FN*FM
     // MFMAs per stage touch every accumulator twice, FN*FM apart. The e4m3
     // twin takes both halves of a k-block in one MFMA, in the order (j, i).
-    auto mma = [&](auto q0_c, auto q1_c, const v4i (&x)[T::FM][2], const v4i (&b)[T::FN][2])
+    auto mma = [&](auto q0_c, auto q1_c, const v4i (&x)[T::FM][2], const v4i (&b)[T::FN][2],
+                   const int (&sx)[FP4 ? T::FM : 1], const int (&sw)[FP4 ? T::FN : 1])
                    __attribute__((always_inline)) {
         constexpr int q0 = decltype(q0_c)::value, q1 = decltype(q1_c)::value;
         static_for<q1 - q0>([&](auto Q) __attribute__((always_inline)) {
@@ -417,6 +519,12 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
                 const v8i xx = __builtin_shufflevector(x[i][0], x[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
                 acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bb, xx, acc[j][i], 0, 0,
                                                                             0, 127, 0, 127);
+            } else if constexpr (FP4) {
+                constexpr int h = q / (T::FN * T::FM), j = (q / T::FM) % T::FN, i = q % T::FM;
+                const v4i bb = b[j][h], xx = x[i][h];
+                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    v8i{bb[0], bb[1], bb[2], bb[3]}, v8i{xx[0], xx[1], xx[2], xx[3]}, acc[j][i], 4, 4, 2 * h, sw[j],
+                    2 * h, sx[i]);
             } else {
                 constexpr int h = q / (T::FN * T::FM), j = (q / T::FM) % T::FN, i = q % T::FM;
                 acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j][h], x[i][h], acc[j][i], 0, 0, 0);
@@ -430,9 +538,12 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
     // instructions as MFMAs; two or three on the tiles with two or three
     // times as many, measured on MI355X); the e4m3 twin has half as many
     // (twice as long) MFMAs, so its memory instructions are spread over them.
-    constexpr int DS_READS = 2 * T::FM + (T::WLDS ? 2 * T::FN : 0);
-    constexpr int MEM_OPS = DS_READS + T::LPW;
-    constexpr int PER = FP8 ? (MEM_OPS + NMMA - PRE - 1) / (NMMA - PRE) : T::MP;
+    constexpr int DS_READS = 2 * T::FM + (T::WLDS ? 2 * T::FN : 0) + (FP4 ? T::FM + T::FN : 0);
+    constexpr int MEM_OPS = DS_READS + T::LPW + (FP4 ? T::SC_LPW : 0);
+    constexpr int PER = FLT ? (MEM_OPS + NMMA - PRE - 1) / (NMMA - PRE) : T::MP;
+
+    using Full = std::integral_constant<bool, true>;
+    using Part = std::integral_constant<bool, false>;
 
     // Step s. On entry this wave's operands of stage s are in xf[s & 1], the
     // images of stages s+1 .. s+LT are landing in LDS and the weights of
@@ -452,7 +563,7 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
         // The steady state waits for exactly what it needs; the last steps
         // (where fewer loads follow) drain.
         if (FULL)
-            wait_vm_lgkm0<T::VM>();
+            wait_vm_lgkm0<FP4 ? T::vm_fp4(u) : T::VM>();
         else
             wait_vm_lgkm0<0>();
         auto &wcur = [&]() -> auto & {
@@ -461,22 +572,31 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
             else
                 return bq[u % T::NB];
         }();
+        constexpr int sc = FP4 ? u & 1 : 0;
         if (run)
-            mma(std::integral_constant<int, 0>{}, std::integral_constant<int, PRE>{}, xf[u & 1], wcur);
+            mma(std::integral_constant<int, 0>{}, std::integral_constant<int, PRE>{}, xf[u & 1], wcur, sxf[sc],
+                swf[sc]);
         __builtin_amdgcn_s_barrier();
         if (FULL || s + 1 < S) {
             read(s + 1, xf[(u + 1) & 1]);
             if constexpr (T::WLDS)
                 bread(s + 1, bf[(u + 1) & 1]);
+            if constexpr (FP4)
+                scale_read(full, s + 1, std::integral_constant<int, (u + 1) % T::SC_STAGES>{}, sxf[(u + 1) & 1],
+                           swf[(u + 1) & 1]);
         }
         if (FULL || s + 1 + T::LT < S)
             dma(s + 1 + T::LT);
+        if constexpr (FP4 && T::scale_loads(u) != 0)
+            if (FULL || (s + 1) / T::SC_STAGES + T::SC_LEAD < chunks)
+                scale_dma((s + 1) / T::SC_STAGES + T::SC_LEAD);
         if constexpr (!T::WLDS) {
             if (FULL || s + T::LW < S)
                 load_b(s + T::LW, bq[(u + T::LW) % T::NB]);
         }
         if (run)
-            mma(std::integral_constant<int, PRE>{}, std::integral_constant<int, NMMA>{}, xf[u & 1], wcur);
+            mma(std::integral_constant<int, PRE>{}, std::integral_constant<int, NMMA>{}, xf[u & 1], wcur, sxf[sc],
+                swf[sc]);
         if (FULL) {
             // PER memory instructions after each MFMA: the operand reads
             // first, then the loads.
@@ -484,7 +604,8 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
                 __builtin_amdgcn_sched_group_barrier(0x100, PER, 0); // DS read
             });
-            static_for<(T::LPW + PER - 1) / PER>([&](auto) __attribute__((always_inline)) {
+            constexpr int LOADS = T::LPW + (FP4 ? T::scale_loads(u) : 0);
+            static_for<(LOADS + PER - 1) / PER>([&](auto) __attribute__((always_inline)) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x020, PER, 0); // VMEM read
             });
@@ -493,9 +614,6 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
         // step, so the load counter pattern repeats exactly.
         __builtin_amdgcn_sched_barrier(0);
     };
-    using Full = std::integral_constant<bool, true>;
-    using Part = std::integral_constant<bool, false>;
-
     if (FUSED) {
         // Fused quant: this workgroup quantizes rows [r0, r1) of x and
         // publishes them (rows_per_wg divides BM, so the rows belong to one
@@ -534,13 +652,13 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
             const int p = u * T::THREADS + (int)threadIdx.x;
             float v = 0.0f;
             if (p < T::BN)
-                v = a.ws[min(n0 + p, a.N - 1)];
+                v = FP4 ? 0.0f : a.ws[min(n0 + p, a.N - 1)];
             else if (p < 2 * T::BN) {
                 if (a.bias) {
                     const unsigned b = a.bias[min(n0 + p - T::BN, a.N - 1)];
                     v = OUT_F16 ? quant_rule::f16_to_float(b) : __uint_as_float(b << 16);
                 }
-            } else if (p < T::SIDE)
+            } else if (!FP4 && p < T::SIDE)
                 v = a.xs[min(m0 + p - 2 * T::BN, a.M - 1)];
             side_v[u] = v;
         }
@@ -558,18 +676,24 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
             constexpr int t = decltype(U)::value;
             load_b(t, bq[t % T::NB]);
         });
+    if constexpr (FP4)
+        scale_dma(0);
     dma(0);
     static_for<T::LT>([&](auto U) __attribute__((always_inline)) {
         constexpr int v = decltype(U)::value - T::LT;  // virtual step -LT .. -1
         dma(v + 1 + T::LT);
+        if constexpr (FP4 && T::scale_loads(v) != 0)
+            scale_dma((v + 1) / T::SC_STAGES + T::SC_LEAD);
         if constexpr (!T::WLDS)
             load_b(v + T::LW, bq[(v + T::LW) % T::NB]);
     });
-    wait_vm_lgkm0<T::LT * T::LPW>();
+    wait_vm_lgkm0<T::LT * T::LPW + (FP4 ? T::scale_loads(-1) + T::scale_loads(-2) + T::scale_loads(-3) : 0)>();
     __builtin_amdgcn_s_barrier();
     read(0, xf[0]);
     if constexpr (T::WLDS)
         bread(0, bf[0]);
+    if constexpr (FP4)
+        scale_read(Part{}, 0, std::integral_constant<int, 0>{}, sxf[0], swf[0]);
 
     W8A8_STAMP(4);
 
@@ -601,13 +725,15 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
     auto epilogue = [&](auto wk_c) __attribute__((always_inline)) {
         constexpr int WKI = decltype(wk_c)::value;
         constexpr int i0 = WKI * FMH;
-        float *side = reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + T::MAIN);
+        // (4-bit: the bias alone, in its place BN words in)
+        float *side = FP4 ? reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + T::SIDE4) - T::BN
+                          : reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + T::MAIN);
         const bool has_bias = !OUT_I32 && a.bias != nullptr;
         if (!OUT_I32) {
 #pragma unroll
             for (int u = 0; u < T::SIDE_PER_THREAD; ++u) {
                 const int p = u * T::THREADS + (int)threadIdx.x;
-                if (p < T::SIDE)
+                if (FP4 ? p >= T::BN && p < 2 * T::BN : p < T::SIDE)
                     side[p] = side_v[u];
             }
         }
@@ -665,7 +791,7 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
                             continue;
                         const Acc &c = acc[j][i0 + i];
                         v4i v;
-                        if constexpr (FP8)
+                        if constexpr (FLT)
                             v = __builtin_bit_cast(
                                 v4i, __builtin_bit_cast(f32x4, quad_bits(c, q)) + __builtin_bit_cast(f32x4, pv[j][q]));
                         else
@@ -694,7 +820,8 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
         for (int j = 0; j < T::FN; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                w4[j][q] = *reinterpret_cast<const f32x4 *>(side + (wn * T::FN + j) * 32 + q * 8 + (lane >> 5) * 4);
+                w4[j][q] = FP4 ? f32x4{} : *reinterpret_cast<const f32x4 *>(side + (wn * T::FN + j) * 32 + q * 8 +
+                                                                            (lane >> 5) * 4);
         char *tile_lds = reinterpret_cast<char *>(lds) + T::TILE_OFF;
         auto scale = [&](auto with_bias) __attribute__((always_inline)) {
             constexpr bool B = decltype(with_bias)::value;
@@ -703,7 +830,7 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
                 v4i pv[T::FN][4];
                 partials(i, pv);
                 const int ml = wm * (T::BM / T::WM) + (i0 + i) * 32 + (lane & 31);
-                const float xr = side[2 * T::BN + ml];
+                const float xr = FP4 ? 1.0f : side[2 * T::BN + ml];
 #pragma unroll
                 for (int j = 0; j < T::FN; ++j)
 #pragma unroll
@@ -714,8 +841,11 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
                         float t[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            t[r] = acc_plus(c, 4 * q + r, pv[j][q][r]) * xr;
-                            t[r] = t[r] * w4[j][q][r];
+                            t[r] = acc_plus(c, 4 * q + r, pv[j][q][r]);
+                            if (!FP4) {
+                                t[r] = t[r] * xr;
+                                t[r] = t[r] * w4[j][q][r];
+                            }
                             if (B)
                                 t[r] = t[r] + b4[r];
                         }
