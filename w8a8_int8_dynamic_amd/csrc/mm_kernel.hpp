@@ -477,8 +477,7 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
                   reinterpret_cast<char *>(lds) + sc_dst[i] + (c & (T::SC_SLOTS - 1)) * T::SC_SLOT);
     };
     // 4-bit: this wave's scale bytes of stage t: lane l takes the four blocks
-    // of its token (channel) l%32 of each 32-row group, shifted so that bytes 0
-    // and 2 are blocks l/32 and 2 + l/32, those of the two halves of a k-block.
+    // of its token (channel) l%32 of each 32-row group as one word.
     // Past the row's last block (in the last k-block, never in the steady
     // state) the byte is 1.0: it meets zero weights, and must not be NaN.
     auto scale_read = [&](auto full, int t, auto u_c, int (&sx)[FP4 ? T::FM : 1],
@@ -495,7 +494,7 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
             unsigned v = (unsigned)slot[(row + (lane & 31)) * 4];
             if constexpr (!decltype(full)::value)
                 v = (v & keep) | (0x7f7f7f7fu & ~keep);
-            return (int)(v >> (8 * (lane >> 5)));
+            return (int)v;
         };
 #pragma unroll
         for (int i = 0; i < T::FM; ++i)
@@ -503,6 +502,19 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
 #pragma unroll
         for (int j = 0; j < T::FN; ++j)
             sw[j] = one(T::BM + (wn * T::FN + j) * 32);
+    };
+    // Those words shifted so that bytes 0 and 2 are blocks l/32 and 2 + l/32,
+    // the ones of this lane in the two halves of a k-block. Done as a step
+    // begins, not where the words are read: the read's wait would stand between
+    // the MFMAs there.
+    const int sc_shift = 8 * (lane >> 5);
+    auto scale_shift = [&](int (&sx)[FP4 ? T::FM : 1], int (&sw)[FP4 ? T::FN : 1]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+            sw[j] = (int)((unsigned)sw[j] >> sc_shift);
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+            sx[i] = (int)((unsigned)sx[i] >> sc_shift);
     };
     // MFMAs number q0 .. q1-1 of a stage, in the order (h, j, i): a wave's 2*FN*FM
     // MFMAs per stage touch every accumulator twice, FN*FM apart. The e4m3
@@ -540,7 +552,7 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
     // (twice as long) MFMAs, so its memory instructions are spread over them.
     constexpr int DS_READS = 2 * T::FM + (T::WLDS ? 2 * T::FN : 0) + (FP4 ? T::FM + T::FN : 0);
     constexpr int MEM_OPS = DS_READS + T::LPW + (FP4 ? T::SC_LPW : 0);
-    constexpr int PER = FLT ? (MEM_OPS + NMMA - PRE - 1) / (NMMA - PRE) : T::MP;
+    constexpr int PER = FP8 ? (MEM_OPS + NMMA - PRE - 1) / (NMMA - PRE) : T::MP;
 
     using Full = std::integral_constant<bool, true>;
     using Part = std::integral_constant<bool, false>;
@@ -573,6 +585,8 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
                 return bq[u % T::NB];
         }();
         constexpr int sc = FP4 ? u & 1 : 0;
+        if constexpr (FP4)
+            scale_shift(sxf[sc], swf[sc]);
         if (run)
             mma(std::integral_constant<int, 0>{}, std::integral_constant<int, PRE>{}, xf[u & 1], wcur, sxf[sc],
                 swf[sc]);
