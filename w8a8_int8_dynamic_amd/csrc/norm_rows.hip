@@ -8,15 +8,381 @@
 // the values; each output is rounded once, and the codes come from the fp32
 // values by the rule of int8_quant_per_token / fp8_quant_per_token.
 //
-// The simplest form: one workgroup per row, which reads the row again (from
-// L2) for each of its passes. It writes nothing before its last pass, so r
-// may be x itself.
+// What bounds it: the bytes of x, y, r and out; the arithmetic (some 20
+// operations per element) and the vectors, which every row reads from L2,
+// come next. norm_rows_kernel reads each row once and holds it in registers
+// (8 * CH elements per thread) while its sums meet; TPR threads share a row.
+// Rows too long for that take norm_rows_looped_kernel, one workgroup a row,
+// which reads the row again (from L2) for each of its passes. Neither writes
+// an element before it has read it for the last time, so r may be x itself.
+#include <algorithm>
+
 #include "norm_rows.hpp"
 
 namespace w8a8 {
 namespace {
 
 using namespace norm_rule;
+
+// ---- rows held in registers ----
+
+// Sum of v over the WAVES wavefronts of a row, the same in each of them.
+// `part` holds two rounds of WAVES words each, used in turn: a wavefront can
+// reach the next round's write only past this round's barrier, and the one
+// after that only when every wavefront has read this round.
+template <int WAVES>
+__device__ __forceinline__ float row_sum(float v, float *part, int &turn)
+{
+    v = wave_sum(v);
+    if constexpr (WAVES == 1)
+        return v;
+    float *p = part + turn * WAVES;
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0)
+        p[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float s[WAVES];
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i)
+        s[i] = p[i];
+#pragma unroll
+    for (int w = WAVES / 2; w > 0; w /= 2)
+#pragma unroll
+        for (int i = 0; i < w; ++i)
+            s[i] += s[i + w];
+    return s[0];
+}
+
+// The same for the largest of bit patterns.
+template <int WAVES>
+__device__ __forceinline__ u32 row_max(u32 m, float *part, int &turn)
+{
+    m = quant_rule::wave_max(m);
+    if constexpr (WAVES == 1)
+        return m;
+    u32 *p = reinterpret_cast<u32 *>(part) + turn * WAVES;
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0)
+        p[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = p[0];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i)
+        m = max(m, p[i]);
+    return m;
+}
+
+// A thread's piece of a row: 8 elements from `at` on, of which those from
+// `skip` on are its own. Pieces begin at multiples of 8 and the row's last one
+// ends with the row, so a ragged row's last piece reads over the piece before
+// it; 8 or more: nothing is this thread's, and it reads what another does.
+struct Piece {
+    int at, skip;
+    int own;                                           // bit j: element j is this thread's
+};
+
+// v where it is this thread's, else 0. (A bit of a register per element: eight
+// comparisons a chunk would be held in more scalar registers than there are.)
+template <bool WHOLE>
+__device__ __forceinline__ float own_or_zero(const Piece &p, int j, float v)
+{
+    return WHOLE ? v : __int_as_float(__float_as_int(v) & __builtin_amdgcn_sbfe(p.own, j, 1));
+}
+
+// One 16-byte word of 16-bit elements, or two of fp32, still in their bits.
+template <int E>
+struct Raw {
+    uint4 w[E == kF32 ? 2 : 1];
+};
+__device__ __forceinline__ uint4 load16(const void *p)
+{
+    const v4u_any a = *static_cast<const v4u_any *>(p);
+    return make_uint4(a[0], a[1], a[2], a[3]);
+}
+template <int E>
+__device__ __forceinline__ Raw<E> raw_load(const char *row, int at)
+{
+    Raw<E> r;
+    r.w[0] = load16(row + (int64_t)at * (E == kF32 ? 4 : 2));
+    if constexpr (E == kF32)
+        r.w[1] = load16(row + (int64_t)at * 4 + 16);
+    return r;
+}
+template <int E>
+__device__ __forceinline__ void raw_values(const uint4 &lo, const uint4 &hi, float (&v)[8])
+{
+    const u32 a[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = E == kF32 ? __uint_as_float(a[j])
+             : E == kF16 ? quant_rule::f16_to_float(j & 1 ? a[j / 2] >> 16 : a[j / 2])
+                         : __uint_as_float(j & 1 ? a[j / 2] & 0xffff0000u : a[j / 2] << 16);
+}
+template <int E>
+__device__ __forceinline__ void raw_values(const Raw<E> &r, float (&v)[8])
+{
+    raw_values<E>(r.w[0], r.w[E == kF32 ? 1 : 0], v);
+}
+
+// One chunk of a vector of a norm or gate: its raw words, read without
+// waiting, whatever its kind (uniform over the launch; a 16-bit vector's one
+// word is read twice, and where there is no vector the row's own words are,
+// unused). vec_values gives `none` where there is no vector.
+struct RawVec {
+    v4u_any lo, hi;
+};
+__device__ __forceinline__ RawVec vec_load(const void *p, int kind, int64_t offset, int at, const char *otherwise)
+{
+    const int size = kind == kF32 ? 4 : 2;
+    const char *s = p ? static_cast<const char *>(p) + (offset + at) * size : otherwise;
+    RawVec r;
+    r.lo = *reinterpret_cast<const v4u_any *>(s);
+    r.hi = *reinterpret_cast<const v4u_any *>(s + (p && kind == kF32 ? 16 : 0));
+    return r;
+}
+__device__ __forceinline__ void vec_values(const void *p, int kind, const RawVec &r, float none, float (&v)[8])
+{
+    const uint4 lo = make_uint4(r.lo[0], r.lo[1], r.lo[2], r.lo[3]);
+    const uint4 hi = make_uint4(r.hi[0], r.hi[1], r.hi[2], r.hi[3]);
+    if (p == nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = none;
+    } else if (kind == kF32) {
+        raw_values<kF32>(lo, hi, v);
+    } else if (kind == kF16) {
+        raw_values<kF16>(lo, hi, v);
+    } else {
+        raw_values<kBF16>(lo, hi, v);
+    }
+}
+
+// v = n(v) for the row's values held as v[CH][8]; elements that are not this
+// thread's are left out of the sums.
+template <int CH, int WAVES, bool WHOLE>
+__device__ __forceinline__ void normalize(float (&v)[CH][8], const Piece (&p)[CH], float k_inv, int kind, float eps,
+                                          float *part, int &turn)
+{
+    if (kind == kNormLayer) {
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s += own_or_zero<WHOLE>(p[c], j, v[c][j]);
+        const float mean = row_sum<WAVES>(s, part, turn) * k_inv;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[c][j] -= mean;
+    }
+    float q = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float d = own_or_zero<WHOLE>(p[c], j, v[c][j]);
+            q = fmaf(d, d, q);
+        }
+    const float inv = 1.0f / sqrtf(row_sum<WAVES>(q, part, turn) * k_inv + eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[c][j] *= inv;
+}
+
+// A piece of a row to memory: whole, or its own elements one by one.
+template <int E, bool WHOLE>
+__device__ __forceinline__ void piece_store(char *row, const Piece &p, const float (&v)[8])
+{
+    if (WHOLE || p.skip == 0) {
+        store8<E>(row, p.at, p.at + 8, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 1; j < 8; ++j)
+        if (j >= p.skip) {
+            if constexpr (E == kF32)
+                reinterpret_cast<float *>(row)[p.at + j] = v[j];
+            else
+                reinterpret_cast<uint16_t *>(row)[p.at + j] = (uint16_t)pack2<E>(v[j], v[j]);
+        }
+}
+
+// TPR threads (whole wavefronts) per row, R rows at a time per workgroup, which
+// takes a run of `per_block` rows. The vectors are read once for all of a
+// run's rows in one group and held as the two factors of each norm:
+//   r = residual_scale * x + n(y) * g1 + g0,  g1 = branch_scale * gate * weight
+//   h = n(r) * h1 + h0,  h1 = weight * (1 + scale), h0 = bias * (1 + scale) + shift
+// and the next row's elements are on their way while a row's sums meet.
+// WHOLE: K is exactly the TPR * CH pieces of 8.
+template <int XE, int AE, bool RES, int CH, int TPR, int R, bool WHOLE>
+__global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a, int64_t per_block)
+{
+    constexpr int WAVES = TPR / 64;
+    static_assert(R == 1 || WAVES == 1, "rows that share a workgroup do not share barriers");
+    constexpr int XB = XE == kF32 ? 4 : 2;
+    __shared__ float part[2 * WAVES];
+    const int t = (int)threadIdx.x % TPR;
+    const int K = (int)a.K;
+    const float k_inv = 1.0f / (float)K;
+    Piece p[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int begin = (c * TPR + t) * 8;
+        p[c].at = min(begin, K - 8);
+        p[c].skip = begin - p[c].at;
+        p[c].own = p[c].skip < 8 ? 0xff & (0xff << p[c].skip) : 0;
+    }
+    const int64_t first = (int64_t)blockIdx.x * per_block + (int)threadIdx.x / TPR;
+    const int64_t end = min(a.rows, ((int64_t)blockIdx.x + 1) * per_block);
+    if (first >= end)
+        return;                                        // whole wavefronts that share no barrier (R > 1), or none
+    const bool next = !RES || a.next.kind != kNormNone;
+
+    Raw<XE> xr[CH];
+    Raw<AE> yr[CH];
+    auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+        const char *x = static_cast<const char *>(a.x) + row * a.ldx * XB;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            xr[c] = raw_load<XE>(x, p[c].at);
+        if constexpr (RES) {
+            const char *y = static_cast<const char *>(a.y) + row * a.ldy * 2;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                yr[c] = raw_load<AE>(y, p[c].at);
+        }
+    };
+    fetch(first);
+
+    float g1[CH][8], g0[CH][8], h1[CH][8], h0[CH][8];
+    int turn = 0;
+    int64_t row = first;
+    while (row < end) {
+        // The rows up to `stop` share one vector of each kind.
+        int64_t stop = end;
+        int64_t gg = 0, ng = 0;
+        if (RES && a.gate) {
+            gg = row / a.gate_rows;
+            stop = min(stop, (gg + 1) * a.gate_rows);
+        }
+        if (next && (a.next.scale || a.next.shift)) {
+            ng = row / a.next.group_rows;
+            stop = min(stop, (ng + 1) * a.next.group_rows);
+        }
+        const void *pw = RES && a.post.kind != kNormNone ? a.post.weight : nullptr;
+        const void *pb = RES && a.post.kind != kNormNone ? a.post.bias : nullptr;
+        static_for<CH>([&](auto C) __attribute__((always_inline)) {
+            constexpr int c = decltype(C)::value;
+            const int at = p[c].at;
+            const char *x = static_cast<const char *>(a.x) + row * a.ldx * XB + (int64_t)at * XB;
+            RawVec vg, vpw, vpb, vw, vb, vs, vt;
+            if constexpr (RES) {
+                vg = vec_load(a.gate, a.gate_kind, gg * a.ld_gate, at, x);
+                vpw = vec_load(pw, a.post.vec_kind, 0, at, x);
+                vpb = vec_load(pb, a.post.vec_kind, 0, at, x);
+            }
+            if (next) {
+                vw = vec_load(a.next.weight, a.next.vec_kind, 0, at, x);
+                vb = vec_load(a.next.bias, a.next.vec_kind, 0, at, x);
+                vs = vec_load(a.next.scale, a.next.mod_kind, ng * a.next.ld_scale, at, x);
+                vt = vec_load(a.next.shift, a.next.mod_kind, ng * a.next.ld_shift, at, x);
+            }
+            if constexpr (RES) {
+                float w[8], b[8];
+                vec_values(a.gate, a.gate_kind, vg, 1.0f, g1[c]);
+                vec_values(pw, a.post.vec_kind, vpw, 1.0f, w);
+                vec_values(pb, a.post.vec_kind, vpb, 0.0f, b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float g = a.branch_scale * g1[c][j];
+                    g1[c][j] = g * w[j];
+                    g0[c][j] = g * b[j];
+                }
+            }
+            if (next) {
+                float sc[8], sh[8];
+                vec_values(a.next.weight, a.next.vec_kind, vw, 1.0f, h1[c]);
+                vec_values(a.next.bias, a.next.vec_kind, vb, 0.0f, h0[c]);
+                vec_values(a.next.scale, a.next.mod_kind, vs, 0.0f, sc);
+                vec_values(a.next.shift, a.next.mod_kind, vt, 0.0f, sh);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    h1[c][j] = h1[c][j] * (1.0f + sc[j]);
+                    h0[c][j] = fmaf(h0[c][j], 1.0f + sc[j], sh[j]);
+                }
+            }
+        });
+        for (; row < stop; row += R) {
+            float v[CH][8], b[RES ? CH : 1][8];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                raw_values<XE>(xr[c], v[c]);
+                if constexpr (RES)
+                    raw_values<AE>(yr[c], b[c]);
+            }
+            if (row + R < end)
+                fetch(row + R);
+            if constexpr (RES) {
+                if (a.post.kind != kNormNone)
+                    normalize<CH, WAVES, WHOLE>(b, p, k_inv, a.post.kind, a.post.eps, part, turn);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[c][j] = fmaf(b[c][j], g1[c][j], fmaf(a.residual_scale, v[c][j], g0[c][j]));
+                    if (WHOLE || p[c].skip < 8)
+                        piece_store<XE, WHOLE>(static_cast<char *>(a.r) + row * a.ldr * XB, p[c], v[c]);
+                }
+                if (!next)
+                    continue;
+            }
+            normalize<CH, WAVES, WHOLE>(v, p, k_inv, a.next.kind, a.next.eps, part, turn);
+            u32 m = 0;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[c][j] = fmaf(v[c][j], h1[c][j], h0[c][j]);
+                    m = max(m, __float_as_uint(own_or_zero<WHOLE>(p[c], j, v[c][j])) & 0x7fffffffu);
+                }
+                if (a.out_kind == kNormOut16 && (WHOLE || p[c].skip < 8))
+                    piece_store<AE, WHOLE>(static_cast<char *>(a.out) + row * a.ldo * 2, p[c], v[c]);
+            }
+            if (a.out_kind == kNormOut16)
+                continue;
+            float sc, inv;
+            quant_rule::scale_of(row_max<WAVES>(m, part, turn), kF32, sc, inv, a.out_kind == kNormOutFp8);
+            if (t == 0)
+                a.out_scale[row] = sc;
+            uint8_t *q = static_cast<uint8_t *>(a.out) + row * a.ldo;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                u32 lo, hi;
+                if (a.out_kind == kNormOutFp8) {
+                    lo = quant_rule::codes4_fp8(v[c][0], v[c][1], v[c][2], v[c][3], inv);
+                    hi = quant_rule::codes4_fp8(v[c][4], v[c][5], v[c][6], v[c][7], inv);
+                } else {
+                    lo = quant_rule::codes4_i8(v[c][0], v[c][1], v[c][2], v[c][3], inv);
+                    hi = quant_rule::codes4_i8(v[c][4], v[c][5], v[c][6], v[c][7], inv);
+                }
+                if (WHOLE || p[c].skip == 0) {
+                    *reinterpret_cast<uint2 *>(q + p[c].at) = make_uint2(lo, hi);
+                } else {
+#pragma unroll
+                    for (int j = 1; j < 8; ++j)
+                        if (j >= p[c].skip)
+                            q[p[c].at + j] = (uint8_t)((j < 4 ? lo >> (8 * j) : hi >> (8 * (j - 4))) & 0xffu);
+                }
+            }
+        }
+    }
+}
+
+// ---- rows of any length, read again for each pass ----
 
 __device__ __forceinline__ float block_sum(float v, float *part)
 {
@@ -184,23 +550,66 @@ __global__ __launch_bounds__(256) void norm_rows_looped_kernel(const NormRowsArg
     }
 }
 
-template <int XE, int AE>
-auto looped(bool res)
+typedef void (*RowsFn)(const NormRowsArgs, int64_t);
+struct Shape {
+    RowsFn fn;
+    int threads, rows;                                 // per workgroup; rows at a time
+};
+
+// The row shapes of norm_rows_kernel: threads per row and chunks per thread,
+// up to 16384 elements (beyond, a row and its vectors no longer fit the
+// registers of 1024 threads).
+constexpr int64_t kHeldElements = 16384;
+template <int XE, int AE, bool RES, int CH, int TPR, int R>
+Shape shape(int64_t K)
 {
-    return res ? norm_rows_looped_kernel<XE, AE, true> : norm_rows_looped_kernel<XE, AE, false>;
+    return {K == CH * TPR * 8 ? norm_rows_kernel<XE, AE, RES, CH, TPR, R, true>
+                              : norm_rows_kernel<XE, AE, RES, CH, TPR, R, false>, TPR * R, R};
+}
+template <int XE, int AE, bool RES>
+Shape pick(int64_t K)
+{
+    const int64_t chunks = ceil_div(K, 8);
+    if (chunks <= 64)
+        return shape<XE, AE, RES, 1, 64, 4>(K);
+    if (chunks <= 128)
+        return shape<XE, AE, RES, 1, 128, 1>(K);
+    if (chunks <= 256)
+        return shape<XE, AE, RES, 1, 256, 1>(K);
+    if (chunks <= 512)
+        return shape<XE, AE, RES, 2, 256, 1>(K);
+    if (chunks <= 1024)
+        return shape<XE, AE, RES, 2, 512, 1>(K);
+    if (chunks <= 1536)
+        return shape<XE, AE, RES, 3, 512, 1>(K);
+    return shape<XE, AE, RES, 2, 1024, 1>(K);
+}
+
+template <int XE, int AE>
+hipError_t launch(const NormRowsArgs &a, hipStream_t stream)
+{
+    const bool res = a.y != nullptr;
+    if (a.K < 8 || a.K > kHeldElements) {
+        const int64_t blocks = std::min(a.rows, kMaxBlocksPerLaunch);
+        auto fn = res ? norm_rows_looped_kernel<XE, AE, true> : norm_rows_looped_kernel<XE, AE, false>;
+        hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+        return hipGetLastError();
+    }
+    const Shape s = res ? pick<XE, AE, true>(a.K) : pick<XE, AE, false>(a.K);
+    // A run of rows per workgroup: enough workgroups to fill the device first.
+    const int64_t want = 256 * 1024 / s.threads;
+    const int64_t per_block = round_up(ceil_div(a.rows, want), s.rows);
+    hipLaunchKernelGGL(s.fn, dim3((unsigned)ceil_div(a.rows, per_block)), dim3(s.threads), 0, stream, a, per_block);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_norm_rows(const NormRowsArgs &a, hipStream_t stream)
 {
-    const bool res = a.y != nullptr;
-    auto fn = a.x_kind == kElemBF16 ? looped<kBF16, kBF16>(res)
-            : a.x_kind == kElemF16  ? looped<kF16, kF16>(res)
-            : a.act_kind == kElemF16 ? looped<kF32, kF16>(res) : looped<kF32, kBF16>(res);
-    const int64_t blocks = a.rows < kMaxBlocksPerLaunch ? a.rows : kMaxBlocksPerLaunch;
-    hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(256), 0, stream, a);
-    return hipGetLastError();
+    return a.x_kind == kElemBF16 ? launch<kBF16, kBF16>(a, stream)
+         : a.x_kind == kElemF16  ? launch<kF16, kF16>(a, stream)
+         : a.act_kind == kElemF16 ? launch<kF32, kF16>(a, stream) : launch<kF32, kBF16>(a, stream);
 }
 
 }  // namespace w8a8

@@ -2,6 +2,8 @@
 // stores with ragged tails, row reductions and the output forms.
 #pragma once
 
+#include <utility>
+
 #include "internal.hpp"
 #include "quant_rule.hpp"
 
@@ -19,6 +21,19 @@ typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// f(std::integral_constant<int, c>) for c = 0 .. N-1: an index that is a
+// constant from the start keeps register arrays in registers.
+template <class F, int... C>
+__device__ __forceinline__ void static_for_impl(F &&f, std::integer_sequence<int, C...>)
+{
+    (f(std::integral_constant<int, C>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F &&f)
+{
+    static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
 
 template <int E>
 __device__ __forceinline__ float widen(u32 bits)
