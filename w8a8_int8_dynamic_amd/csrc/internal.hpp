@@ -62,7 +62,7 @@ hipError_t launch_prepack_fp4(const void *w, int kind, const uint8_t *ws, int64_
 hipError_t launch_unpack_fp4(const void *packed, const void *spacked, int64_t N, int64_t K, uint8_t *wq, int64_t ldw,
                              uint8_t *ws, int64_t lds, hipStream_t stream);
 
-// ---- norms before a block, gate, residual and norm after it (norm_rows.hip) ----
+// ---- norms before a block, gate, residual and norm after it (norm_kernel.hpp) ----
 // One pass over rows of K elements:
 //   v = x, or with y: v = residual_scale * x + branch_scale * gate * post(y),
 //       stored to r in x's type;
@@ -92,7 +92,16 @@ struct NormRowsArgs {
     float residual_scale, branch_scale;
     NormVectors post, next;
 };
-hipError_t launch_norm_rows(const NormRowsArgs &a, hipStream_t stream);
+hipError_t launch_norm_rows_bf16(const NormRowsArgs &a, hipStream_t stream);
+hipError_t launch_norm_rows_f16(const NormRowsArgs &a, hipStream_t stream);
+hipError_t launch_norm_rows_f32_bf16(const NormRowsArgs &a, hipStream_t stream);
+hipError_t launch_norm_rows_f32_f16(const NormRowsArgs &a, hipStream_t stream);
+inline hipError_t launch_norm_rows(const NormRowsArgs &a, hipStream_t stream)
+{
+    return a.x_kind == kElemBF16 ? launch_norm_rows_bf16(a, stream)
+         : a.x_kind == kElemF16  ? launch_norm_rows_f16(a, stream)
+         : a.act_kind == kElemF16 ? launch_norm_rows_f32_f16(a, stream) : launch_norm_rows_f32_bf16(a, stream);
+}
 
 // ---- scaled matmul (scaled_mm.hip) ----
 struct MmArgs {

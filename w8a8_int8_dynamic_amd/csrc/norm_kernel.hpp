@@ -15,9 +15,12 @@
 // Rows too long for that take norm_rows_looped_kernel, one workgroup a row,
 // which reads the row again (from L2) for each of its passes. Neither writes
 // an element before it has read it for the last time, so r may be x itself.
+#pragma once
+
 #include <algorithm>
 
 #include "norm_rows.hpp"
+
 
 namespace w8a8 {
 namespace {
@@ -94,9 +97,11 @@ template <int E>
 struct Raw {
     uint4 w[E == kF32 ? 2 : 1];
 };
+// Rows are read once: nontemporal loads keep them out of the caches' way
+// (measured on MI355X: M8192 K8192 bf16, gated residual 82 -> 66 us).
 __device__ __forceinline__ uint4 load16(const void *p)
 {
-    const v4u_any a = *static_cast<const v4u_any *>(p);
+    const v4u_any a = __builtin_nontemporal_load(static_cast<const v4u_any *>(p));
     return make_uint4(a[0], a[1], a[2], a[3]);
 }
 template <int E>
@@ -185,7 +190,7 @@ __device__ __forceinline__ void normalize(float (&v)[CH][8], const Piece (&p)[CH
             const float d = own_or_zero<WHOLE>(p[c], j, v[c][j]);
             q = fmaf(d, d, q);
         }
-    const float inv = 1.0f / sqrtf(row_sum<WAVES>(q, part, turn) * k_inv + eps);
+    const float inv = __builtin_amdgcn_rsqf(row_sum<WAVES>(q, part, turn) * k_inv + eps);   // within 1 ulp
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -217,8 +222,12 @@ __device__ __forceinline__ void piece_store(char *row, const Piece &p, const flo
 //   r = residual_scale * x + n(y) * g1 + g0,  g1 = branch_scale * gate * weight
 //   h = n(r) * h1 + h0,  h1 = weight * (1 + scale), h0 = bias * (1 + scale) + shift
 // and the next row's elements are on their way while a row's sums meet.
-// WHOLE: K is exactly the TPR * CH pieces of 8.
-template <int XE, int AE, bool RES, int CH, int TPR, int R, bool WHOLE>
+// WHOLE: K is exactly the TPR * CH pieces of 8. OUT: what becomes of h (kOut*),
+// a template argument so that the loop's loads and stores are the same in every
+// pass: the wait for the next row's elements then leaves this row's stores in
+// flight.
+constexpr int kOutNone = 0, kOutFloat = 1, kOutCodes = 2;
+template <int XE, int AE, bool RES, int OUT, int CH, int TPR, int R, bool WHOLE>
 __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a, int64_t per_block)
 {
     constexpr int WAVES = TPR / 64;
@@ -236,14 +245,15 @@ __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a
         p[c].skip = begin - p[c].at;
         p[c].own = p[c].skip < 8 ? 0xff & (0xff << p[c].skip) : 0;
     }
-    const int64_t first = (int64_t)blockIdx.x * per_block + (int)threadIdx.x / TPR;
+    const int64_t first = (int64_t)blockIdx.x * per_block +
+                          (R > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR) : 0);
     const int64_t end = min(a.rows, ((int64_t)blockIdx.x + 1) * per_block);
     if (first >= end)
         return;                                        // whole wavefronts that share no barrier (R > 1), or none
-    const bool next = !RES || a.next.kind != kNormNone;
+    constexpr bool next = OUT != kOutNone;
 
-    Raw<XE> xr[CH];
-    Raw<AE> yr[CH];
+    Raw<XE> xr[CH];                                    // the next row
+    Raw<AE> yr[RES ? CH : 1];
     auto fetch = [&](int64_t row) __attribute__((always_inline)) {
         const char *x = static_cast<const char *>(a.x) + row * a.ldx * XB;
 #pragma unroll
@@ -260,17 +270,17 @@ __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a
 
     float g1[CH][8], g0[CH][8], h1[CH][8], h0[CH][8];
     int turn = 0;
-    int64_t row = first;
-    while (row < end) {
-        // The rows up to `stop` share one vector of each kind.
-        int64_t stop = end;
+    int64_t row = first, stop = first;                 // the rows before `stop` share the vectors held
+    const int64_t last = first + (end - 1 - first) / R * R;
+    auto vectors = [&]() __attribute__((always_inline)) {
+        stop = end;
         int64_t gg = 0, ng = 0;
         if (RES && a.gate) {
-            gg = row / a.gate_rows;
+            gg = (uint32_t)row / (uint32_t)a.gate_rows;
             stop = min(stop, (gg + 1) * a.gate_rows);
         }
         if (next && (a.next.scale || a.next.shift)) {
-            ng = row / a.next.group_rows;
+            ng = (uint32_t)row / (uint32_t)a.next.group_rows;
             stop = min(stop, (ng + 1) * a.next.group_rows);
         }
         const void *pw = RES && a.post.kind != kNormNone ? a.post.weight : nullptr;
@@ -316,69 +326,79 @@ __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a
                 }
             }
         });
-        for (; row < stop; row += R) {
-            float v[CH][8], b[RES ? CH : 1][8];
+    };
+    auto one_row = [&]() __attribute__((always_inline)) {
+        float v[CH][8], b[RES ? CH : 1][8];
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                raw_values<XE>(xr[c], v[c]);
-                if constexpr (RES)
-                    raw_values<AE>(yr[c], b[c]);
-            }
-            if (row + R < end)
-                fetch(row + R);
-            if constexpr (RES) {
-                if (a.post.kind != kNormNone)
-                    normalize<CH, WAVES, WHOLE>(b, p, k_inv, a.post.kind, a.post.eps, part, turn);
-#pragma unroll
-                for (int c = 0; c < CH; ++c) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[c][j] = fmaf(b[c][j], g1[c][j], fmaf(a.residual_scale, v[c][j], g0[c][j]));
-                    if (WHOLE || p[c].skip < 8)
-                        piece_store<XE, WHOLE>(static_cast<char *>(a.r) + row * a.ldr * XB, p[c], v[c]);
-                }
-                if (!next)
-                    continue;
-            }
-            normalize<CH, WAVES, WHOLE>(v, p, k_inv, a.next.kind, a.next.eps, part, turn);
-            u32 m = 0;
+        for (int c = 0; c < CH; ++c) {
+            raw_values<XE>(xr[c], v[c]);
+            if constexpr (RES)
+                raw_values<AE>(yr[c], b[c]);
+        }
+        // The next row into the registers that this one's words leave (the last
+        // row once more at the end of the run: a load that nothing waits for).
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(min(row + R, last));
+        if constexpr (RES) {
+            if (a.post.kind != kNormNone)
+                normalize<CH, WAVES, WHOLE>(b, p, k_inv, a.post.kind, a.post.eps, part, turn);
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v[c][j] = fmaf(v[c][j], h1[c][j], h0[c][j]);
+                for (int j = 0; j < 8; ++j)
+                    v[c][j] = fmaf(b[c][j], g1[c][j], fmaf(a.residual_scale, v[c][j], g0[c][j]));
+                if (WHOLE || p[c].skip < 8)
+                    piece_store<XE, WHOLE>(static_cast<char *>(a.r) + row * a.ldr * XB, p[c], v[c]);
+            }
+            if constexpr (!next)
+                return;
+        }
+        normalize<CH, WAVES, WHOLE>(v, p, k_inv, a.next.kind, a.next.eps, part, turn);
+        u32 m = 0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[c][j] = fmaf(v[c][j], h1[c][j], h0[c][j]);
+                if constexpr (OUT == kOutCodes)
                     m = max(m, __float_as_uint(own_or_zero<WHOLE>(p[c], j, v[c][j])) & 0x7fffffffu);
-                }
-                if (a.out_kind == kNormOut16 && (WHOLE || p[c].skip < 8))
-                    piece_store<AE, WHOLE>(static_cast<char *>(a.out) + row * a.ldo * 2, p[c], v[c]);
             }
-            if (a.out_kind == kNormOut16)
-                continue;
-            float sc, inv;
-            quant_rule::scale_of(row_max<WAVES>(m, part, turn), kF32, sc, inv, a.out_kind == kNormOutFp8);
-            if (t == 0)
-                a.out_scale[row] = sc;
-            uint8_t *q = static_cast<uint8_t *>(a.out) + row * a.ldo;
+            if (OUT == kOutFloat && (WHOLE || p[c].skip < 8))
+                piece_store<AE, WHOLE>(static_cast<char *>(a.out) + row * a.ldo * 2, p[c], v[c]);
+        }
+        if constexpr (OUT != kOutCodes)
+            return;
+        float sc, inv;
+        quant_rule::scale_of(row_max<WAVES>(m, part, turn), kF32, sc, inv, a.out_kind == kNormOutFp8);
+        if (t == 0)
+            a.out_scale[row] = sc;
+        uint8_t *q = static_cast<uint8_t *>(a.out) + row * a.ldo;
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                u32 lo, hi;
-                if (a.out_kind == kNormOutFp8) {
-                    lo = quant_rule::codes4_fp8(v[c][0], v[c][1], v[c][2], v[c][3], inv);
-                    hi = quant_rule::codes4_fp8(v[c][4], v[c][5], v[c][6], v[c][7], inv);
-                } else {
-                    lo = quant_rule::codes4_i8(v[c][0], v[c][1], v[c][2], v[c][3], inv);
-                    hi = quant_rule::codes4_i8(v[c][4], v[c][5], v[c][6], v[c][7], inv);
-                }
-                if (WHOLE || p[c].skip == 0) {
-                    *reinterpret_cast<uint2 *>(q + p[c].at) = make_uint2(lo, hi);
-                } else {
+        for (int c = 0; c < CH; ++c) {
+            u32 lo, hi;
+            if (a.out_kind == kNormOutFp8) {
+                lo = quant_rule::codes4_fp8(v[c][0], v[c][1], v[c][2], v[c][3], inv);
+                hi = quant_rule::codes4_fp8(v[c][4], v[c][5], v[c][6], v[c][7], inv);
+            } else {
+                lo = quant_rule::codes4_i8(v[c][0], v[c][1], v[c][2], v[c][3], inv);
+                hi = quant_rule::codes4_i8(v[c][4], v[c][5], v[c][6], v[c][7], inv);
+            }
+            if (WHOLE || p[c].skip == 0) {
+                *reinterpret_cast<uint2 *>(q + p[c].at) = make_uint2(lo, hi);
+            } else {
 #pragma unroll
-                    for (int j = 1; j < 8; ++j)
-                        if (j >= p[c].skip)
-                            q[p[c].at + j] = (uint8_t)((j < 4 ? lo >> (8 * j) : hi >> (8 * (j - 4))) & 0xffu);
-                }
+                for (int j = 1; j < 8; ++j)
+                    if (j >= p[c].skip)
+                        q[p[c].at + j] = (uint8_t)((j < 4 ? lo >> (8 * j) : hi >> (8 * (j - 4))) & 0xffu);
             }
         }
+    };
+    while (row < end) {
+        vectors();
+        do {
+            one_row();
+            row += R;
+        } while (row < stop);
     }
 }
 
@@ -560,29 +580,29 @@ struct Shape {
 // up to 16384 elements (beyond, a row and its vectors no longer fit the
 // registers of 1024 threads).
 constexpr int64_t kHeldElements = 16384;
-template <int XE, int AE, bool RES, int CH, int TPR, int R>
+template <int XE, int AE, bool RES, int OUT, int CH, int TPR, int R>
 Shape shape(int64_t K)
 {
-    return {K == CH * TPR * 8 ? norm_rows_kernel<XE, AE, RES, CH, TPR, R, true>
-                              : norm_rows_kernel<XE, AE, RES, CH, TPR, R, false>, TPR * R, R};
+    return {K == CH * TPR * 8 ? norm_rows_kernel<XE, AE, RES, OUT, CH, TPR, R, true>
+                              : norm_rows_kernel<XE, AE, RES, OUT, CH, TPR, R, false>, TPR * R, R};
 }
-template <int XE, int AE, bool RES>
+template <int XE, int AE, bool RES, int OUT>
 Shape pick(int64_t K)
 {
     const int64_t chunks = ceil_div(K, 8);
     if (chunks <= 64)
-        return shape<XE, AE, RES, 1, 64, 4>(K);
+        return shape<XE, AE, RES, OUT, 1, 64, 4>(K);
     if (chunks <= 128)
-        return shape<XE, AE, RES, 1, 128, 1>(K);
+        return shape<XE, AE, RES, OUT, 1, 128, 1>(K);
     if (chunks <= 256)
-        return shape<XE, AE, RES, 1, 256, 1>(K);
+        return shape<XE, AE, RES, OUT, 1, 256, 1>(K);
     if (chunks <= 512)
-        return shape<XE, AE, RES, 2, 256, 1>(K);
+        return shape<XE, AE, RES, OUT, 2, 256, 1>(K);
     if (chunks <= 1024)
-        return shape<XE, AE, RES, 2, 512, 1>(K);
+        return shape<XE, AE, RES, OUT, 2, 512, 1>(K);
     if (chunks <= 1536)
-        return shape<XE, AE, RES, 3, 512, 1>(K);
-    return shape<XE, AE, RES, 2, 1024, 1>(K);
+        return shape<XE, AE, RES, OUT, 3, 512, 1>(K);
+    return shape<XE, AE, RES, OUT, 2, 1024, 1>(K);
 }
 
 template <int XE, int AE>
@@ -595,7 +615,10 @@ hipError_t launch(const NormRowsArgs &a, hipStream_t stream)
         hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(256), 0, stream, a);
         return hipGetLastError();
     }
-    const Shape s = res ? pick<XE, AE, true>(a.K) : pick<XE, AE, false>(a.K);
+    const bool codes = a.out_kind != kNormOut16;
+    const Shape s = !res ? (codes ? pick<XE, AE, false, kOutCodes>(a.K) : pick<XE, AE, false, kOutFloat>(a.K))
+                  : a.next.kind == kNormNone ? pick<XE, AE, true, kOutNone>(a.K)
+                  : codes ? pick<XE, AE, true, kOutCodes>(a.K) : pick<XE, AE, true, kOutFloat>(a.K);
     // A run of rows per workgroup: enough workgroups to fill the device first.
     const int64_t want = 256 * 1024 / s.threads;
     const int64_t per_block = round_up(ceil_div(a.rows, want), s.rows);
@@ -604,12 +627,4 @@ hipError_t launch(const NormRowsArgs &a, hipStream_t stream)
 }
 
 }  // namespace
-
-hipError_t launch_norm_rows(const NormRowsArgs &a, hipStream_t stream)
-{
-    return a.x_kind == kElemBF16 ? launch<kBF16, kBF16>(a, stream)
-         : a.x_kind == kElemF16  ? launch<kF16, kF16>(a, stream)
-         : a.act_kind == kElemF16 ? launch<kF32, kF16>(a, stream) : launch<kF32, kBF16>(a, stream);
-}
-
 }  // namespace w8a8

@@ -1,4 +1,4 @@
-// Arithmetic shared by the norm kernels (norm_rows.hip): element loads and
+// Arithmetic shared by the norm kernels (norm_kernel.hpp): element loads and
 // stores with ragged tails, row reductions and the output forms.
 #pragma once
 
