@@ -33,7 +33,7 @@ LIBRARY = os.path.join(HERE, "libw8a8.so")
 TIMELINE_LIBRARY = os.path.join(HERE, "libw8a8_timeline.so")
 TIMELINE_SOURCE = "scaled_mm.hip"
 SOURCES = ["quant.hip", "prepack.hip", "scaled_mm.hip", "scaled_mm_fp8.hip", "skinny_mm.hip",
-           "quant_fp4.hip", "scaled_mm_fp4.hip", "norm_rows_bf16.hip", "norm_rows_f16.hip",
+           "quant_fp4.hip", "scaled_mm_fp4.hip", "skinny_fp4.hip", "norm_rows_bf16.hip", "norm_rows_f16.hip",
            "norm_rows_f32_bf16.hip", "norm_rows_f32_f16.hip", "api.cpp", "api_fp4.cpp", "api_norm.cpp"]
 ARCH = "gfx950"
 

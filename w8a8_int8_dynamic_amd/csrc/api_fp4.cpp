@@ -270,7 +270,13 @@ W8A8_API w8a8_status_t fp4_quant_scaled_mm_tile(const void *x, int x_dtype, int6
     if (st != W8A8_OK)
         return st;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    hipError_t err = w8a8::launch_quant_fp4(x, x_dtype, M, K, ldx, xq, ldq, x_scale, lds, s);
+    a.x = reinterpret_cast<const uint16_t *>(x);
+    a.ldx = ldx;
+    hipError_t err = w8a8::launch_quant_scaled_mm_fp4(a, x_dtype, mode, t, s);
+    if (err != hipErrorNotSupported)
+        return launched(err, what);
+    a.x = nullptr;
+    err = w8a8::launch_quant_fp4(x, x_dtype, M, K, ldx, xq, ldq, x_scale, lds, s);
     if (err != hipSuccess)
         return launched(err, what);
     return launched(w8a8::launch_scaled_mm_fp4(a, mode, t, s), what);

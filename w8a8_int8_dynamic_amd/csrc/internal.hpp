@@ -205,13 +205,26 @@ int mm_tile_auto(int64_t M, int64_t N, int64_t K);
 bool mm_launch_fits(int tile, int64_t M, int64_t N);
 bool fp8_launch_fits(int tile, int64_t M, int64_t N);
 
-// ---- the microscaled 4-bit matmul (scaled_mm_fp4.hip) ----
-// mode kOutI32 stores the raw fp32 sums.
+// ---- the microscaled 4-bit matmul (scaled_mm_fp4.hip, skinny_fp4.hip) ----
+// Tiles: the main kernel's, then the small-M ones; mode kOutI32 stores the raw
+// fp32 sums. quant: the small-M kernels that quantize rows of x (by element
+// kind, then mode) in the same launch.
+struct Fp4Skinny {
+    TileEntry tile;
+    MmKernel quant[3][kOutKinds];
+};
+int fp4_skinny_count();
+const Fp4Skinny &fp4_skinny(int i);
 int fp4_tile_count();
 const char *fp4_tile_name(int tile);
 int fp4_tile_auto(int64_t M, int64_t N, int64_t K);
 bool fp4_launch_fits(int tile, int64_t M, int64_t N);
 hipError_t launch_scaled_mm_fp4(const MmArgs &a, int mode, int tile, hipStream_t stream);
+// The quant of a.x (element kind x_kind) and the matmul in one launch;
+// hipErrorNotSupported (nothing launched) for a main tile or more rows than
+// the small-M kernel quantizes itself.
+hipError_t launch_skinny_quant_fp4(const MmArgs &a, int x_kind, int mode, int i, hipStream_t stream);
+hipError_t launch_quant_scaled_mm_fp4(const MmArgs &a, int x_kind, int mode, int tile, hipStream_t stream);
 
 // ---- the e4m3 twin of the matmul (scaled_mm_fp8.hip) ----
 // Tiles are numbered as the int8 ones (main, then small-M); mode kOutI32

@@ -32,18 +32,25 @@ struct Fp4Entry {
 
 const auto kFp4Tiles = main_table<Fp4Entry>(std::make_index_sequence<kNumMainTiles>{});
 
+const TileEntry &fp4_entry(int tile)
+{
+    return tile < kNumMainTiles ? kFp4Tiles[tile] : fp4_skinny(tile - kNumMainTiles).tile;
+}
+
 }  // namespace
 
-int fp4_tile_count() { return kNumMainTiles; }
-const char *fp4_tile_name(int tile) { return kFp4Tiles[tile].name; }
+int fp4_tile_count() { return kNumMainTiles + fp4_skinny_count(); }
+const char *fp4_tile_name(int tile) { return fp4_entry(tile).name; }
 
 int fp4_tile_auto(int64_t M, int64_t N, int64_t K)
 {
+    if (M <= 16)
+        return kNumMainTiles;
     const double cus = 256.0;
     const double kk = (double)round_up(K / 2, 64);
     int best = 0;
     double best_cost = 1e300;
-    for (int t = 0; t < fp4_tile_count(); ++t) {
+    for (int t = 0; t < kNumMainTiles; ++t) {
         const TileEntry &e = kFp4Tiles[t];
         const int64_t tiles_m = ceil_div(M, e.bm);
         const int64_t tiles = tiles_m * ceil_div(N, e.bn);
@@ -62,16 +69,23 @@ int fp4_tile_auto(int64_t M, int64_t N, int64_t K)
 
 bool fp4_launch_fits(int tile, int64_t M, int64_t N)
 {
-    const TileEntry &e = kFp4Tiles[tile];
+    const TileEntry &e = fp4_entry(tile);
     return mm_grid_fits(ceil_div(M, e.bm) * ceil_div(N, e.bn), e.threads);
 }
 
 hipError_t launch_scaled_mm_fp4(const MmArgs &a, int mode, int tile, hipStream_t stream)
 {
-    const TileEntry &e = kFp4Tiles[tile];
+    const TileEntry &e = fp4_entry(tile);
     const int64_t tiles = ceil_div(a.M, e.bm) * ceil_div(a.N, e.bn);
     hipLaunchKernelGGL(e.plain[mode], dim3((unsigned)tiles), dim3(e.threads), 0, stream, a);
     return hipGetLastError();
+}
+
+hipError_t launch_quant_scaled_mm_fp4(const MmArgs &a, int x_kind, int mode, int tile, hipStream_t stream)
+{
+    if (tile < kNumMainTiles)
+        return hipErrorNotSupported;
+    return launch_skinny_quant_fp4(a, x_kind, mode, tile - kNumMainTiles, stream);
 }
 
 }  // namespace w8a8
