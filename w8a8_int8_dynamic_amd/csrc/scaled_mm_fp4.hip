@@ -42,24 +42,48 @@ const TileEntry &fp4_entry(int tile)
 int fp4_tile_count() { return kNumMainTiles + fp4_skinny_count(); }
 const char *fp4_tile_name(int tile) { return fp4_entry(tile).name; }
 
+// Automatic choice: the smallest modelled time, a sum of what each tile pays
+//   main:    fixed + per round of 256 workgroups (a round, and each k-block of
+//            it) + per MB of weight and of 16-bit output;
+//   small-M: fixed + per workgroup and k-block + per chunk of 512 elements in
+//            a wave's chain, for up to 256 token rows.
+// The rates (us) are fitted to the times of every tile on 643 shapes (M 8-8192,
+// N 512-12288, K 512-12288, weights from HBM) on MI355X; over them the chosen
+// tile takes 0.9 % more than the best on average, 21 % at most.
+struct MainCost {
+    double fixed, kblock, round, weight, out;
+};
+constexpr MainCost kMainCost[] = {
+    {3.89, 0.1045, 0.0, 0.0588, 0.2476},   {4.14, 0.1504, 0.217, 0.0578, 0.2575}, {3.04, 0.1691, 1.312, 0.0218, 0.4217},
+    {3.07, 0.2347, 2.652, 0.0308, 0.2244}, {5.22, 0.2994, 2.777, 0.0080, 0.2614}, {1.93, 0.3999, 4.040, 0.0910, 0.1613},
+    {4.32, 0.5250, 6.028, 0.0053, 0.1106}, {0.40, 0.5753, 8.836, 0.1214, 0.1250}};
+static_assert(sizeof(kMainCost) / sizeof(kMainCost[0]) == kNumMainTiles, "a cost for every main tile");
+struct SmallCost {
+    double fixed, work, chain;
+};
+constexpr SmallCost kSmallCost[] = {{3.29, 1.773e-4, 0.692}, {3.55, 2.482e-4, 1.164}};
+constexpr int64_t kSmallRows = 256;
+
 int fp4_tile_auto(int64_t M, int64_t N, int64_t K)
 {
-    if (M <= 16)
-        return kNumMainTiles;
-    const double cus = 256.0;
-    const double kk = (double)round_up(K / 2, 64);
+    const double kblocks = (double)ceil_div(K, 128);
     int best = 0;
     double best_cost = 1e300;
-    for (int t = 0; t < kNumMainTiles; ++t) {
-        const TileEntry &e = kFp4Tiles[t];
-        const int64_t tiles_m = ceil_div(M, e.bm);
-        const int64_t tiles = tiles_m * ceil_div(N, e.bn);
-        const double rounds = std::ceil((double)tiles / cus);
-        const double t_mma = 2.0 * e.bm * e.bn * kk / 16000.0;
-        const double t_l2 = (double)(e.bm + e.bn) * kk / 80.0;
-        const double t_hbm = (double)e.bn * kk / (double)std::min<int64_t>(tiles_m, 4) / 22.0;
-        const double cost = rounds * (std::max({t_mma, t_l2, t_hbm}) + 3000.0);
-        if (cost < best_cost * 0.999) {
+    for (int t = 0; t < fp4_tile_count(); ++t) {
+        const TileEntry &e = fp4_entry(t);
+        if (e.skinny && M > kSmallRows)
+            continue;
+        const double tiles = (double)(ceil_div(M, e.bm) * ceil_div(N, e.bn));
+        double cost;
+        if (e.skinny) {
+            const SmallCost &c = kSmallCost[t - kNumMainTiles];
+            cost = c.fixed + c.work * tiles * kblocks + c.chain * std::ceil((double)ceil_div(K, 512) / 8.0);
+        } else {
+            const MainCost &c = kMainCost[t];
+            cost = c.fixed + std::ceil(tiles / 256.0) * (c.kblock * kblocks + c.round) +
+                   c.weight * (double)N * (double)K * 17.0 / 32e6 + c.out * (double)M * (double)N * 2e-6;
+        }
+        if (cost < best_cost) {
             best_cost = cost;
             best = t;
         }
