@@ -603,9 +603,9 @@ w8a8_status_t norm_rows(const void *x, int x_dtype, int64_t M, int64_t K, int64_
 /* A block's way back into the residual stream x [M, ldx] (bf16, fp16, or fp32
  * with a 16-bit y):
  *   r = residual_scale * x + branch_scale * gate * post(y)
- * y [M, ldy]; post: a norm with weight and bias only, or NULL (y itself);
- * gate [gate_groups, ld_gate] with rows as a norm's scale, or NULL (1); r
- * [M, ldr] in x's type. r may be x itself (same pointer and pitch). */
+ * y [M, ldy]; gate [gate_groups, ld_gate] with rows as a norm's scale, or
+ * NULL (1); r [M, ldr] in x's type. r may be x itself (same pointer and
+ * pitch). post is the entry point's. */
 typedef struct w8a8_residual {
     const void *x;
     const void *y;
@@ -616,7 +616,6 @@ typedef struct w8a8_residual {
     const void *gate;
     int64_t ld_gate;
     int64_t gate_groups;
-    const w8a8_norm_t *post;
     float residual_scale;
     float branch_scale;
     int x_dtype;
@@ -625,13 +624,14 @@ typedef struct w8a8_residual {
 } w8a8_residual_t;
 
 /*
- * gated_residual_rows - r, and with a norm (or NULL) also norm(r) to out as
- * norm_rows writes it (16-bit: in y's type), taken from r before its
+ * gated_residual_rows - r, with post a norm with weight and bias only, or
+ * NULL (y itself); and with a norm (or NULL) also norm(r) to out as norm_rows
+ * writes it (16-bit: in y's type), taken from r before its
  * rounding to the stored type. Requirements: those of norm_rows.
  */
-w8a8_status_t gated_residual_rows(const w8a8_residual_t *res, int64_t M, int64_t K,
-                                  const w8a8_norm_t *norm, int out_kind, void *out, int64_t ldo,
-                                  float *out_scale, void *stream);
+w8a8_status_t gated_residual_rows(const w8a8_residual_t *res, const w8a8_norm_t *post, int64_t M,
+                                  int64_t K, const w8a8_norm_t *norm, int out_kind, void *out,
+                                  int64_t ldo, float *out_scale, void *stream);
 
 /* Number of tile configurations, a short name of one, and the tile the
  * automatic choice picks for a shape. Main kernel: "128x192/m1n2k2/l33" is

@@ -2,32 +2,35 @@
 and the 64-bit reference on values worked out by hand."""
 from __future__ import annotations
 
-import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
 
 from tests import norm_reference as ref
-from tests.test_abi_cpu import A, ALIGN, DEVICE, L, MODE, NULL, OK, SHAPE
+from tests.test_abi_cpu import A, ALIGN, DEVICE, HEADER, L, MODE, NULL, OK, SHAPE
 from w8a8_int8_dynamic_amd import _lib, ops
 
 NO_GPU = not torch.cuda.is_available()
 
 
-def ns(**k):
-    return _lib.NormStruct(**{"kind": 0, "eps": 1e-6, "groups": 1, "ld_scale": 64, "ld_shift": 64, **k})
+def ns(kind=0, eps=1e-6, weight=0, bias=0, scale=0, shift=0, ld_scale=64, ld_shift=64, groups=1, vec_dtype=0,
+       mod_dtype=0):
+    return _lib.NORM_STRUCT.pack(kind, eps, weight, bias, scale, shift, ld_scale, ld_shift, groups, vec_dtype,
+                                 mod_dtype)
 
 
 def rows(n=None, x=A, t=0, M=4, K=64, ldx=64, act=0, kind=0, out=A, ldo=64, s=A):
     n = ns() if n is None else n
-    return L.norm_rows(x, t, M, K, ldx, ctypes.byref(n) if n else None, act, kind, out, ldo, s, None)
+    return L.norm_rows(x, t, M, K, ldx, n, act, kind, out, ldo, s, None)
 
 
-def res(n=None, M=4, K=64, kind=0, out=A, ldo=64, s=A, **k):
-    r = _lib.ResidualStruct(**{"x": A, "y": A, "r": A, "ldx": 64, "ldy": 64, "ldr": 64, "gate_groups": 1,
-                               "ld_gate": 64, "residual_scale": 1.0, "branch_scale": 1.0, **k})
-    return L.gated_residual_rows(ctypes.byref(r), M, K, None if n is None else ctypes.byref(n), kind, out, ldo, s,
-                                 None)
+def res(n=None, post=None, M=4, K=64, kind=0, out=A, ldo=64, s=A, x=A, y=A, r=A, ldx=64, ldy=64, ldr=64, gate=0,
+        ld_gate=64, gate_groups=1, x_dtype=0, y_dtype=0, gate_dtype=0):
+    b = _lib.RESIDUAL_STRUCT.pack(x or 0, y or 0, r or 0, ldx, ldy, ldr, gate, ld_gate, gate_groups, 1.0, 1.0,
+                                  x_dtype, y_dtype, gate_dtype)
+    return L.gated_residual_rows(b, post, M, K, n, kind, out, ldo, s, None)
 
 
 def test_norm_rows_checks():
@@ -58,7 +61,7 @@ def test_norm_struct_checks():
 
 
 def test_residual_checks():
-    assert L.gated_residual_rows(None, 4, 64, None, 0, A, 64, A, None) == NULL
+    assert L.gated_residual_rows(None, None, 4, 64, None, 0, A, 64, A, None) == NULL
     assert res(x_dtype=3) == MODE and res(y_dtype=1) == MODE and res(x_dtype=2) == MODE
     assert res(M=-1) == SHAPE and res(K=0) == SHAPE
     assert res(ldx=63) == SHAPE and res(ldy=63) == SHAPE and res(ldr=63) == SHAPE
@@ -67,22 +70,26 @@ def test_residual_checks():
     assert res(gate=A, gate_dtype=5) == MODE and res(gate=A, gate_groups=3) == SHAPE
     assert res(gate=A, gate_groups=2, ld_gate=63) == SHAPE and res(gate=A, gate_groups=0) == SHAPE
     assert res(gate=A + 2, gate_dtype=1) == ALIGN
-    post = ns(scale=A)
-    assert res(post=ctypes.pointer(post)) == MODE                 # a branch's norm has no modulation
-    post = ns(kind=7)
-    assert res(post=ctypes.pointer(post)) == MODE
+    assert res(post=ns(scale=A)) == MODE                          # a branch's norm has no modulation
+    assert res(post=ns(kind=7)) == MODE
     assert res(n=ns(), out=None) == NULL and res(n=ns(), ldo=0) == SHAPE and res(n=ns(), kind=9) == MODE
     assert res(M=0, x=None, y=None, r=None) == OK
     if NO_GPU:
         assert res(out=None, ldo=0) == DEVICE and res(x_dtype=1, y_dtype=2, n=ns(), kind=1) == DEVICE
-        post = ns(weight=A)
-        assert res(post=ctypes.pointer(post), gate=A, gate_groups=4) == DEVICE
+        assert res(post=ns(weight=A), gate=A, gate_groups=4) == DEVICE
 
 
-def test_structs_match_the_header():
-    """The binding's structures have the C layout (sizes of the LP64 ABI)."""
-    assert ctypes.sizeof(_lib.NormStruct) == 72 and _lib.NormStruct.groups.offset == 56
-    assert ctypes.sizeof(_lib.ResidualStruct) == 104 and _lib.ResidualStruct.residual_scale.offset == 80
+def test_structs_match_the_header(tmp_path):
+    """The binding packs the structures in the C layout: a C program prints it."""
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include "w8a8.h"\nint main(void) { printf("%zu %zu %zu %zu\\n", '
+                   "sizeof(w8a8_norm_t), offsetof(w8a8_norm_t, mod_dtype), sizeof(w8a8_residual_t), "
+                   "offsetof(w8a8_residual_t, gate_dtype)); return 0; }")
+    subprocess.run(["gcc", "-I", os.path.dirname(HEADER), str(src), "-o", str(tmp_path / "layout")], check=True)
+    got = subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True).stdout.split()
+    n = _lib.NORM_STRUCT.pack(*range(10), 77)
+    r = _lib.RESIDUAL_STRUCT.pack(*range(13), 78)
+    assert [int(v) for v in got] == [len(n), n.index(b"\x4d"), len(r), r.index(b"\x4e")]
 
 
 def test_host_tensors_are_refused():

@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(HERE, "libw8a8.so")
@@ -35,23 +36,9 @@ W8A8_NORM_OUT_INT8 = 1
 W8A8_NORM_OUT_FP8 = 2
 
 
-class NormStruct(ctypes.Structure):
-    """w8a8_norm_t"""
-    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
-                ("bias", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p),
-                ("ld_scale", ctypes.c_int64), ("ld_shift", ctypes.c_int64), ("groups", ctypes.c_int64),
-                ("vec_dtype", ctypes.c_int), ("mod_dtype", ctypes.c_int)]
-
-
-class ResidualStruct(ctypes.Structure):
-    """w8a8_residual_t"""
-    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("r", ctypes.c_void_p),
-                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64),
-                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64), ("gate_groups", ctypes.c_int64),
-                ("post", ctypes.POINTER(NormStruct)), ("residual_scale", ctypes.c_float),
-                ("branch_scale", ctypes.c_float), ("x_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int),
-                ("gate_dtype", ctypes.c_int)]
-
+# w8a8_norm_t and w8a8_residual_t, packed in the C layout (passed as bytes)
+NORM_STRUCT = struct.Struct("@if4P3q2i")
+RESIDUAL_STRUCT = struct.Struct("@3P3qP2q2f3i4x")
 
 # name -> (restype, argtypes), in the order of include/w8a8.h
 _i64, _vp, _int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
@@ -112,7 +99,7 @@ SIGNATURES = {
     "fp4_quant_scaled_mm_tile": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
                                         _i64, _i64, _int, _vp, _i64, _vp, _int]),
     "norm_rows": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _int, _vp, _i64, _vp, _vp]),
-    "gated_residual_rows": (_int, [_vp, _i64, _i64, _vp, _int, _vp, _i64, _vp, _vp]),
+    "gated_residual_rows": (_int, [_vp, _vp, _i64, _i64, _vp, _int, _vp, _i64, _vp, _vp]),
     "w8a8_fp4_tile_count": (_int, []),
     "w8a8_fp4_tile_name": (ctypes.c_char_p, [_int]),
     "w8a8_fp4_tile_auto": (_int, [_i64, _i64, _i64]),

@@ -123,8 +123,8 @@ W8A8_API w8a8_status_t norm_rows(const void *x, int x_dtype, int64_t M, int64_t 
     return launched(w8a8::launch_norm_rows(a, reinterpret_cast<hipStream_t>(stream)), what);
 }
 
-W8A8_API w8a8_status_t gated_residual_rows(const w8a8_residual_t *res, int64_t M, int64_t K,
-                                           const w8a8_norm_t *norm, int out_kind, void *out, int64_t ldo,
+W8A8_API w8a8_status_t gated_residual_rows(const w8a8_residual_t *res, const w8a8_norm_t *post, int64_t M,
+                                           int64_t K, const w8a8_norm_t *norm, int out_kind, void *out, int64_t ldo,
                                            float *out_scale, void *stream)
 {
     const char *what = "gated_residual_rows";
@@ -158,8 +158,8 @@ W8A8_API w8a8_status_t gated_residual_rows(const w8a8_residual_t *res, int64_t M
         a.ld_gate = res->ld_gate;
         a.gate_rows = M > 0 ? M / res->gate_groups : 1;
     }
-    if (res->post) {
-        st = norm_args(res->post, M, K, true, what, a.post);
+    if (post) {
+        st = norm_args(post, M, K, true, what, a.post);
         if (st != W8A8_OK)
             return st;
     }

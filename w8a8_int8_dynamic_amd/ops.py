@@ -8,7 +8,6 @@ contiguous (stride 1); the row stride becomes the leading dimension.
 """
 from __future__ import annotations
 
-import ctypes
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
@@ -438,6 +437,25 @@ def fp8_quant_scaled_mm(x: torch.Tensor, w_packed: torch.Tensor, ws: Optional[to
 # ---- the microscaled 4-bit (MX FP4) layer ---------------------------------
 _DTYPE = {torch.bfloat16: _lib.W8A8_T_BF16, torch.float16: _lib.W8A8_T_F16, torch.float32: _lib.W8A8_T_F32}
 _FP4_BLOCK = 32
+_entry = {}
+
+
+def _run(x: torch.Tensor, name: str, *args, tile: Tuple[int, ...] = ()) -> None:
+    """Call entry point ``name`` with args, x's current stream and tile (behind
+    it, where the entry point has one), on x's device.
+    (The device is only switched when it is not the current one, and the
+    stream is asked for by its handle: a call of a small kernel is short.)"""
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(_lib.lib(), name)
+    device = x.get_device()
+    if device == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device), *tile)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device), *tile)
+    if rc != _lib.W8A8_OK:
+        raise _lib.W8A8Error(rc, name, _lib.last_error())
 
 
 def _fp4_k(K: int) -> int:
@@ -446,8 +464,10 @@ def _fp4_k(K: int) -> int:
     return K
 
 
-def _bytes_rows(M: int, n: int, device) -> torch.Tensor:
-    """uint8 [M, n] view of a buffer whose rows are padded to 16 bytes."""
+def _scale_bytes(M: int, n: int, device) -> torch.Tensor:
+    """uint8 [M, n] whose rows start on, and are readable to, 16-byte boundaries."""
+    if n % 16 == 0:
+        return torch.empty((M, n), dtype=torch.uint8, device=device)
     return torch.empty((M, _round_up(n, 16)), dtype=torch.uint8, device=device)[:, :n]
 
 
@@ -466,18 +486,27 @@ def _scale_rows(xs: torch.Tensor) -> torch.Tensor:
     """xs itself when its rows start on 16-byte boundaries and the last one can
     be read to a whole 16 bytes, else a copy into a row-padded buffer."""
     M, n = xs.shape
-    ld = _ld(xs)
-    if xs.data_ptr() % 16 == 0 and ld % 16 == 0 and \
+    ld = _ldp(xs)
+    if xs.data_ptr() % 16 == 0 and ld % 16 == 0 and ld >= n and \
             xs.untyped_storage().nbytes() - xs.storage_offset() >= M * ld:
         return xs
-    buf = _bytes_rows(M, n, xs.device)
+    buf = _scale_bytes(M, n, xs.device)
     buf.copy_(xs)
     return buf
 
 
 def _ldp(t: torch.Tensor) -> int:
-    """Row pitch of a row-padded byte buffer (one row: its padded length)."""
+    """Row pitch of byte rows (a single row's: its length to a whole 16 bytes)."""
     return t.stride(0) if t.shape[0] > 1 else _round_up(t.shape[1], 16)
+
+
+def _float_rows(x: torch.Tensor, name: str) -> int:
+    """The element type of rows x [M, K] of floats."""
+    t = _DTYPE.get(x.dtype)
+    if t is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
+    _matrix(x, name, x.dtype)
+    return t
 
 
 def fp4_quant_per_block(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
@@ -485,19 +514,18 @@ def fp4_quant_per_block(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
     """MX FP4 quantization of bf16, fp16 or fp32 x [M, K] (K a multiple of 32):
     (uint8 codes [M, K/2], the even element in the low nibble; uint8 scale
     bytes [M, K/32], one power of two per 32 elements)."""
-    if x.dtype not in _DTYPE:
-        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    _matrix(x, "x", x.dtype)
-    M, K = x.shape[0], _fp4_k(x.shape[1])
-    x = _rows_aligned(x, 4 if x.dtype == torch.float32 else 8)
-    xq = _bytes_rows(M, K // 2, x.device) if xq is None else xq
-    xs = _bytes_rows(M, K // _FP4_BLOCK, x.device) if xs is None else xs
-    if _fp4_rows(xq, xs) != (M, K):
-        raise ValueError(f"xq must have shape {(M, K // 2)}")
-    _same_device(x, xq)
-    with torch.cuda.device(x.device):
-        call("fp4_quant_per_block", x.data_ptr(), _DTYPE[x.dtype], M, K, _ld(x), xq.data_ptr(), _ld(xq),
-             xs.data_ptr(), _ld(xs), _stream(x))
+    t = _float_rows(x, "x")
+    M, K = x.shape
+    _fp4_k(K)
+    x = _rows_aligned(x, 4 if t == _lib.W8A8_T_F32 else 8)
+    own = xq is None and xs is None
+    xq = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device) if xq is None else xq
+    xs = _scale_bytes(M, K // _FP4_BLOCK, x.device) if xs is None else xs
+    if not own:
+        if _fp4_rows(xq, xs) != (M, K):
+            raise ValueError(f"xq must have shape {(M, K // 2)}")
+        _same_device(x, xq)
+    _run(x, "fp4_quant_per_block", x.data_ptr(), t, M, K, _ld(x), xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs))
     return xq, xs
 
 
@@ -510,9 +538,7 @@ def fp4_dequant(xq: torch.Tensor, xs: torch.Tensor, dtype: torch.dtype = torch.b
     if xq.data_ptr() % 4 != 0 or _ld(xq) % 4 != 0:
         xq = _rows_aligned(xq, 16)
     out = torch.empty((M, K), dtype=dtype, device=xq.device)
-    with torch.cuda.device(xq.device):
-        call("fp4_dequant", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), M, K, _DTYPE[dtype],
-             out.data_ptr(), K, _stream(xq))
+    _run(xq, "fp4_dequant", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), M, K, _DTYPE[dtype], out.data_ptr(), K)
     return out
 
 
@@ -525,12 +551,18 @@ def _fp4_packed(N: int, K: int, device) -> Tuple[torch.Tensor, torch.Tensor]:
             torch.empty((s,), dtype=torch.uint8, device=device))
 
 
-def _check_fp4_packed(w_packed: torch.Tensor, s_packed: torch.Tensor, N: int, K: int) -> None:
-    L = _lib.lib()
-    for t, n, name in ((w_packed, L.fp4_prepack_weight_bytes(N, K), "w_packed"),
-                       (s_packed, L.fp4_prepack_scale_bytes(N, K), "s_packed")):
-        if not t.is_cuda or t.dtype != torch.uint8 or not t.is_contiguous() or n == 0 or t.numel() < n:
+def _check_fp4_packed(w_packed: torch.Tensor, s_packed: torch.Tensor, N: int, K: int, ref: torch.Tensor) -> None:
+    """The packed buffers of a weight [N, K] (fp4_prepack_weight_bytes and
+    fp4_prepack_scale_bytes of include/w8a8.h), on ref's device."""
+    if N < 1:
+        raise ValueError(f"N must be at least 1, got {N}")
+    rows = _round_up(N, 16)
+    for t, n, name in ((w_packed, rows * _round_up(K, 128) // 2, "w_packed"),
+                       (s_packed, rows * _round_up(K, 512) // _FP4_BLOCK, "s_packed")):
+        if t.dtype != torch.uint8 or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
             raise ValueError(f"{name} must be a uint8 device buffer of the packed layout (N, K)")
+        if t.get_device() != ref.get_device():
+            raise ValueError(f"all tensors must be on {ref.device}, got one on {t.device}")
 
 
 def fp4_prepack_weight(wq: torch.Tensor, ws: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -538,9 +570,8 @@ def fp4_prepack_weight(wq: torch.Tensor, ws: torch.Tensor) -> Tuple[torch.Tensor
     [N, K/32], into the two buffers that fp4_scaled_mm reads."""
     N, K = _fp4_rows(wq, ws)
     packed, spacked = _fp4_packed(N, K, wq.device)
-    with torch.cuda.device(wq.device):
-        call("fp4_prepack_weight", wq.data_ptr(), _ld(wq), ws.data_ptr(), _ld(ws), N, K, packed.data_ptr(),
-             spacked.data_ptr(), _stream(wq))
+    _run(wq, "fp4_prepack_weight", wq.data_ptr(), _ld(wq), ws.data_ptr(), _ld(ws), N, K, packed.data_ptr(),
+         spacked.data_ptr())
     return packed, spacked
 
 
@@ -554,37 +585,38 @@ def fp4_quant_prepack_weight(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tenso
     f32 = w.dtype == torch.float32
     w = _rows_aligned(w, 4 if f32 else 8)
     packed, spacked = _fp4_packed(N, K, w.device)
-    with torch.cuda.device(w.device):
-        call("fp4_quant_prepack_weight", w.data_ptr(), 0 if f32 else 1, N, K, _ld(w), packed.data_ptr(),
-             spacked.data_ptr(), _stream(w))
+    _run(w, "fp4_quant_prepack_weight", w.data_ptr(), 0 if f32 else 1, N, K, _ld(w), packed.data_ptr(),
+         spacked.data_ptr())
     return packed, spacked
 
 
 def fp4_unpack_weight(w_packed: torch.Tensor, s_packed: torch.Tensor, N: int, K: int
                       ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Inverse of fp4_prepack_weight: codes [N, K/2] and scale bytes [N, K/32]."""
-    _check_fp4_packed(w_packed, s_packed, N, _fp4_k(K))
-    _same_device(w_packed, s_packed)
+    _check_fp4_packed(w_packed, s_packed, N, _fp4_k(K), w_packed)
     wq = torch.empty((N, K // 2), dtype=torch.uint8, device=w_packed.device)
     ws = torch.empty((N, K // _FP4_BLOCK), dtype=torch.uint8, device=w_packed.device)
-    with torch.cuda.device(w_packed.device):
-        call("fp4_unpack_weight", w_packed.data_ptr(), s_packed.data_ptr(), N, K, wq.data_ptr(), K // 2,
-             ws.data_ptr(), K // _FP4_BLOCK, _stream(w_packed))
+    _run(w_packed, "fp4_unpack_weight", w_packed.data_ptr(), s_packed.data_ptr(), N, K, wq.data_ptr(), K // 2,
+         ws.data_ptr(), K // _FP4_BLOCK)
     return wq, ws
 
 
-def _fp4_out(M: int, N: int, bias, out_dtype, out, device):
-    if out_dtype not in _FP8_OUT_MODE:
+def _fp4_out(M: int, N: int, bias, out_dtype, out, x: torch.Tensor):
+    """(mode, out), with bias and out checked."""
+    mode = _FP8_OUT_MODE.get(out_dtype)
+    if mode is None:
         raise TypeError("out_dtype must be torch.bfloat16, torch.float16 or torch.float32")
-    mode = _FP8_OUT_MODE[out_dtype]
-    if mode != W8A8_OUT_I32:
+    if bias is not None:
+        if mode == W8A8_OUT_I32:
+            raise ValueError("out_dtype=torch.float32 gives the raw sums: bias must be None")
         _vector(bias, N, "bias", out_dtype)
-    elif bias is not None:
-        raise ValueError("out_dtype=torch.float32 gives the raw sums: bias must be None")
-    out = torch.empty((M, N), dtype=out_dtype, device=device) if out is None else out
+        _same_device(x, bias)
+    if out is None:
+        return mode, torch.empty((M, N), dtype=out_dtype, device=x.device)
     _matrix(out, "out", out_dtype)
     if out.shape != (M, N):
         raise ValueError(f"out must have shape {(M, N)}")
+    _same_device(x, out)
     return mode, out
 
 
@@ -595,14 +627,12 @@ def fp4_scaled_mm(xq: torch.Tensor, xs: torch.Tensor, w_packed: torch.Tensor, s_
     [M, K/32]) with a packed weight, plus bias, rounded to out_dtype (bf16 or
     fp16; the bias in the same type), or the raw fp32 sums."""
     M, K = _fp4_rows(xq, xs)
-    _check_fp4_packed(w_packed, s_packed, N, K)
-    mode, out = _fp4_out(M, N, bias, out_dtype, out, xq.device)
-    _same_device(xq, w_packed, s_packed, bias, out)
+    _check_fp4_packed(w_packed, s_packed, N, K, xq)
+    mode, out = _fp4_out(M, N, bias, out_dtype, out, xq)
     xq, xs = _rows_aligned(xq, 16), _scale_rows(xs)
-    with torch.cuda.device(xq.device):
-        call("fp4_scaled_mm_tile", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ldp(xs), w_packed.data_ptr(),
-             s_packed.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, mode, out.data_ptr(),
-             _ld(out), _stream(xq), tile)
+    _run(xq, "fp4_scaled_mm_tile", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ldp(xs), w_packed.data_ptr(),
+         s_packed.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, mode, out.data_ptr(), _ld(out),
+         tile=(tile,))
     return out
 
 
@@ -612,21 +642,19 @@ def fp4_quant_scaled_mm(x: torch.Tensor, w_packed: torch.Tensor, s_packed: torch
                         ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """fp4_quant_per_block of x [M, K] and fp4_scaled_mm in one call: (out, xq,
     xs). out_dtype defaults to x's type, bf16 for fp32 x."""
-    if x.dtype not in _DTYPE:
-        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    _matrix(x, "x", x.dtype)
-    M, K = x.shape[0], _fp4_k(x.shape[1])
+    t = _float_rows(x, "x")
+    M, K = x.shape
+    _fp4_k(K)
     if out_dtype is None:
-        out_dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
-    _check_fp4_packed(w_packed, s_packed, N, K)
-    mode, out = _fp4_out(M, N, bias, out_dtype, out, x.device)
-    _same_device(x, w_packed, s_packed, bias, out)
-    x = _rows_aligned(x, 4 if x.dtype == torch.float32 else 8)
-    xq, xs = _bytes_rows(M, K // 2, x.device), _bytes_rows(M, K // _FP4_BLOCK, x.device)
-    with torch.cuda.device(x.device):
-        call("fp4_quant_scaled_mm_tile", x.data_ptr(), _DTYPE[x.dtype], _ld(x), xq.data_ptr(), _ldp(xq),
-             xs.data_ptr(), _ldp(xs), w_packed.data_ptr(), s_packed.data_ptr(),
-             None if bias is None else bias.data_ptr(), M, N, K, mode, out.data_ptr(), _ld(out), _stream(x), tile)
+        out_dtype = torch.bfloat16 if t == _lib.W8A8_T_F32 else x.dtype
+    _check_fp4_packed(w_packed, s_packed, N, K, x)
+    mode, out = _fp4_out(M, N, bias, out_dtype, out, x)
+    x = _rows_aligned(x, 4 if t == _lib.W8A8_T_F32 else 8)
+    xq = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+    xs = _scale_bytes(M, K // _FP4_BLOCK, x.device)
+    _run(x, "fp4_quant_scaled_mm_tile", x.data_ptr(), t, _ld(x), xq.data_ptr(), _ldp(xq), xs.data_ptr(), _ldp(xs),
+         w_packed.data_ptr(), s_packed.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, mode,
+         out.data_ptr(), _ld(out), tile=(tile,))
     return out, xq, xs
 
 
@@ -663,7 +691,7 @@ def device_supported(device: int = 0) -> bool:
 
 
 # ---- norms around a layer -------------------------------------------------
-@dataclass(frozen=True)
+@dataclass(eq=False)
 class Norm:
     """A norm over the last dimension and its vectors:
 
@@ -692,7 +720,7 @@ def _groups(t: torch.Tensor, M: int, K: int, ref: torch.Tensor, name: str) -> Tu
     if t.dtype not in _DTYPE:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
     shape = t.shape
-    if t.device != ref.device or len(shape) not in (1, 2) or shape[-1] != K or (K > 1 and t.stride(-1) != 1):
+    if len(shape) not in (1, 2) or shape[-1] != K or (K > 1 and t.stride(-1) != 1) or t.device != ref.device:
         raise ValueError(f"{name} must be [{K}] or [G, {K}] on {ref.device} with a contiguous last dimension")
     if len(shape) == 1:
         return 1, K
@@ -702,56 +730,60 @@ def _groups(t: torch.Tensor, M: int, K: int, ref: torch.Tensor, name: str) -> Tu
     return G, (t.stride(0) if G > 1 else K)
 
 
-def _norm_struct(n: Norm, M: int, K: int, ref: torch.Tensor) -> _lib.NormStruct:
-    if n.kind not in _NORM_KIND:
+def _norm_struct(n: Norm, M: int, K: int, ref: torch.Tensor) -> bytes:
+    """The w8a8_norm_t of n for rows [M, K]."""
+    kind = _NORM_KIND.get(n.kind)
+    if kind is None:
         raise ValueError(f"kind must be 'rms' or 'layer', got {n.kind!r}")
-    s = _lib.NormStruct(kind=_NORM_KIND[n.kind], eps=n.eps)
-    for name, t in (("weight", n.weight), ("bias", n.bias)):
-        if t is not None:
-            if t.dim() != 1:
-                raise ValueError(f"{name} must be [{K}], got shape {tuple(t.shape)}")
-            _groups(t, M, K, ref, name)
-            setattr(s, name, t.data_ptr())
-            s.vec_dtype = _DTYPE[t.dtype]
-    if n.weight is not None and n.bias is not None and n.weight.dtype != n.bias.dtype:
-        raise TypeError("weight and bias must have one type")
-    for name, t in (("scale", n.scale), ("shift", n.shift)):
-        if t is not None:
-            G, ld = _groups(t, M, K, ref, name)
-            if s.groups not in (0, G):
+    weight = bias = scale = shift = ld_scale = ld_shift = vec = mod = 0
+    groups = 1
+    if n.weight is not None or n.bias is not None:
+        for name, t in (("weight", n.weight), ("bias", n.bias)):
+            if t is not None:
+                if t.dim() != 1:
+                    raise ValueError(f"{name} must be [{K}], got shape {tuple(t.shape)}")
+                _groups(t, M, K, ref, name)
+        if n.weight is not None:
+            weight, vec = n.weight.data_ptr(), _DTYPE[n.weight.dtype]
+        if n.bias is not None:
+            bias, kind_of = n.bias.data_ptr(), _DTYPE[n.bias.dtype]
+            if weight and kind_of != vec:
+                raise TypeError("weight and bias must have one type")
+            vec = kind_of
+    if n.scale is not None:
+        groups, ld_scale = _groups(n.scale, M, K, ref, "scale")
+        scale, mod = n.scale.data_ptr(), _DTYPE[n.scale.dtype]
+    if n.shift is not None:
+        G, ld_shift = _groups(n.shift, M, K, ref, "shift")
+        if n.scale is not None:
+            if G != groups:
                 raise ValueError("scale and shift must have the same number of rows")
-            s.groups = G
-            setattr(s, name, t.data_ptr())
-            setattr(s, "ld_" + name, ld)
-            s.mod_dtype = _DTYPE[t.dtype]
-    if n.scale is not None and n.shift is not None and n.scale.dtype != n.shift.dtype:
-        raise TypeError("scale and shift must have one type")
-    return s
+            if n.scale.dtype != n.shift.dtype:
+                raise TypeError("scale and shift must have one type")
+        groups, shift, mod = G, n.shift.data_ptr(), _DTYPE[n.shift.dtype]
+    return _lib.NORM_STRUCT.pack(kind, n.eps, weight, bias, scale, shift, ld_scale, ld_shift, groups, vec, mod)
 
 
 def _norm_out(M: int, K: int, act: torch.dtype, kind: int, device):
-    """(out, scales or None) of a norm."""
+    """(out, its leading dimension, scales or None) of a norm."""
     if kind == _lib.W8A8_NORM_OUT_16:
-        return torch.empty((M, K), dtype=act, device=device), None
-    codes = torch.empty((M, _round_up(K, 16)), dtype=_CODE_TYPE[kind], device=device)[:, :K]
-    return codes, torch.empty((M,), dtype=torch.float32, device=device)
+        return torch.empty((M, K), dtype=act, device=device), K, None
+    ld = _round_up(K, 16)
+    codes = torch.empty((M, ld), dtype=_CODE_TYPE[kind], device=device)
+    return codes if ld == K else codes[:, :K], ld, torch.empty((M,), dtype=torch.float32, device=device)
 
 
 def _norm_call(x: torch.Tensor, norm: Norm, kind: int, out_dtype: Optional[torch.dtype]):
-    if x.dtype not in _DTYPE:
-        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    _matrix(x, "x", x.dtype)
+    t = _float_rows(x, "x")
     if out_dtype is None:
-        out_dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
-    if out_dtype not in _ACT_ENTRY or (x.dtype != torch.float32 and out_dtype != x.dtype):
-        raise TypeError(f"out_dtype must be {'bfloat16 or float16' if x.dtype == torch.float32 else x.dtype}")
+        out_dtype = torch.bfloat16 if t == _lib.W8A8_T_F32 else x.dtype
+    elif out_dtype not in _ACT_ENTRY or (t != _lib.W8A8_T_F32 and out_dtype != x.dtype):
+        raise TypeError(f"out_dtype must be {'bfloat16 or float16' if t == _lib.W8A8_T_F32 else x.dtype}")
     M, K = x.shape
     n = _norm_struct(norm, M, K, x)
-    out, scales = _norm_out(M, K, out_dtype, kind, x.device)
-    with torch.cuda.device(x.device):
-        call("norm_rows", x.data_ptr(), _DTYPE[x.dtype], M, K, _ld(x), ctypes.byref(n), _DTYPE[out_dtype], kind,
-             out.data_ptr(), _ldp(out) if scales is not None else _ld(out),
-             None if scales is None else scales.data_ptr(), _stream(x))
+    out, ld, scales = _norm_out(M, K, out_dtype, kind, x.device)
+    _run(x, "norm_rows", x.data_ptr(), t, M, K, _ld(x), n, _DTYPE[out_dtype], kind, out.data_ptr(), ld,
+         None if scales is None else scales.data_ptr())
     return out, scales
 
 
@@ -776,36 +808,38 @@ def _residual_call(x: torch.Tensor, y: torch.Tensor, norm: Optional[Norm], kind:
                    gate: Optional[torch.Tensor], post: Optional[Norm], residual_scale: float,
                    branch_scale: float, out: Optional[torch.Tensor]):
     _matrix(y, "y", _act_dtype(y))
-    if x.dtype not in (y.dtype, torch.float32):
+    if x.dtype != y.dtype and x.dtype != torch.float32:
         raise TypeError(f"x must be {y.dtype} (y's type) or float32, got {x.dtype}")
     _matrix(x, "x", x.dtype)
     M, K = x.shape
     if y.shape != (M, K):
         raise ValueError(f"y must have shape {(M, K)}, got {tuple(y.shape)}")
-    r = torch.empty((M, K), dtype=x.dtype, device=x.device) if out is None else out
-    _matrix(r, "out", x.dtype)
-    if r.shape != (M, K):
-        raise ValueError(f"out must have shape {(M, K)}")
-    _same_device(x, y, r)
-    s = _lib.ResidualStruct(x=x.data_ptr(), y=y.data_ptr(), r=r.data_ptr(), ldx=_ld(x), ldy=_ld(y), ldr=_ld(r),
-                            residual_scale=residual_scale, branch_scale=branch_scale, x_dtype=_DTYPE[x.dtype],
-                            y_dtype=_DTYPE[y.dtype])
+    _same_device(x, y)
+    if out is None:
+        r = torch.empty((M, K), dtype=x.dtype, device=x.device)
+    else:
+        r = _matrix(out, "out", x.dtype)
+        if r.shape != (M, K):
+            raise ValueError(f"out must have shape {(M, K)}")
+        _same_device(x, r)
+    groups, ld_gate, gate_ptr, gate_dtype = 1, 0, 0, 0
     if gate is not None:
-        s.gate_groups, s.ld_gate = _groups(gate, M, K, x, "gate")
-        s.gate, s.gate_dtype = gate.data_ptr(), _DTYPE[gate.dtype]
+        groups, ld_gate = _groups(gate, M, K, x, "gate")
+        gate_ptr, gate_dtype = gate.data_ptr(), _DTYPE[gate.dtype]
+    p = n = None
     if post is not None:
         if post.scale is not None or post.shift is not None:
             raise ValueError("post takes no scale or shift: the gate multiplies its result")
         p = _norm_struct(post, M, K, x)
-        s.post = ctypes.pointer(p)
-    n, h, hs = None, None, None
+    h, ld, hs = None, 0, None
     if norm is not None:
         n = _norm_struct(norm, M, K, x)
-        h, hs = _norm_out(M, K, y.dtype, kind, x.device)
-    with torch.cuda.device(x.device):
-        call("gated_residual_rows", ctypes.byref(s), M, K, None if n is None else ctypes.byref(n), kind,
-             None if h is None else h.data_ptr(), 0 if h is None else _ldp(h) if hs is not None else _ld(h),
-             None if hs is None else hs.data_ptr(), _stream(x))
+        h, ld, hs = _norm_out(M, K, y.dtype, kind, x.device)
+    res = _lib.RESIDUAL_STRUCT.pack(x.data_ptr(), y.data_ptr(), r.data_ptr(), _ld(x), _ld(y), _ld(r), gate_ptr,
+                                    ld_gate, groups, residual_scale, branch_scale, _DTYPE[x.dtype],
+                                    _DTYPE[y.dtype], gate_dtype)
+    _run(x, "gated_residual_rows", res, p, M, K, n, kind, None if h is None else h.data_ptr(), ld,
+         None if hs is None else hs.data_ptr())
     return r, h, hs
 
 
