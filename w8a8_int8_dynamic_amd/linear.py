@@ -94,7 +94,7 @@ class W8A8Linear(torch.nn.Module):
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
         lead = x.shape[:-1]
-        x2 = x.reshape(-1, self.in_features)
+        x2 = x if x.dim() == 2 else x.reshape(-1, self.in_features)
         if x2.stride(-1) != 1:
             x2 = x2.contiguous()
         # The per-token quant and the scaled matmul, as one library call; the
@@ -108,7 +108,9 @@ class W8A8Linear(torch.nn.Module):
         elif self.scheme == "fp4":
             if x2.dtype not in (torch.bfloat16, torch.float16):
                 raise TypeError(f"the fp4 scheme takes bfloat16 or float16 activations, got {x2.dtype}")
-            out, _, _ = ops.fp4_quant_scaled_mm(x2, self.w_packed, self.w_scale, self.out_features, bias)
+            out = ops._fp4_linear(x2, self.w_packed, self.w_scale, self.out_features, bias)
+            if x2 is x:
+                return out
         else:
             wsp = self.workspace if x2.dtype == torch.bfloat16 else None
             out, _, _ = ops.quant_scaled_mm(x2, self.w_packed, self.w_scale, self.out_features,

@@ -464,11 +464,11 @@ def _fp4_k(K: int) -> int:
     return K
 
 
-def _scale_bytes(M: int, n: int, device) -> torch.Tensor:
+def _scale_bytes(M: int, n: int, ref: torch.Tensor) -> torch.Tensor:
     """uint8 [M, n] whose rows start on, and are readable to, 16-byte boundaries."""
     if n % 16 == 0:
-        return torch.empty((M, n), dtype=torch.uint8, device=device)
-    return torch.empty((M, _round_up(n, 16)), dtype=torch.uint8, device=device)[:, :n]
+        return ref.new_empty((M, n), dtype=torch.uint8)
+    return ref.new_empty((M, _round_up(n, 16)), dtype=torch.uint8)[:, :n]
 
 
 def _fp4_rows(xq: torch.Tensor, xs: torch.Tensor) -> Tuple[int, int]:
@@ -490,7 +490,7 @@ def _scale_rows(xs: torch.Tensor) -> torch.Tensor:
     if xs.data_ptr() % 16 == 0 and ld % 16 == 0 and ld >= n and \
             xs.untyped_storage().nbytes() - xs.storage_offset() >= M * ld:
         return xs
-    buf = _scale_bytes(M, n, xs.device)
+    buf = _scale_bytes(M, n, xs)
     buf.copy_(xs)
     return buf
 
@@ -500,13 +500,23 @@ def _ldp(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else _round_up(t.shape[1], 16)
 
 
-def _float_rows(x: torch.Tensor, name: str) -> int:
-    """The element type of rows x [M, K] of floats."""
+def _float_rows(x: torch.Tensor, name: str) -> Tuple[int, int, int, int]:
+    """(element type, M, K, row pitch) of rows x [M, K] of floats."""
     t = _DTYPE.get(x.dtype)
     if t is None:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
     _matrix(x, name, x.dtype)
-    return t
+    M, K = x.shape
+    return t, M, K, (x.stride(0) if M > 1 else K)
+
+
+def _vector_rows(x: torch.Tensor, t: int, ld: int) -> Tuple[torch.Tensor, int]:
+    """x and its pitch as _rows_aligned gives them: rows on 16-byte boundaries."""
+    step = 4 if t == _lib.W8A8_T_F32 else 8
+    if x.data_ptr() % 16 == 0 and ld % step == 0:
+        return x, ld
+    x = _rows_aligned(x, step)
+    return x, _ld(x)
 
 
 def fp4_quant_per_block(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
@@ -514,18 +524,17 @@ def fp4_quant_per_block(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
     """MX FP4 quantization of bf16, fp16 or fp32 x [M, K] (K a multiple of 32):
     (uint8 codes [M, K/2], the even element in the low nibble; uint8 scale
     bytes [M, K/32], one power of two per 32 elements)."""
-    t = _float_rows(x, "x")
-    M, K = x.shape
+    t, M, K, ld = _float_rows(x, "x")
     _fp4_k(K)
-    x = _rows_aligned(x, 4 if t == _lib.W8A8_T_F32 else 8)
+    x, ld = _vector_rows(x, t, ld)
     own = xq is None and xs is None
-    xq = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device) if xq is None else xq
-    xs = _scale_bytes(M, K // _FP4_BLOCK, x.device) if xs is None else xs
+    xq = x.new_empty((M, K // 2), dtype=torch.uint8) if xq is None else xq
+    xs = _scale_bytes(M, K // _FP4_BLOCK, x) if xs is None else xs
     if not own:
         if _fp4_rows(xq, xs) != (M, K):
             raise ValueError(f"xq must have shape {(M, K // 2)}")
         _same_device(x, xq)
-    _run(x, "fp4_quant_per_block", x.data_ptr(), t, M, K, _ld(x), xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs))
+    _run(x, "fp4_quant_per_block", x.data_ptr(), t, M, K, ld, xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs))
     return xq, xs
 
 
@@ -537,7 +546,7 @@ def fp4_dequant(xq: torch.Tensor, xs: torch.Tensor, dtype: torch.dtype = torch.b
     M, K = _fp4_rows(xq, xs)
     if xq.data_ptr() % 4 != 0 or _ld(xq) % 4 != 0:
         xq = _rows_aligned(xq, 16)
-    out = torch.empty((M, K), dtype=dtype, device=xq.device)
+    out = xq.new_empty((M, K), dtype=dtype)
     _run(xq, "fp4_dequant", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), M, K, _DTYPE[dtype], out.data_ptr(), K)
     return out
 
@@ -557,12 +566,15 @@ def _check_fp4_packed(w_packed: torch.Tensor, s_packed: torch.Tensor, N: int, K:
     if N < 1:
         raise ValueError(f"N must be at least 1, got {N}")
     rows = _round_up(N, 16)
-    for t, n, name in ((w_packed, rows * _round_up(K, 128) // 2, "w_packed"),
-                       (s_packed, rows * _round_up(K, 512) // _FP4_BLOCK, "s_packed")):
-        if t.dtype != torch.uint8 or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"{name} must be a uint8 device buffer of the packed layout (N, K)")
-        if t.get_device() != ref.get_device():
-            raise ValueError(f"all tensors must be on {ref.device}, got one on {t.device}")
+
+    def fits(t: torch.Tensor, n: int) -> bool:
+        return t.dtype == torch.uint8 and t.numel() >= n and t.is_contiguous() and t.is_cuda
+
+    if not fits(w_packed, rows * _round_up(K, 128) // 2) or not fits(s_packed, rows * _round_up(K, 512) // _FP4_BLOCK):
+        raise ValueError("w_packed and s_packed must be uint8 device buffers of the packed layout (N, K)")
+    device = ref.get_device()
+    if w_packed.get_device() != device or s_packed.get_device() != device:
+        raise ValueError(f"all tensors must be on {ref.device}")
 
 
 def fp4_prepack_weight(wq: torch.Tensor, ws: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -612,7 +624,7 @@ def _fp4_out(M: int, N: int, bias, out_dtype, out, x: torch.Tensor):
         _vector(bias, N, "bias", out_dtype)
         _same_device(x, bias)
     if out is None:
-        return mode, torch.empty((M, N), dtype=out_dtype, device=x.device)
+        return mode, x.new_empty((M, N), dtype=out_dtype)
     _matrix(out, "out", out_dtype)
     if out.shape != (M, N):
         raise ValueError(f"out must have shape {(M, N)}")
@@ -642,20 +654,38 @@ def fp4_quant_scaled_mm(x: torch.Tensor, w_packed: torch.Tensor, s_packed: torch
                         ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """fp4_quant_per_block of x [M, K] and fp4_scaled_mm in one call: (out, xq,
     xs). out_dtype defaults to x's type, bf16 for fp32 x."""
-    t = _float_rows(x, "x")
-    M, K = x.shape
+    t, M, K, ld = _float_rows(x, "x")
     _fp4_k(K)
     if out_dtype is None:
         out_dtype = torch.bfloat16 if t == _lib.W8A8_T_F32 else x.dtype
     _check_fp4_packed(w_packed, s_packed, N, K, x)
     mode, out = _fp4_out(M, N, bias, out_dtype, out, x)
-    x = _rows_aligned(x, 4 if t == _lib.W8A8_T_F32 else 8)
-    xq = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-    xs = _scale_bytes(M, K // _FP4_BLOCK, x.device)
-    _run(x, "fp4_quant_scaled_mm_tile", x.data_ptr(), t, _ld(x), xq.data_ptr(), _ldp(xq), xs.data_ptr(), _ldp(xs),
+    x, ld = _vector_rows(x, t, ld)
+    xq = x.new_empty((M, K // 2), dtype=torch.uint8)
+    xs = _scale_bytes(M, K // _FP4_BLOCK, x)
+    _run(x, "fp4_quant_scaled_mm_tile", x.data_ptr(), t, ld, xq.data_ptr(), K // 2, xs.data_ptr(), _ldp(xs),
          w_packed.data_ptr(), s_packed.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, mode,
          out.data_ptr(), _ld(out), tile=(tile,))
     return out, xq, xs
+
+
+def _fp4_linear(x: torch.Tensor, w_packed: torch.Tensor, s_packed: torch.Tensor, N: int,
+                bias: Optional[torch.Tensor]) -> torch.Tensor:
+    """fp4_quant_scaled_mm's out alone, for a layer (which has no use for the codes:
+    they go through one buffer)."""
+    t, M, K, ld = _float_rows(x, "x")
+    _check_fp4_packed(w_packed, s_packed, N, K, x)
+    if bias is not None:
+        _same_device(x, bias)
+    x, ld = _vector_rows(x, t, ld)
+    out = x.new_empty((M, N))
+    lds = _round_up(K // _FP4_BLOCK, 16)
+    xq = x.new_empty((M * (K // 2 + lds),), dtype=torch.uint8)
+    at = xq.data_ptr()
+    _run(x, "fp4_quant_scaled_mm", x.data_ptr(), t, ld, at, K // 2, at + M * (K // 2), lds, w_packed.data_ptr(),
+         s_packed.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, _OUT_MODE[x.dtype],
+         out.data_ptr(), N)
+    return out
 
 
 def fp4_tile_count() -> int:
@@ -764,25 +794,24 @@ def _norm_struct(n: Norm, M: int, K: int, ref: torch.Tensor) -> bytes:
     return _lib.NORM_STRUCT.pack(kind, n.eps, weight, bias, scale, shift, ld_scale, ld_shift, groups, vec, mod)
 
 
-def _norm_out(M: int, K: int, act: torch.dtype, kind: int, device):
+def _norm_out(M: int, K: int, act: torch.dtype, kind: int, x: torch.Tensor):
     """(out, its leading dimension, scales or None) of a norm."""
     if kind == _lib.W8A8_NORM_OUT_16:
-        return torch.empty((M, K), dtype=act, device=device), K, None
+        return x.new_empty((M, K), dtype=act), K, None
     ld = _round_up(K, 16)
-    codes = torch.empty((M, ld), dtype=_CODE_TYPE[kind], device=device)
-    return codes if ld == K else codes[:, :K], ld, torch.empty((M,), dtype=torch.float32, device=device)
+    codes = x.new_empty((M, ld), dtype=_CODE_TYPE[kind])
+    return codes if ld == K else codes[:, :K], ld, x.new_empty((M,), dtype=torch.float32)
 
 
 def _norm_call(x: torch.Tensor, norm: Norm, kind: int, out_dtype: Optional[torch.dtype]):
-    t = _float_rows(x, "x")
+    t, M, K, ldx = _float_rows(x, "x")
     if out_dtype is None:
         out_dtype = torch.bfloat16 if t == _lib.W8A8_T_F32 else x.dtype
     elif out_dtype not in _ACT_ENTRY or (t != _lib.W8A8_T_F32 and out_dtype != x.dtype):
         raise TypeError(f"out_dtype must be {'bfloat16 or float16' if t == _lib.W8A8_T_F32 else x.dtype}")
-    M, K = x.shape
     n = _norm_struct(norm, M, K, x)
-    out, ld, scales = _norm_out(M, K, out_dtype, kind, x.device)
-    _run(x, "norm_rows", x.data_ptr(), t, M, K, _ld(x), n, _DTYPE[out_dtype], kind, out.data_ptr(), ld,
+    out, ld, scales = _norm_out(M, K, out_dtype, kind, x)
+    _run(x, "norm_rows", x.data_ptr(), t, M, K, ldx, n, _DTYPE[out_dtype], kind, out.data_ptr(), ld,
          None if scales is None else scales.data_ptr())
     return out, scales
 
@@ -816,7 +845,7 @@ def _residual_call(x: torch.Tensor, y: torch.Tensor, norm: Optional[Norm], kind:
         raise ValueError(f"y must have shape {(M, K)}, got {tuple(y.shape)}")
     _same_device(x, y)
     if out is None:
-        r = torch.empty((M, K), dtype=x.dtype, device=x.device)
+        r = x.new_empty((M, K))
     else:
         r = _matrix(out, "out", x.dtype)
         if r.shape != (M, K):
@@ -834,7 +863,7 @@ def _residual_call(x: torch.Tensor, y: torch.Tensor, norm: Optional[Norm], kind:
     h, ld, hs = None, 0, None
     if norm is not None:
         n = _norm_struct(norm, M, K, x)
-        h, ld, hs = _norm_out(M, K, y.dtype, kind, x.device)
+        h, ld, hs = _norm_out(M, K, y.dtype, kind, x)
     res = _lib.RESIDUAL_STRUCT.pack(x.data_ptr(), y.data_ptr(), r.data_ptr(), _ld(x), _ld(y), _ld(r), gate_ptr,
                                     ld_gate, groups, residual_scale, branch_scale, _DTYPE[x.dtype],
                                     _DTYPE[y.dtype], gate_dtype)
