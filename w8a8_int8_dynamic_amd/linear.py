@@ -108,7 +108,8 @@ class W8A8Linear(torch.nn.Module):
         elif self.scheme == "fp4":
             if x2.dtype not in (torch.bfloat16, torch.float16):
                 raise TypeError(f"the fp4 scheme takes bfloat16 or float16 activations, got {x2.dtype}")
-            out = ops._fp4_linear(x2, self.w_packed, self.w_scale, self.out_features, bias)
+            b = self._buffers
+            out = ops._fp4_linear(x2, b["w_packed"], b["w_scale"], self.out_features, bias)
             if x2 is x:
                 return out
         else:

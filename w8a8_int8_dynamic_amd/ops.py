@@ -438,6 +438,8 @@ def fp8_quant_scaled_mm(x: torch.Tensor, w_packed: torch.Tensor, ws: Optional[to
 _DTYPE = {torch.bfloat16: _lib.W8A8_T_BF16, torch.float16: _lib.W8A8_T_F16, torch.float32: _lib.W8A8_T_F32}
 _FP4_BLOCK = 32
 _entry = {}
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _run(x: torch.Tensor, name: str, *args, tile: Tuple[int, ...] = ()) -> None:
@@ -449,12 +451,12 @@ def _run(x: torch.Tensor, name: str, *args, tile: Tuple[int, ...] = ()) -> None:
     if fn is None:
         fn = _entry[name] = getattr(_lib.lib(), name)
     device = x.get_device()
-    if device == torch.cuda.current_device():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device), *tile)
+    if device == _current_device():
+        rc = fn(*args, _raw_stream(device), *tile)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device), *tile)
-    if rc != _lib.W8A8_OK:
+            rc = fn(*args, _raw_stream(device), *tile)
+    if rc:
         raise _lib.W8A8Error(rc, name, _lib.last_error())
 
 
@@ -475,10 +477,12 @@ def _fp4_rows(xq: torch.Tensor, xs: torch.Tensor) -> Tuple[int, int]:
     """(M, K) of 4-bit codes [M, K/2] and their scale bytes [M, K/32]."""
     _matrix(xq, "xq", torch.uint8)
     _matrix(xs, "xs", torch.uint8)
-    M, K = xq.shape[0], _fp4_k(2 * xq.shape[1])
+    M, half = xq.shape
+    K = _fp4_k(2 * half)
     if xs.shape != (M, K // _FP4_BLOCK):
         raise ValueError(f"xs must have shape {(M, K // _FP4_BLOCK)}, got {tuple(xs.shape)}")
-    _same_device(xq, xs)
+    if xs.get_device() != xq.get_device():
+        _same_device(xq, xs)
     return M, K
 
 
@@ -505,9 +509,13 @@ def _float_rows(x: torch.Tensor, name: str) -> Tuple[int, int, int, int]:
     t = _DTYPE.get(x.dtype)
     if t is None:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
-    _matrix(x, name, x.dtype)
+    if not x.is_cuda or x.dim() != 2:
+        _matrix(x, name, x.dtype)
     M, K = x.shape
-    return t, M, K, (x.stride(0) if M > 1 else K)
+    ld, step = x.stride()
+    if step != 1 and K > 1:
+        _matrix(x, name, x.dtype)
+    return t, M, K, (ld if M > 1 else K)
 
 
 def _vector_rows(x: torch.Tensor, t: int, ld: int) -> Tuple[torch.Tensor, int]:
@@ -527,14 +535,16 @@ def fp4_quant_per_block(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
     t, M, K, ld = _float_rows(x, "x")
     _fp4_k(K)
     x, ld = _vector_rows(x, t, ld)
+    ldq, lds = K // 2, _round_up(K // _FP4_BLOCK, 16)
     own = xq is None and xs is None
-    xq = x.new_empty((M, K // 2), dtype=torch.uint8) if xq is None else xq
+    xq = x.new_empty((M, ldq), dtype=torch.uint8) if xq is None else xq
     xs = _scale_bytes(M, K // _FP4_BLOCK, x) if xs is None else xs
     if not own:
         if _fp4_rows(xq, xs) != (M, K):
             raise ValueError(f"xq must have shape {(M, K // 2)}")
         _same_device(x, xq)
-    _run(x, "fp4_quant_per_block", x.data_ptr(), t, M, K, ld, xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs))
+        ldq, lds = _ld(xq), _ld(xs)
+    _run(x, "fp4_quant_per_block", x.data_ptr(), t, M, K, ld, xq.data_ptr(), ldq, xs.data_ptr(), lds)
     return xq, xs
 
 
@@ -750,7 +760,8 @@ def _groups(t: torch.Tensor, M: int, K: int, ref: torch.Tensor, name: str) -> Tu
     if t.dtype not in _DTYPE:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
     shape = t.shape
-    if len(shape) not in (1, 2) or shape[-1] != K or (K > 1 and t.stride(-1) != 1) or t.device != ref.device:
+    if len(shape) not in (1, 2) or shape[-1] != K or (K > 1 and t.stride(-1) != 1) or \
+            t.get_device() != ref.get_device():
         raise ValueError(f"{name} must be [{K}] or [G, {K}] on {ref.device} with a contiguous last dimension")
     if len(shape) == 1:
         return 1, K
@@ -839,18 +850,19 @@ def _residual_call(x: torch.Tensor, y: torch.Tensor, norm: Optional[Norm], kind:
     _matrix(y, "y", _act_dtype(y))
     if x.dtype != y.dtype and x.dtype != torch.float32:
         raise TypeError(f"x must be {y.dtype} (y's type) or float32, got {x.dtype}")
-    _matrix(x, "x", x.dtype)
-    M, K = x.shape
+    t, M, K, ldx = _float_rows(x, "x")
     if y.shape != (M, K):
         raise ValueError(f"y must have shape {(M, K)}, got {tuple(y.shape)}")
-    _same_device(x, y)
+    if y.get_device() != x.get_device():
+        _same_device(x, y)
     if out is None:
-        r = x.new_empty((M, K))
+        r, ldr = x.new_empty((M, K)), K
     else:
         r = _matrix(out, "out", x.dtype)
         if r.shape != (M, K):
             raise ValueError(f"out must have shape {(M, K)}")
         _same_device(x, r)
+        ldr = _ld(r)
     groups, ld_gate, gate_ptr, gate_dtype = 1, 0, 0, 0
     if gate is not None:
         groups, ld_gate = _groups(gate, M, K, x, "gate")
@@ -864,9 +876,9 @@ def _residual_call(x: torch.Tensor, y: torch.Tensor, norm: Optional[Norm], kind:
     if norm is not None:
         n = _norm_struct(norm, M, K, x)
         h, ld, hs = _norm_out(M, K, y.dtype, kind, x)
-    res = _lib.RESIDUAL_STRUCT.pack(x.data_ptr(), y.data_ptr(), r.data_ptr(), _ld(x), _ld(y), _ld(r), gate_ptr,
-                                    ld_gate, groups, residual_scale, branch_scale, _DTYPE[x.dtype],
-                                    _DTYPE[y.dtype], gate_dtype)
+    res = _lib.RESIDUAL_STRUCT.pack(x.data_ptr(), y.data_ptr(), r.data_ptr(), ldx, y.stride(0) if M > 1 else K, ldr,
+                                    gate_ptr, ld_gate, groups, residual_scale, branch_scale, t, _DTYPE[y.dtype],
+                                    gate_dtype)
     _run(x, "gated_residual_rows", res, p, M, K, n, kind, None if h is None else h.data_ptr(), ld,
          None if hs is None else hs.data_ptr())
     return r, h, hs
