@@ -313,3 +313,84 @@ def test_other_stream_and_graph(ops, m):
         torch.cuda.synchronize()
         assert torch.equal(out, want[i]), i
         assert torch.equal(ops.fp4_quant_scaled_mm(xs[i], *packed, n)[0], want[i])
+
+
+@pytest.mark.parametrize("m", [2, 40])
+def test_longest_k(ops, m):
+    """The largest K: every tile's chunk and block offsets at their limits."""
+    n, k = 24, ops._lib.W8A8_FP4_MAX_K
+    xq, xs = codes(m, k, 1)
+    wq, ws = codes(n, k, 2)
+    exact, mag = ref.product(ref.dequant(xq, xs), ref.dequant(wq, ws))
+    packed = ops.fp4_prepack_weight(dev(wq), dev(ws))
+    for tile in range(-1, ops.fp4_tile_count()):
+        got = ops.fp4_scaled_mm(dev(xq), dev(xs), *packed, n, tile=tile)
+        check(got, exact, mag, k, torch.bfloat16, what=f"tile {tile}")
+    x = rows(m, k, 3)
+    out, q, s = ops.fp4_quant_scaled_mm(x.to(DEV), *packed, n)
+    want = ref.quant(x.double().numpy())
+    assert np.array_equal(q.cpu().numpy(), want[0]) and np.array_equal(s.cpu().numpy(), want[1])
+    exact, mag = ref.product(ref.dequant(*want), ref.dequant(wq, ws))
+    check(out, exact, mag, k, torch.bfloat16, what="quant")
+
+
+def test_offsets_past_32_bits(ops):
+    """Rows whose pitch puts the last of them billions of elements behind the
+    first: rows of floats, codes, scales and outputs."""
+    k, n = 544, 40
+    wq, ws = codes(n, k, 2)
+    packed = ops.fp4_prepack_weight(dev(wq), dev(ws))
+    m, pitch = 5, (1 << 30) + 64
+    x = rows(m, k, 3)
+    big = torch.empty(m * pitch, dtype=torch.bfloat16, device=DEV)
+    wide = big.as_strided((m, k), (pitch, 1))
+    wide.copy_(x)
+    want = ref.quant(x.double().numpy())
+    exact, mag = ref.product(ref.dequant(*want), ref.dequant(wq, ws))
+    for tile in range(-1, ops.fp4_tile_count()):
+        out = big.as_strided((m, n), (pitch, 1), 4096)
+        _, q, s = ops.fp4_quant_scaled_mm(wide, *packed, n, out=out, tile=tile)
+        assert np.array_equal(q.cpu().numpy(), want[0]) and np.array_equal(s.cpu().numpy(), want[1])
+        check(out, exact, mag, k, torch.bfloat16, what=f"tile {tile}")
+    del big, wide, out
+    # codes and scales at the largest pitch the product takes, past 2^32 bytes
+    m, pitch = 1030, ops._lib.W8A8_MAX_LDQ
+    xq, xs = codes(m, k, 5)
+    bytes_ = torch.empty(m * pitch, dtype=torch.uint8, device=DEV)
+    q, s = bytes_.as_strided((m, k // 2), (pitch, 1)), bytes_.as_strided((m, k // 32), (pitch, 1), 1024)
+    q.copy_(dev(xq))
+    s.copy_(dev(xs))
+    exact, mag = ref.product(ref.dequant(xq, xs), ref.dequant(wq, ws))
+    for tile in range(-1, ops.fp4_tile_count()):
+        check(ops.fp4_scaled_mm(q, s, *packed, n, tile=tile), exact, mag, k, torch.bfloat16, what=f"tile {tile}")
+    assert np.array_equal(ops.fp4_dequant(q, s, torch.float32).cpu().numpy(), ref.dequant(xq, xs).astype(np.float32))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 20, 16384), (1, 20, 16416), (2, 20, 8192), (2, 20, 8224), (3, 40, 4096),
+                                   (4, 40, 4096), (4, 40, 4128), (5, 40, 4096)])
+def test_quant_inside_the_product_and_beside_it(ops, m, n, k):
+    """Either side of where the rows are too many to be quantized in the same
+    launch."""
+    x = rows(m, k, m + k)
+    wq, ws = codes(n, k, 5)
+    packed = ops.fp4_prepack_weight(dev(wq), dev(ws))
+    want = ref.quant(x.double().numpy())
+    exact, mag = ref.product(ref.dequant(*want), ref.dequant(wq, ws))
+    for dtype in (torch.bfloat16, torch.float32):
+        out, q, s = ops.fp4_quant_scaled_mm(x.to(dtype).to(DEV), *packed, n)
+        assert np.array_equal(q.cpu().numpy(), want[0]) and np.array_equal(s.cpu().numpy(), want[1])
+        check(out, exact, mag, k, torch.bfloat16)
+
+
+def test_rows_that_hold_nan_next_to_others(ops):
+    """A NaN or infinity reaches the outputs of its row alone, quantized in the
+    product's launch or before it; a row of zeros gives the bias."""
+    n, k = 33, 1056
+    packed = ops.fp4_quant_prepack_weight(rows(n, k, 1).to(DEV))
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    for m in (4, 24):
+        x = rows(m, k, 2)
+        x[0, 7], x[2, k - 1], x[3] = float("nan"), float("inf"), 0
+        out, _, s = ops.fp4_quant_scaled_mm(x.to(DEV), *packed, n, bias)
+        assert torch.isnan(out[0]).all() and torch.isnan(out[2]).all() and torch.isfinite(out[1]).all()
+        assert torch.equal(out[3], bias) and s[0, 0] == 255 and s[2, -1] == 255 and (s[3] == 0).all()

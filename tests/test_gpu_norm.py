@@ -249,3 +249,59 @@ def test_other_stream_and_graph(ops):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
         assert all(torch.equal(a, b) for a, b in zip(call(xs[i]), want[i]))
+
+
+@pytest.mark.parametrize("m,k", [(515, 4096), (600, 3000), (520, 8192), (513, 6000), (1100, 12288), (2050, 2048),
+                                 (1030, 1500), (300, 16384), (1025, 16000)])
+def test_many_wide_rows(ops, m, k):
+    """Runs of several rows per workgroup in every row shape, whole and ragged,
+    with groups that end inside a run."""
+    groups = 5 if m % 5 == 0 else None
+    x, y = rows(m, k, m), rows(m, k, m + 1)
+    v = {"scale": vec(k, 3, F32, groups=groups), "shift": vec(k, 4, F32, 0.5, groups=groups)}
+    z = torch.zeros(m, k, device=DEV, dtype=torch.float64)
+    for kind in ("rms", "layer"):
+        want, bound = ref.norm(x.double(), z, kind, 1e-6, **v)
+        n = ops.Norm(kind, **v)
+        for out in ("same", "int8", "fp8"):
+            check_norm(ops, run_norm(ops, x, n, out), want, bound, BF, out, f"{kind} {out}")
+    post = {"kind": "rms", "eps": 1e-6, "weight": vec(k, 6, BF, 1.0)}
+    gate = vec(k, 5, BF, groups=groups, spread=0.7)
+    r, err = ref.residual(x, y, gate=gate, post=post)
+    h, h_err = ref.norm(r, err, "layer", 1e-6, **v)
+    got_r, got_h = ops.gated_residual_norm(x, y, ops.Norm("layer", **v), gate=gate, post=ops.Norm(**post))
+    ref.check_float(got_r, r, err, BF, "r")
+    ref.check_float(got_h, h, h_err, BF, "h")
+    assert torch.equal(ops.gated_residual(x, y, gate=gate, post=ops.Norm(**post)), got_r)
+
+
+@pytest.mark.parametrize("k", [104, 33000])
+def test_offsets_past_32_bits(ops, k):
+    """Rows, modulation vectors and outputs billions of elements apart."""
+    m, pitch = 5, (1 << 30) + 7
+    big = torch.empty(m * pitch, dtype=BF, device=DEV)
+    x, y = rows(m, k, 1), rows(m, k, 2)
+    at = lambda i: big.as_strided((m, k), (pitch, 1), i * 40000)  # noqa: E731
+    wx, wy, mod, out = (at(i) for i in range(4))
+    wx.copy_(x)
+    wy.copy_(y)
+    mod.copy_(vec(k, 3, BF, groups=m))
+    n = ops.Norm("layer", scale=mod, shift=mod)
+    small = ops.Norm("layer", scale=mod.contiguous(), shift=mod.contiguous())
+    assert torch.equal(ops.norm(wx, n), ops.norm(x, small))
+    got = ops.gated_residual_norm_quant(wx, wy, n, gate=mod, out=out)
+    want = ops.gated_residual_norm_quant(x, y, small, gate=mod.contiguous())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_rows_one_vector_each(ops):
+    """As many groups as rows, and a gate that is one row for all."""
+    m, k = 40, 520
+    x, y = rows(m, k, 1, F32), rows(m, k, 2)
+    v = {"scale": vec(k, 3, HF, groups=m), "shift": vec(k, 4, HF, 0.3, groups=m)}
+    gate = vec(k, 5, F32, groups=1)
+    r, err = ref.residual(x, y, gate=gate, residual_scale=0.5)
+    h, h_err = ref.norm(r, err, "rms", 1e-6, **v)
+    got_r, *codes = ops.gated_residual_norm_quant(x, y, ops.Norm("rms", **v), gate=gate, residual_scale=0.5)
+    ref.check_float(got_r, r, err, F32, "r")
+    ref.check_codes(*codes, h, h_err, 127, "codes")
