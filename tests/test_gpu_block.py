@@ -124,3 +124,41 @@ def test_calls_at_once_on_two_streams():
     for i in range(2):
         for r in got[i]:
             assert all(torch.equal(u, v) for u, v in zip(r, want[i]))
+
+
+@pytest.mark.parametrize("scheme", ["int8", "fp8", "fp4"])
+@pytest.mark.parametrize("m", [1, 70])
+def test_forward_quantized(scheme, m):
+    """A layer on codes made beside it is the layer on the floats, in both
+    output types; several streams at once give what one gives."""
+    from w8a8_int8_dynamic_amd import W8A8Linear, ops
+    n, k = 200, 1056
+    g = torch.Generator().manual_seed(3)
+    lin = W8A8Linear.from_float((0.05 * torch.randn(n, k, generator=g)).to(DEV),
+                                torch.randn(n, generator=g).to(DEV), scheme=scheme)
+    quant = {"int8": ops.quant_per_token, "fp8": ops.fp8_quant_per_token, "fp4": ops.fp4_quant_per_block}[scheme]
+    for dtype in (torch.bfloat16, torch.float16):
+        if scheme == "fp8" and dtype == torch.float16:
+            continue
+        x = torch.randn(m, k, generator=g).to(dtype).to(DEV)
+        assert torch.equal(lin.forward_quantized(*quant(x), out_dtype=dtype), lin(x))
+    codes = quant(torch.randn(m, k, generator=g).bfloat16().to(DEV))
+    want = lin.forward_quantized(*codes)
+    half = lin.forward_quantized(*codes, out_dtype=torch.float16)
+    # one sum rounded to either type (bias too): each within its half steps
+    top = want.float().abs().max().item()
+    assert (want.float() - half.float()).abs().max().item() <= top * (2 ** -7 + 2 ** -10) + 4 * (2 ** -8 + 2 ** -11)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(6):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(lin.forward_quantized(*codes))
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want) for t in got)
+    for bad in ((codes[0][:, :-16], codes[1]), (codes[0].cpu(), codes[1])):
+        with pytest.raises((ValueError, TypeError)):
+            lin.forward_quantized(*bad)
+    with pytest.raises(TypeError):
+        lin.forward_quantized(*codes, out_dtype=torch.float32)

@@ -65,7 +65,8 @@ class W8A8Linear(torch.nn.Module):
         if scheme == "fp4":
             if (w_scale == 255).any():
                 raise ValueError("weight scales must be finite")
-            return cls(*ops.fp4_prepack_weight(wq, w_scale), N, 2 * K, bias, scheme)
+            packed = ops.fp4_prepack_weight(wq.contiguous(), w_scale.contiguous())
+            return cls(*packed, N, 2 * K, bias, scheme)
         if not torch.isfinite(w_scale).all():
             raise ValueError("weight scales must be finite")
         packed = ops.prepack_weight(wq.contiguous())
@@ -123,7 +124,8 @@ class W8A8Linear(torch.nn.Module):
         """The layer's product alone, for activations quantized elsewhere (by the
         ops that end in quant_per_token for "int8" and "fp8", by
         fp4_quant_per_block for "fp4"): codes [M, K] (fp4: [M, K/2]) and their
-        scales to [M, N] in out_dtype (bf16 or fp16)."""
+        scales to [M, N] in out_dtype (bf16 or fp16). It uses no workspace of the
+        layer, so calls on several streams may run at once."""
         if out_dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"out_dtype must be bfloat16 or float16, got {out_dtype}")
         K = xq.shape[-1] * (2 if self.scheme == "fp4" else 1)
@@ -134,8 +136,7 @@ class W8A8Linear(torch.nn.Module):
             return ops.fp4_scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype)
         if self.scheme == "fp8":
             return ops.fp8_scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype)
-        return ops.scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype,
-                             workspace=self.workspace)
+        return ops.scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype)
 
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
@@ -149,13 +150,14 @@ def quantize_linear_layers(module: torch.nn.Module, method: str = "int8",
 
     The selection follows the page "Online Quantization" (Parameters table):
     `method` is "int8", "fp8" or "fp4"; `activation_scheme` must be "dynamic"
-    (activation scales computed at run time, the only scheme implemented); `ignored_layers` holds name patterns of layers to keep in
-    their float type. A layer is kept when its qualified name (as in
+    (activation scales computed at run time, the only scheme implemented);
+    `ignored_layers` holds name patterns of layers to keep in their float
+    type. A layer is kept when its qualified name (as in
     module.named_modules()) matches a pattern by fnmatch or contains it.
     Weights are quantized online on their device (W8A8Linear.from_float).
     Anything the path cannot run raises ValueError naming the layer: a layer
-    on the CPU, or in_features not a multiple of 16 (32 for "fp4"). Returns `module`, or the
-    replacement when `module` is itself a Linear."""
+    on the CPU, or in_features not a multiple of 16 (32 for "fp4"). Returns
+    `module`, or the replacement when `module` is itself a Linear."""
     if method not in ("int8", "fp8", "fp4"):
         raise ValueError(f"method must be 'int8', 'fp8' or 'fp4', got {method!r}")
     if activation_scheme != "dynamic":
