@@ -275,6 +275,33 @@ def test_many_wide_rows(ops, m, k):
     assert torch.equal(ops.gated_residual(x, y, gate=gate, post=ops.Norm(**post)), got_r)
 
 
+@pytest.mark.parametrize("m,k", [(6, 1536), (7, 1200), (5, 2500), (3, 5120), (7, 5001), (4, 6144), (9, 5200),
+                                 (515, 5120), (700, 5001), (520, 1536), (514, 9001), (515, 10240), (2, 16001),
+                                 (514, 12296)])
+def test_thread_counts(ops, m, k):
+    """The row shapes in between, whole and ragged, few rows and many; the
+    residual in place of the stream."""
+    x, y = rows(m, k, m), rows(m, k, m + 1)
+    v = {"scale": vec(k, 3, F32), "shift": vec(k, 4, F32, 0.5)}
+    z = torch.zeros(m, k, device=DEV, dtype=torch.float64)
+    for kind in ("rms", "layer"):
+        want, bound = ref.norm(x.double(), z, kind, 1e-6, **v)
+        for out in ("same", "int8", "fp8"):
+            check_norm(ops, run_norm(ops, x, ops.Norm(kind, **v), out), want, bound, BF, out, f"{kind} {out}")
+    post = {"kind": "layer", "eps": 1e-6, "weight": vec(k, 6, BF, 1.0)}
+    for stream in (BF, F32):
+        xs = x.to(stream)
+        r, err = ref.residual(xs, y, post=post)
+        h, h_err = ref.norm(r, err, "rms", 1e-6, **v)
+        got_r, got_h = ops.gated_residual_norm(xs, y, ops.Norm("rms", **v), post=ops.Norm(**post))
+        ref.check_float(got_r, r, err, stream, "r")
+        ref.check_float(got_h, h, h_err, BF, "h")
+        again, *codes = ops.gated_residual_norm_quant(xs, y, ops.Norm("rms", **v), post=ops.Norm(**post))
+        ref.check_codes(*codes, h, h_err, 127, "codes")
+        assert torch.equal(again, got_r)
+        assert torch.equal(ops.gated_residual(xs, y, post=ops.Norm(**post), out=xs), got_r)
+
+
 @pytest.mark.parametrize("k", [104, 33000])
 def test_offsets_past_32_bits(ops, k):
     """Rows, modulation vectors and outputs billions of elements apart."""

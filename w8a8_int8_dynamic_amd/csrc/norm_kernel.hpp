@@ -49,10 +49,10 @@ __device__ __forceinline__ float row_sum(float v, float *part, int &turn)
     for (int i = 0; i < WAVES; ++i)
         s[i] = p[i];
 #pragma unroll
-    for (int w = WAVES / 2; w > 0; w /= 2)
+    for (int n = WAVES; n > 1; n = (n + 1) / 2)
 #pragma unroll
-        for (int i = 0; i < w; ++i)
-            s[i] += s[i + w];
+        for (int i = 0; i < n / 2; ++i)
+            s[i] += s[i + (n + 1) / 2];
     return s[0];
 }
 
@@ -199,6 +199,10 @@ __device__ __forceinline__ void normalize(float (&v)[CH][8], const Piece (&p)[CH
 }
 
 // A piece of a row to memory: whole, or its own elements one by one.
+// A norm's own output needs no such care: pieces that share elements hold the
+// same values there, bit for bit, so each is stored whole (NormRowsArgs.r may be
+// x, where a piece may have read its neighbour's result). Stores that no
+// branch skips can be counted, and the next row's elements waited for alone.
 template <int E, bool WHOLE>
 __device__ __forceinline__ void piece_store(char *row, const Piece &p, const float (&v)[8])
 {
@@ -363,7 +367,9 @@ __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a
                 if constexpr (OUT == kOutCodes)
                     m = max(m, __float_as_uint(own_or_zero<WHOLE>(p[c], j, v[c][j])) & 0x7fffffffu);
             }
-            if (OUT == kOutFloat && (WHOLE || p[c].skip < 8))
+            if constexpr (OUT == kOutFloat && !RES)
+                store8<AE>(static_cast<char *>(a.out) + row * a.ldo * 2, p[c].at, p[c].at + 8, v[c]);
+            else if (OUT == kOutFloat && (WHOLE || p[c].skip < 8))
                 piece_store<AE, WHOLE>(static_cast<char *>(a.out) + row * a.ldo * 2, p[c], v[c]);
         }
         if constexpr (OUT != kOutCodes)
@@ -383,7 +389,9 @@ __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a
                 lo = quant_rule::codes4_i8(v[c][0], v[c][1], v[c][2], v[c][3], inv);
                 hi = quant_rule::codes4_i8(v[c][4], v[c][5], v[c][6], v[c][7], inv);
             }
-            if (WHOLE || p[c].skip == 0) {
+            if constexpr (!RES && !WHOLE) {
+                *reinterpret_cast<v2u_any *>(q + p[c].at) = v2u_any{lo, hi};
+            } else if (WHOLE || p[c].skip == 0) {
                 *reinterpret_cast<uint2 *>(q + p[c].at) = make_uint2(lo, hi);
             } else {
 #pragma unroll
@@ -579,21 +587,26 @@ struct Shape {
 
 // The row shapes of norm_rows_kernel: threads per row and chunks per thread,
 // up to 16384 elements (beyond, a row and its vectors no longer fit the
-// registers of 1024 threads).
+// registers of one workgroup; M4096 K16000 in passes takes 1.4 to 1.8 times as
+// long).
 constexpr int64_t kHeldElements = 16384;
 template <int XE, int AE, bool RES, int OUT, int CH, int TPR, int R>
 Shape shape(int64_t K)
 {
+    static_assert(TPR * R <= (CH > 2 ? 512 : 1024), "a workgroup fits its share of a CU");
     return {K == CH * TPR * 8 ? norm_rows_kernel<XE, AE, RES, OUT, CH, TPR, R, true>
                               : norm_rows_kernel<XE, AE, RES, OUT, CH, TPR, R, false>, TPR * R, R,
             (CH > 2 ? 512 : 1024) / (TPR * R)};
 }
 // One chunk per thread as far as 1024 threads reach, where a thread has the
 // words of two tensors and the vectors of two norms to hold, or where rows are
-// few and their latency counts; two otherwise, for more rows in flight.
-// Measured on MI355X, two chunks against one: M8192 K4096 bf16 gated residual
+// few and their latency counts; two otherwise, for more rows in flight. In
+// between, the thread counts leave at most a third of the threads without
+// elements.
+// Measured on MI355X, bf16: two chunks against one, M8192 K4096, gated residual
 // with post norm and next norm 48.9 against 45.1 us, norm to int8 codes 24.0
-// against 28.9 us, the same of one row 3.5 against 3.2 us.
+// against 28.9 us, the same of one row 3.5 against 3.2 us; M4096 K6000, the
+// gated residual on 768 threads 37.1, on 1024 44.5 us.
 constexpr int64_t kFewRows = 512;
 template <int XE, int AE, bool RES, int OUT>
 Shape pick(int64_t rows, int64_t K)
@@ -603,19 +616,33 @@ Shape pick(int64_t rows, int64_t K)
         return shape<XE, AE, RES, OUT, 1, 64, 4>(K);
     if (chunks <= 128)
         return shape<XE, AE, RES, OUT, 1, 128, 1>(K);
+    if (chunks <= 192)
+        return shape<XE, AE, RES, OUT, 1, 192, 1>(K);
     if (chunks <= 256)
         return shape<XE, AE, RES, OUT, 1, 256, 1>(K);
     if (RES || rows <= kFewRows) {
+        if (chunks <= 384)
+            return shape<XE, AE, RES, OUT, 1, 384, 1>(K);
         if (chunks <= 512)
             return shape<XE, AE, RES, OUT, 1, 512, 1>(K);
+        if (chunks <= 640)
+            return shape<XE, AE, RES, OUT, 1, 640, 1>(K);
+        if (chunks <= 768)
+            return shape<XE, AE, RES, OUT, 1, 768, 1>(K);
         if (chunks <= 1024)
             return shape<XE, AE, RES, OUT, 1, 1024, 1>(K);
     } else {
+        if (chunks <= 384)
+            return shape<XE, AE, false, OUT, 2, 192, 1>(K);
         if (chunks <= 512)
             return shape<XE, AE, false, OUT, 2, 256, 1>(K);
+        if (chunks <= 768)
+            return shape<XE, AE, false, OUT, 2, 384, 1>(K);
         if (chunks <= 1024)
             return shape<XE, AE, false, OUT, 2, 512, 1>(K);
     }
+    if (chunks <= 1280)
+        return shape<XE, AE, RES, OUT, 2, 640, 1>(K);
     if (chunks <= 1536)
         return shape<XE, AE, RES, OUT, 3, 512, 1>(K);
     return shape<XE, AE, RES, OUT, 2, 1024, 1>(K);

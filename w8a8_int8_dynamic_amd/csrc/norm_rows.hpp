@@ -15,9 +15,11 @@ using quant_rule::kF16;
 using quant_rule::kF32;
 using quant_rule::u32;
 
-// 16 bytes at any element boundary: gfx950 takes unaligned vector accesses to
-// global memory, so rows of odd pitch or start need no path of their own.
+// 16 (or 8) bytes at any element boundary: gfx950 takes unaligned vector
+// accesses to global memory, so rows of odd pitch or start need no path of
+// their own.
 typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned v2u_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
