@@ -367,7 +367,8 @@ def test_offsets_past_32_bits(ops):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 20, 16384), (1, 20, 16416), (2, 20, 8192), (2, 20, 8224), (3, 40, 4096),
-                                   (4, 40, 4096), (4, 40, 4128), (5, 40, 4096)])
+                                   (4, 40, 4096), (4, 40, 4128), (5, 40, 4096), (16, 20, 1024), (16, 20, 1056),
+                                   (17, 33, 1024), (40, 100, 992), (100, 300, 64), (250, 20, 736), (16, 20, 32)])
 def test_quant_inside_the_product_and_beside_it(ops, m, n, k):
     """Either side of where the rows are too many to be quantized in the same
     launch."""

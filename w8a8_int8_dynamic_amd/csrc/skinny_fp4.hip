@@ -17,9 +17,11 @@
 //     its first weights are on their way, 8 elements a thread at a time (the
 //     rows are few and sit in L2), and takes its token operands from there;
 //     the workgroups of the first channels write the codes and scales out.
-//     Measured on MI355X, one row, N 12288, K 4096: a row quantized by each
-//     lane in place of its own operand takes 10.6 us, this 6.5, two launches
-//     8.7.
+//     Up to kSlots such steps: measured on MI355X, N 1111, two launches against
+//     this, M 16 K 512 (two steps) 4.7 against 3.5 us, M 8 K 2048 (four) 5.3
+//     against 4.3, M 16 K 2048 (eight) 5.4 against 5.9. One row, N 12288, K
+//     4096: a row quantized by each lane in place of its own operand takes 10.6
+//     us, this 6.5, two launches 8.7.
 // Ragged tails: token rows past M read row M-1 and channels past N the last
 // image (never stored); blocks past the row's last read the last one again, as
 // 1.0-scaled operands of zero weights.
@@ -52,50 +54,59 @@ constexpr int kSlots = 4;        // units of 8 elements that a thread quantizes,
 __host__ __device__ constexpr int row_bytes(int blocks) { return blocks * 16 + (blocks + 15) / 16 * 16; }
 
 // Rows m0 .. m0+rows-1 of x quantized by the workgroup into LDS, row r at
-// r * row_bytes, and with `writer` to xq and sx. Every thread calls this (it
-// holds a barrier). rows * ceil(units / THREADS) is at most kSlots.
-template <int THREADS, int E>
+// r * row_bytes, and with `writer` to xq and sx. The rows' units of 8 elements
+// are one list, dealt out THREADS at a time, of which a thread reads AHEAD
+// before it quantizes the first; a block's four are neighbouring lanes'.
+template <int THREADS, int E, int AHEAD>
 __device__ __forceinline__ void quantize_rows(const MmArgs &a, int m0, int rows, bool writer, char *tok)
 {
     constexpr int XB = E == kF32 ? 4 : 2;
-    const int units = a.blocks * 4, per_row = (units + THREADS - 1) / THREADS;
-    uint4 lo[kSlots], hi[kSlots];
+    const int units = a.blocks * 4;
+    const int row_step = THREADS / units, unit_step = THREADS % units;
+    auto next = [&](int &row, int &unit) __attribute__((always_inline)) {
+        row += row_step;
+        unit += unit_step;
+        if (unit >= units) {
+            unit -= units;
+            ++row;
+        }
+    };
+    int r = (int)threadIdx.x / units, u = (int)threadIdx.x - r * units;
+    for (int s0 = 0; s0 < rows * units; s0 += AHEAD * THREADS) {
+        uint4 lo[AHEAD], hi[AHEAD];
+        int rr = r, uu = u;
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
-        const int r = s / per_row, u = (s - r * per_row) * THREADS + (int)threadIdx.x;
-        lo[s] = hi[s] = make_uint4(0, 0, 0, 0);
-        if (r < rows && u < units) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(a.x) +
-                                                               ((int64_t)(m0 + r) * a.ldx + u * 8) * XB);
+        for (int s = 0; s < AHEAD; ++s) {
+            // (past the last row: the first unit again, not kept)
+            const bool in = rr < rows;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                reinterpret_cast<const char *>(a.x) + ((int64_t)(m0 + (in ? rr : 0)) * a.ldx + (in ? uu : 0) * 8) * XB);
             lo[s] = src[0];
-            if (E == kF32)
-                hi[s] = src[1];
+            hi[s] = E == kF32 ? src[1] : lo[s];
+            next(rr, uu);
         }
-    }
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
-        const int r = s / per_row, u = (s - r * per_row) * THREADS + (int)threadIdx.x;
-        if (r >= rows)
-            break;
-        // The four lanes of a block are all inside the row or all past it.
-        u32 m = absmax8<E>(lo[s], hi[s]);
-        m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0xB1, 0xF, 0xF, false));
-        m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x4E, 0xF, 0xF, false));
-        const u32 byte = scale_byte(m);
-        if (u < units) {
-            const u32 c = codes8<E>(lo[s], hi[s], byte);
-            char *row = tok + r * row_bytes(a.blocks);
-            *reinterpret_cast<u32 *>(row + u * 4) = c;
-            if ((u & 3) == 0)
-                row[a.blocks * 16 + (u >> 2)] = (char)byte;
-            if (writer) {
-                *reinterpret_cast<u32 *>(const_cast<int8_t *>(a.xq) + (int64_t)(m0 + r) * a.ldq + u * 4) = c;
+        for (int s = 0; s < AHEAD; ++s) {
+            // The four lanes of a block are all inside the rows or all past them.
+            u32 m = absmax8<E>(lo[s], hi[s]);
+            m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0xB1, 0xF, 0xF, false));
+            m = max(m, (u32)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x4E, 0xF, 0xF, false));
+            const u32 byte = scale_byte(m);
+            if (r < rows) {
+                const u32 c = codes8<E>(lo[s], hi[s], byte);
+                char *row = tok + r * row_bytes(a.blocks);
+                *reinterpret_cast<u32 *>(row + u * 4) = c;
                 if ((u & 3) == 0)
-                    const_cast<uint8_t *>(a.sx)[(int64_t)(m0 + r) * a.lds + (u >> 2)] = (uint8_t)byte;
+                    row[a.blocks * 16 + (u >> 2)] = (char)byte;
+                if (writer) {
+                    *reinterpret_cast<u32 *>(const_cast<int8_t *>(a.xq) + (int64_t)(m0 + r) * a.ldq + u * 4) = c;
+                    if ((u & 3) == 0)
+                        const_cast<uint8_t *>(a.sx)[(int64_t)(m0 + r) * a.lds + (u >> 2)] = (uint8_t)byte;
+                }
             }
+            next(r, u);
         }
     }
-    __syncthreads();
 }
 
 template <class S, int OUT, int QK>
@@ -177,7 +188,14 @@ __global__ __launch_bounds__(S::THREADS) void skinny_fp4_kernel(const MmArgs a)
     if constexpr (QK != kCodes) {
         // (of every wave, clamped into the weight: no wave skips the barrier)
         weights(wk, w, ws);
-        quantize_rows<S::THREADS, QK>(a, m0, min(S::BM, a.M - m0), nb0 == 0, tok);
+        const int rows = min(S::BM, a.M - m0);
+        if (rows * a.blocks * 4 <= S::THREADS)
+            quantize_rows<S::THREADS, QK, 1>(a, m0, rows, nb0 == 0, tok);
+        else if (rows * a.blocks * 4 <= 2 * S::THREADS)
+            quantize_rows<S::THREADS, QK, 2>(a, m0, rows, nb0 == 0, tok);
+        else
+            quantize_rows<S::THREADS, QK, 4>(a, m0, rows, nb0 == 0, tok);
+        __syncthreads();
         if (wk < chunks)
             products(wk, w, ws);
     }
@@ -289,9 +307,9 @@ hipError_t launch_skinny_quant_fp4(const MmArgs &a, int x_kind, int mode, int i,
 {
     const Fp4Skinny &s = kSkinny4[i];
     const int64_t rows = std::min<int64_t>(a.M, s.tile.bm);
-    if (a.M > s.tile.bm || rows * ceil_div(a.blocks * 4, s.tile.threads) > kSlots)
+    if (ceil_div(rows * a.blocks * 4, s.tile.threads) > kSlots)
         return hipErrorNotSupported;
-    const int64_t tiles = ceil_div(a.N, s.tile.bn);
+    const int64_t tiles = ceil_div(a.M, s.tile.bm) * ceil_div(a.N, s.tile.bn);
     hipLaunchKernelGGL(s.quant[x_kind][mode], dim3((unsigned)tiles), dim3(s.tile.threads),
                        (size_t)(rows * row_bytes(a.blocks)), stream, a);
     return hipGetLastError();
