@@ -12,7 +12,8 @@
  * the int8 weights and a debug unpack of the repacked weight. Beyond them:
  * the quant and the matmul in one call (int8_quant_scaled_mm), fp16
  * activations and outputs, the online weight quant straight into the
- * repacked layout, and an FP8 (e4m3) twin of the whole path.
+ * repacked layout, an FP8 (e4m3) twin of the whole path, a microscaled 4-bit
+ * (MX FP4) layer, and the norms and gated residuals around such layers.
  *
  * Conventions for every entry point:
  *   - Pointers to tensors are DEVICE pointers on the current HIP device.
@@ -24,7 +25,8 @@
  *     and the call returns without synchronizing; inputs must stay alive and
  *     unmodified until the stream reaches the work.
  *   - The library never allocates, frees or synchronizes device memory. The
- *     caller owns every buffer. Outputs must not alias inputs.
+ *     caller owns every buffer. Outputs must not alias inputs (but see
+ *     w8a8_residual_t).
  *   - All argument checks run on the host before any HIP call, so a bad
  *     argument returns an error without touching the device. There is no
  *     fallback path: an unsupported device or argument is an error.
@@ -525,7 +527,9 @@ w8a8_status_t fp4_scaled_mm_tile(const uint8_t *xq, int64_t ldq, const uint8_t *
 
 /*
  * fp4_quant_scaled_mm - fp4_quant_per_block of x [M, ldx], then
- * fp4_scaled_mm of the result, in one call; xq and x_scale are written.
+ * fp4_scaled_mm of the result, in one call; xq and x_scale are written. One
+ * launch where a small-M tile runs and its rows (the tile's 16, or M) times K
+ * are at most 16384 elements, else two.
  * Requirements: those of the two.
  */
 w8a8_status_t fp4_quant_scaled_mm(const void *x, int x_dtype, int64_t ldx, uint8_t *xq,

@@ -15,12 +15,16 @@
 // Rows too long for that take norm_rows_looped_kernel, one workgroup a row,
 // which reads the row again (from L2) for each of its passes. Neither writes
 // an element before it has read it for the last time, so r may be x itself.
+// Measured on MI355X, bf16, from rotating buffers: M8192 K4096 layer norm with
+// scale and shift 25.6 us (5.2 TB/s; a large copy makes 5.1); M8192 K12288 rms to
+// e4m3 codes 56.5 us (5.3); M8192 K4096 gated residual with post norm and next
+// norm 44.4 us (6.0); M999 K5001 fp16 into an fp32 stream 13.4 us (3.7: four
+// rows to a workgroup); one row of 4096 to int8 codes 3.1 us.
 #pragma once
 
 #include <algorithm>
 
 #include "norm_rows.hpp"
-
 
 namespace w8a8 {
 namespace {
@@ -664,7 +668,7 @@ hipError_t launch(const NormRowsArgs &a, hipStream_t stream)
                   : codes ? pick<XE, AE, true, kOutCodes>(a.rows, a.K) : pick<XE, AE, true, kOutFloat>(a.rows, a.K);
     // A run of rows per workgroup, as long as every CU has its workgroups: each
     // run pays for its vectors once (measured on MI355X, twice as many
-    // workgroups cost 5-13 % from 2048 rows on).
+    // workgroups cost 5 to 30 % from 600 rows on).
     const int64_t want = 256 * s.per_cu;
     const int64_t per_block = round_up(ceil_div(a.rows, want), s.rows);
     hipLaunchKernelGGL(s.fn, dim3((unsigned)ceil_div(a.rows, per_block)), dim3(s.threads), 0, stream, a, per_block);
