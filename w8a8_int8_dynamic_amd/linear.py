@@ -98,21 +98,21 @@ class W8A8Linear(torch.nn.Module):
         x2 = x if x.dim() == 2 else x.reshape(-1, self.in_features)
         if x2.stride(-1) != 1:
             x2 = x2.contiguous()
-        # The per-token quant and the scaled matmul, as one library call; the
-        # output (and bias) type is x's.
+        # The quant and the scaled matmul, as one library call; the output (and
+        # bias) type is x's.
+        if self.scheme == "fp4":
+            dtype, b = x2.dtype, self._buffers
+            if dtype != torch.bfloat16 and dtype != torch.float16:
+                raise TypeError(f"the fp4 scheme takes bfloat16 or float16 activations, got {dtype}")
+            out = ops._fp4_linear(x2, b["w_packed"], b["w_scale"], self.out_features,
+                                  b["bias_f16"] if dtype == torch.float16 else b["bias"])
+            return out if x2 is x else out.reshape(*lead, self.out_features)
         bias = self.bias_f16 if x2.dtype == torch.float16 else self.bias
         if self.scheme == "fp8":
             if x2.dtype != torch.bfloat16:
                 raise TypeError(f"the fp8 scheme takes bfloat16 activations, got {x2.dtype}")
             out, _, _ = ops.fp8_quant_scaled_mm(x2, self.w_packed, self.w_scale,
                                                 self.out_features, bias)
-        elif self.scheme == "fp4":
-            if x2.dtype not in (torch.bfloat16, torch.float16):
-                raise TypeError(f"the fp4 scheme takes bfloat16 or float16 activations, got {x2.dtype}")
-            b = self._buffers
-            out = ops._fp4_linear(x2, b["w_packed"], b["w_scale"], self.out_features, bias)
-            if x2 is x:
-                return out
         else:
             wsp = self.workspace if x2.dtype == torch.bfloat16 else None
             out, _, _ = ops.quant_scaled_mm(x2, self.w_packed, self.w_scale, self.out_features,

@@ -577,14 +577,13 @@ def _check_fp4_packed(w_packed: torch.Tensor, s_packed: torch.Tensor, N: int, K:
         raise ValueError(f"N must be at least 1, got {N}")
     rows = _round_up(N, 16)
 
-    def fits(t: torch.Tensor, n: int) -> bool:
-        return t.dtype == torch.uint8 and t.numel() >= n and t.is_contiguous() and t.is_cuda
-
-    if not fits(w_packed, rows * _round_up(K, 128) // 2) or not fits(s_packed, rows * _round_up(K, 512) // _FP4_BLOCK):
-        raise ValueError("w_packed and s_packed must be uint8 device buffers of the packed layout (N, K)")
     device = ref.get_device()
-    if w_packed.get_device() != device or s_packed.get_device() != device:
-        raise ValueError(f"all tensors must be on {ref.device}")
+    if device < 0 or w_packed.get_device() != device or s_packed.get_device() != device:
+        raise ValueError(f"all tensors must be on one GPU, and x is on {ref.device}")
+    if w_packed.dtype != torch.uint8 or s_packed.dtype != torch.uint8 or \
+            w_packed.numel() < rows * ((K + 127) // 128 * 64) or s_packed.numel() < rows * ((K + 511) // 512 * 16) or \
+            not w_packed.is_contiguous() or not s_packed.is_contiguous():
+        raise ValueError("w_packed and s_packed must be uint8 device buffers of the packed layout (N, K)")
 
 
 def fp4_prepack_weight(wq: torch.Tensor, ws: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
