@@ -218,17 +218,30 @@ struct Tile {
     static constexpr int SIDE_PER_THREAD = (SIDE + THREADS - 1) / THREADS;
     static constexpr int FLAG = MAIN + SIDE * 4;        // one word: fused-path decision
     static constexpr int LDS = FLAG + 16;
-    // The 4-bit kernel's block scales: a ring of SC_SLOTS LDS slots behind the
-    // image ring, each the 16 scale bytes of SC_STAGES stages (4 k-blocks) for
-    // every token and channel of the tile, loaded in units of 64 rows (one
-    // wave's 16 bytes a lane) SC_LEAD slots ahead.
+    // The 4-bit kernel's block scales, in two rings of LDS slots behind the
+    // image ring. A chunk is the 16 scale bytes of a row that SC_STAGES stages
+    // (4 k-blocks) take. Channels (packed chunk by chunk): SC_SLOTS slots of
+    // one chunk, loaded SC_LEAD slots ahead, 64 rows a load (a wave's 16
+    // bytes a lane). Tokens (whose rows lie apart, so that each load fetches a
+    // line per row): 2 slots of SX_CH chunks, loaded one ahead, 64 / SX_CH
+    // rows a load (measured on MI355X, two chunks against one: M8192 N4096
+    // K12288 with 64x64 tiles 375 against 393 us, with 128x192 252 against
+    // 265; one where a stage holds a single k-block, whose loop two would
+    // make twice as long: 256x192, M512, 24.6 against 25.5).
     static constexpr int SC_STAGES = 4 / WK;
     static constexpr int SC_LEAD = WK, SC_SLOTS = 2 * WK;
-    static constexpr int SC_UNITS = (BM + BN) / 64;
+    static constexpr int SC_SLOT = BN * 16;                   // bytes
+    static constexpr int SC_UNITS = BN / 64;
     static constexpr int SC_LPW = (SC_UNITS + NW - 1) / NW;   // loads per wave per slot
-    static constexpr int SC_SLOT = (BM + BN) * 16;            // bytes
-    static constexpr int SIDE4 = cmax(MAIN, RING + SC_SLOTS * SC_SLOT);
+    static constexpr int SX_CH = WK == 2 ? 2 : 1;
+    static constexpr int SX_STAGES = SX_CH * SC_STAGES;
+    static constexpr int SX_SLOT = BM * 16 * SX_CH;           // bytes
+    static constexpr int SX_UNITS = BM * SX_CH / 64;
+    static constexpr int SX_LPW = (SX_UNITS + NW - 1) / NW;
+    static constexpr int SX_RING = RING, SC_RING = RING + 2 * SX_SLOT;
+    static constexpr int SIDE4 = cmax(MAIN, SC_RING + SC_SLOTS * SC_SLOT);
     static constexpr int LDS4 = SIDE4 + BN * 4;               // then the bias of the tile
+    static constexpr int GROUP4 = clcm(GROUP, SX_STAGES);
     static_assert(NW == 4 || NW == 8, "four or eight wavefronts per workgroup");
     static_assert(BM % (32 * WM) == 0 && BN % (32 * WN) == 0, "tile/wave mismatch");
     static_assert(AIMG % NW == 0, "token loads must split evenly over waves");
@@ -237,9 +250,11 @@ struct Tile {
     static_assert(WLDS || LW >= LT, "weight lead >= token lead");
     static_assert(VM < 64 && (LT + 1) * LPW < 64 && (LW + 1) * LPW < 64, "vmcnt range");
     static_assert(LDS <= 160 * 1024 && LDS4 <= 160 * 1024, "LDS budget");
-    static_assert(LT <= 3 && GROUP % SC_STAGES == 0, "scales land a slot's stages before their use");
+    static_assert(LT <= 3 && LW <= 3 && SX_STAGES >= 4 && SC_LEAD * SC_STAGES >= 4, "scales land a slot's stages before their use");
     // Loads that step v issues for the scales.
-    static constexpr int scale_loads(int v) { return (v + 1 + 64) % SC_STAGES == 0 ? SC_LPW : 0; }
+    static constexpr bool sc_step(int v) { return (v + 1 + 64) % SC_STAGES == 0; }
+    static constexpr bool sx_step(int v) { return (v + 1 + 64) % SX_STAGES == 0; }
+    static constexpr int scale_loads(int v) { return (sc_step(v) ? SC_LPW : 0) + (sx_step(v) ? SX_LPW : 0); }
     // VM for the 4-bit kernel at step u (modulo GROUP): the same wait with the
     // scale loads counted (a step issues images, scales, weights).
     static constexpr int vm_fp4(int u)
@@ -442,66 +457,78 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
             for (int i = 0; i < T::FM; ++i)
                 x[i][h] = st[(2 * i) * 64 + xslot[h]];
     };
-    // 4-bit: the scale bytes of slot c (k-blocks 4c .. 4c+3 of the tile's
-    // tokens, then channels) into LDS slot c % SC_SLOTS. Unit g is rows 64*g ..
-    // of them, lane l row 64*g + l; with fewer units than loads the last unit
-    // is loaded twice (the same bytes to the same place).
-    // Where each load starts, and how far it moves with c, is settled before
-    // the loop: a choice inside it would cut a step in pieces.
+    // 4-bit: the scale bytes of the channels' slot c (k-blocks 4c .. 4c+3) and
+    // of the tokens' slot c (SX_CH chunks from SX_CH*c on) into the rings.
+    // Channels: unit g is rows 64*g .., lane l row 64*g + l. Tokens: lane l of
+    // unit g is row 64/SX_CH*g + l/SX_CH; its pieces stand in the slot in turned
+    // order for every other eight rows, so that scale_read's lanes spread over
+    // the banks. With fewer units than loads the last unit is loaded twice
+    // (the same bytes to the same place).
     const int chunks = (a.kblocks + 3) / 4;
-    const uint8_t *sc_base[FP4 ? T::SC_LPW : 1];
-    int sc_off[FP4 ? T::SC_LPW : 1], sc_step[FP4 ? T::SC_LPW : 1], sc_dst[FP4 ? T::SC_LPW : 1];
+    const uint8_t *sc_base = nullptr, *sx_base = nullptr;
+    int sc_off[FP4 ? T::SC_LPW : 1], sx_off[FP4 ? T::SX_LPW : 1], sx_piece = 0;
     if constexpr (FP4) {
+        sc_base = pinned_ptr(a.sw + (int64_t)(n0 / 16) * chunks * 256);
+        sx_base = pinned_ptr(a.sx + (int64_t)m0 * a.lds);
+        sx_piece = (lane & (T::SX_CH - 1)) ^ ((lane / (8 * T::SX_CH)) & (T::SX_CH - 1));
 #pragma unroll
         for (int i = 0; i < T::SC_LPW; ++i) {
             const int g = min(i * T::NW + wave, T::SC_UNITS - 1);
-            const int tok = (g - T::BM / 64) >> 31;    // all ones for token rows
-            const int row = g * 64 + lane;             // token row, or channel BM + n, of the tile
-            const int nb = min(n0 / 16 + ((row - T::BM) >> 4), a.nblocks - 1) - n0 / 16;
-            const int off_tok = (min(m0 + row, a.M - 1) - m0) * (int)a.lds;
-            const int off_ch = nb * chunks * 256 + (lane & 15) * 16;
-            const uintptr_t base_tok = reinterpret_cast<uintptr_t>(a.sx + (int64_t)m0 * a.lds);
-            const uintptr_t base_ch = reinterpret_cast<uintptr_t>(a.sw + (int64_t)(n0 / 16) * chunks * 256);
-            sc_off[i] = (off_tok & tok) | (off_ch & ~tok);
-            sc_step[i] = pinned((16 & tok) | (256 & ~tok));
-            sc_dst[i] = pinned(T::RING + g * 1024);
-            sc_base[i] = pinned_ptr(reinterpret_cast<const uint8_t *>((base_tok & (intptr_t)tok) |
-                                                                      (base_ch & ~(intptr_t)tok)));
+            const int nb = min(n0 / 16 + g * 4 + (lane >> 4), a.nblocks - 1) - n0 / 16;
+            sc_off[i] = nb * chunks * 256 + (lane & 15) * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < T::SX_LPW; ++i) {
+            const int g = min(i * T::NW + wave, T::SX_UNITS - 1);
+            const int row = g * (64 / T::SX_CH) + lane / T::SX_CH;
+            sx_off[i] = (min(m0 + row, a.M - 1) - m0) * (int)a.lds;
         }
     }
-    auto scale_dma = [&](int c) __attribute__((always_inline)) {
+    auto sc_dma = [&](int c) __attribute__((always_inline)) {
         const int cc = min(c, chunks - 1);
 #pragma unroll
         for (int i = 0; i < T::SC_LPW; ++i)
-            dma16(sc_base[i], sc_off[i] + cc * sc_step[i],
-                  reinterpret_cast<char *>(lds) + sc_dst[i] + (c & (T::SC_SLOTS - 1)) * T::SC_SLOT);
+            dma16(sc_base, sc_off[i] + cc * 256,
+                  reinterpret_cast<char *>(lds) + T::SC_RING + (c & (T::SC_SLOTS - 1)) * T::SC_SLOT +
+                      min(i * T::NW + wave, T::SC_UNITS - 1) * 1024);
     };
+    auto sx_dma = [&](int c) __attribute__((always_inline)) {
+        const int at = min(c * T::SX_CH + sx_piece, chunks - 1) * 16;
+#pragma unroll
+        for (int i = 0; i < T::SX_LPW; ++i)
+            dma16(sx_base, sx_off[i] + at,
+                  reinterpret_cast<char *>(lds) + T::SX_RING + (c & 1) * T::SX_SLOT +
+                      min(i * T::NW + wave, T::SX_UNITS - 1) * 1024);
+    };
+    const int sx_lane = (lane & 31) * 16 * T::SX_CH + (((lane & 31) / 8) & (T::SX_CH - 1)) * 16;
     // 4-bit: this wave's scale bytes of stage t: lane l takes the four blocks
     // of its token (channel) l%32 of each 32-row group as one word.
     // Past the row's last block (in the last k-block, never in the steady
     // state) the byte is 1.0: it meets zero weights, and must not be NaN.
     auto scale_read = [&](auto full, int t, auto u_c, int (&sx)[FP4 ? T::FM : 1],
                           int (&sw)[FP4 ? T::FN : 1]) __attribute__((always_inline)) {
-        constexpr int u = decltype(u_c)::value;        // t modulo SC_STAGES
-        const int c = t / T::SC_STAGES;
+        constexpr int u = decltype(u_c)::value;        // t modulo SX_STAGES
+        constexpr int piece = u / T::SC_STAGES;
         const int word = T::WK == 1 ? u % 4 : (u % 2) * 2 + wk;
-        const int *slot = reinterpret_cast<const int *>(reinterpret_cast<const char *>(lds) + T::RING +
-                                                        (c & (T::SC_SLOTS - 1)) * T::SC_SLOT) + word;
+        const char *slots = reinterpret_cast<const char *>(lds) + word * 4;
+        const char *sc_slot = slots + T::SC_RING + ((t / T::SC_STAGES) & (T::SC_SLOTS - 1)) * T::SC_SLOT +
+                              (lane & 31) * 16;
+        const char *sx_slot = slots + T::SX_RING + ((t / T::SX_STAGES) & 1) * T::SX_SLOT + (sx_lane ^ (piece * 16));
         unsigned keep = ~0u;
         if constexpr (!decltype(full)::value)
             keep = t * T::WK + wk == kblast && (a.blocks & 3) ? (1u << (8 * (a.blocks & 3))) - 1u : ~0u;
-        auto one = [&](int row) __attribute__((always_inline)) {
-            unsigned v = (unsigned)slot[(row + (lane & 31)) * 4];
+        auto one = [&](const char *p) __attribute__((always_inline)) {
+            unsigned v = *reinterpret_cast<const unsigned *>(p);
             if constexpr (!decltype(full)::value)
                 v = (v & keep) | (0x7f7f7f7fu & ~keep);
             return (int)v;
         };
 #pragma unroll
         for (int i = 0; i < T::FM; ++i)
-            sx[i] = one(wm * (T::BM / T::WM) + i * 32);
+            sx[i] = one(sx_slot + (wm * (T::BM / T::WM) + i * 32) * 16 * T::SX_CH);
 #pragma unroll
         for (int j = 0; j < T::FN; ++j)
-            sw[j] = one(T::BM + (wn * T::FN + j) * 32);
+            sw[j] = one(sc_slot + (wn * T::FN + j) * 32 * 16);
     };
     // Those words shifted so that bytes 0 and 2 are blocks l/32 and 2 + l/32,
     // the ones of this lane in the two halves of a k-block. Done as a step
@@ -551,7 +578,7 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
     // times as many, measured on MI355X); the e4m3 twin has half as many
     // (twice as long) MFMAs, so its memory instructions are spread over them.
     constexpr int DS_READS = 2 * T::FM + (T::WLDS ? 2 * T::FN : 0) + (FP4 ? T::FM + T::FN : 0);
-    constexpr int MEM_OPS = DS_READS + T::LPW + (FP4 ? T::SC_LPW : 0);
+    constexpr int MEM_OPS = DS_READS + T::LPW + (FP4 ? T::SC_LPW + T::SX_LPW : 0);
     constexpr int PER = FP8 ? (MEM_OPS + NMMA - PRE - 1) / (NMMA - PRE) : T::MP;
 
     using Full = std::integral_constant<bool, true>;
@@ -596,14 +623,17 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
             if constexpr (T::WLDS)
                 bread(s + 1, bf[(u + 1) & 1]);
             if constexpr (FP4)
-                scale_read(full, s + 1, std::integral_constant<int, (u + 1) % T::SC_STAGES>{}, sxf[(u + 1) & 1],
+                scale_read(full, s + 1, std::integral_constant<int, (u + 1) % T::SX_STAGES>{}, sxf[(u + 1) & 1],
                            swf[(u + 1) & 1]);
         }
         if (FULL || s + 1 + T::LT < S)
             dma(s + 1 + T::LT);
-        if constexpr (FP4 && T::scale_loads(u) != 0)
+        if constexpr (FP4 && T::sc_step(u))
             if (FULL || (s + 1) / T::SC_STAGES + T::SC_LEAD < chunks)
-                scale_dma((s + 1) / T::SC_STAGES + T::SC_LEAD);
+                sc_dma((s + 1) / T::SC_STAGES + T::SC_LEAD);
+        if constexpr (FP4 && T::sx_step(u))
+            if (FULL || ((s + 1) / T::SX_STAGES + 1) * T::SX_CH < chunks)
+                sx_dma((s + 1) / T::SX_STAGES + 1);
         if constexpr (!T::WLDS) {
             if (FULL || s + T::LW < S)
                 load_b(s + T::LW, bq[(u + T::LW) % T::NB]);
@@ -690,14 +720,18 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
             constexpr int t = decltype(U)::value;
             load_b(t, bq[t % T::NB]);
         });
-    if constexpr (FP4)
-        scale_dma(0);
+    if constexpr (FP4) {
+        sc_dma(0);
+        sx_dma(0);
+    }
     dma(0);
     static_for<T::LT>([&](auto U) __attribute__((always_inline)) {
         constexpr int v = decltype(U)::value - T::LT;  // virtual step -LT .. -1
         dma(v + 1 + T::LT);
-        if constexpr (FP4 && T::scale_loads(v) != 0)
-            scale_dma((v + 1) / T::SC_STAGES + T::SC_LEAD);
+        if constexpr (FP4 && T::sc_step(v))
+            sc_dma((v + 1) / T::SC_STAGES + T::SC_LEAD);
+        if constexpr (FP4 && T::sx_step(v))
+            sx_dma((v + 1) / T::SX_STAGES + 1);
         if constexpr (!T::WLDS)
             load_b(v + T::LW, bq[(v + T::LW) % T::NB]);
     });
@@ -714,13 +748,14 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
     // Steady state: GROUP unconditional steps while every stage they fetch
     // exists.
     int s0 = 0;
-    for (; s0 + T::GROUP + T::AHEAD <= S; s0 += T::GROUP) {
-        static_for<T::GROUP>([&](auto U) __attribute__((always_inline)) {
+    constexpr int GROUP = FP4 ? T::GROUP4 : T::GROUP;
+    for (; s0 + GROUP + T::AHEAD <= S; s0 += GROUP) {
+        static_for<GROUP>([&](auto U) __attribute__((always_inline)) {
             step(Full{}, s0 + decltype(U)::value, U);
         });
     }
     // Tail: fewer than GROUP + AHEAD stages, each step guarded.
-    static_for<T::GROUP + T::AHEAD>([&](auto U) __attribute__((always_inline)) {
+    static_for<GROUP + T::AHEAD>([&](auto U) __attribute__((always_inline)) {
         if (s0 + decltype(U)::value < S)
             step(Part{}, s0 + decltype(U)::value, U);
     });
