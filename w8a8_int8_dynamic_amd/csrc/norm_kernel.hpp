@@ -34,9 +34,9 @@ using namespace norm_rule;
 // ---- rows held in registers ----
 
 // Sum of v over the WAVES wavefronts of a row, the same in each of them.
-// `part` holds two rounds of WAVES words each, used in turn: a wavefront can
-// reach the next round's write only past this round's barrier, and the one
-// after that only when every wavefront has read this round.
+// `part` holds WAVES words twice, for one exchange and the next in turn: a
+// wavefront can reach the next exchange's write only past this one's barrier,
+// and the one after that only when every wavefront has read this one's words.
 template <int WAVES>
 __device__ __forceinline__ float row_sum(float v, float *part, int &turn)
 {
