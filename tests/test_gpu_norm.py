@@ -277,7 +277,7 @@ def test_many_wide_rows(ops, m, k):
 
 @pytest.mark.parametrize("m,k", [(6, 1536), (7, 1200), (5, 2500), (3, 5120), (7, 5001), (4, 6144), (9, 5200),
                                  (515, 5120), (700, 5001), (520, 1536), (514, 9001), (515, 10240), (2, 16001),
-                                 (514, 12296)])
+                                 (514, 12296), (3, 16384), (1024, 12296), (1025, 12296), (1030, 16384)])
 def test_thread_counts(ops, m, k):
     """The row shapes in between, whole and ragged, few rows and many; the
     residual in place of the stream."""

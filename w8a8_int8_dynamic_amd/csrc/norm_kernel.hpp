@@ -235,7 +235,9 @@ __device__ __forceinline__ void piece_store(char *row, const Piece &p, const flo
 // pass: the wait for the next row's elements then leaves this row's stores in
 // flight.
 constexpr int kOutNone = 0, kOutFloat = 1, kOutCodes = 2;
-template <int XE, int AE, bool RES, int OUT, int CH, int TPR, int R, bool WHOLE>
+// HOLD: the factors stay in registers for the run; otherwise each row makes
+// them again, chunk by chunk.
+template <int XE, int AE, bool RES, int OUT, int CH, int TPR, int R, bool WHOLE, bool HOLD>
 __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a, int64_t per_block)
 {
     constexpr int WAVES = TPR / 64;
@@ -276,13 +278,61 @@ __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a
     };
     fetch(first);
 
-    float g1[CH][8], g0[CH][8], h1[CH][8], h0[CH][8];
+    float g1[HOLD ? CH : 1][8], g0[HOLD ? CH : 1][8], h1[HOLD ? CH : 1][8], h0[HOLD ? CH : 1][8];
+    int64_t gg = 0, ng = 0;                            // the row's groups of the gate and of the next norm
     int turn = 0;
     int64_t row = first, stop = first;                 // the rows before `stop` share the vectors held
     const int64_t last = first + (end - 1 - first) / R * R;
+    // Chunk C's factors of the residual (G) and of the next norm (N), all loads
+    // before the first wait.
+    const void *pw = RES && a.post.kind != kNormNone ? a.post.weight : nullptr;
+    const void *pb = RES && a.post.kind != kNormNone ? a.post.bias : nullptr;
+    auto factors = [&](auto G, auto N, auto C, float (&c1)[8], float (&c0)[8], float (&d1)[8], float (&d0)[8])
+                       __attribute__((always_inline)) {
+        constexpr bool gate = RES && decltype(G)::value, norm = next && decltype(N)::value;
+        const int at = p[decltype(C)::value].at;
+        const char *x = static_cast<const char *>(a.x) + row * a.ldx * XB + (int64_t)at * XB;
+        RawVec vg, vpw, vpb, vw, vb, vs, vt;
+        if constexpr (gate) {
+            vg = vec_load(a.gate, a.gate_kind, gg * a.ld_gate, at, x);
+            vpw = vec_load(pw, a.post.vec_kind, 0, at, x);
+            vpb = vec_load(pb, a.post.vec_kind, 0, at, x);
+        }
+        if constexpr (norm) {
+            vw = vec_load(a.next.weight, a.next.vec_kind, 0, at, x);
+            vb = vec_load(a.next.bias, a.next.vec_kind, 0, at, x);
+            vs = vec_load(a.next.scale, a.next.mod_kind, ng * a.next.ld_scale, at, x);
+            vt = vec_load(a.next.shift, a.next.mod_kind, ng * a.next.ld_shift, at, x);
+        }
+        if constexpr (gate) {
+            float w[8], b[8];
+            vec_values(a.gate, a.gate_kind, vg, 1.0f, c1);
+            vec_values(pw, a.post.vec_kind, vpw, 1.0f, w);
+            vec_values(pb, a.post.vec_kind, vpb, 0.0f, b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float g = a.branch_scale * c1[j];
+                c1[j] = g * w[j];
+                c0[j] = g * b[j];
+            }
+        }
+        if constexpr (norm) {
+            float sc[8], sh[8];
+            vec_values(a.next.weight, a.next.vec_kind, vw, 1.0f, d1);
+            vec_values(a.next.bias, a.next.vec_kind, vb, 0.0f, d0);
+            vec_values(a.next.scale, a.next.mod_kind, vs, 0.0f, sc);
+            vec_values(a.next.shift, a.next.mod_kind, vt, 0.0f, sh);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                d1[j] = d1[j] * (1.0f + sc[j]);
+                d0[j] = fmaf(d0[j], 1.0f + sc[j], sh[j]);
+            }
+        }
+    };
+    using Yes = std::integral_constant<bool, true>;
+    using No = std::integral_constant<bool, false>;
     auto vectors = [&]() __attribute__((always_inline)) {
         stop = end;
-        int64_t gg = 0, ng = 0;
         if (RES && a.gate) {
             gg = (uint32_t)row / (uint32_t)a.gate_rows;
             stop = min(stop, (gg + 1) * a.gate_rows);
@@ -291,49 +341,11 @@ __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a
             ng = (uint32_t)row / (uint32_t)a.next.group_rows;
             stop = min(stop, (ng + 1) * a.next.group_rows);
         }
-        const void *pw = RES && a.post.kind != kNormNone ? a.post.weight : nullptr;
-        const void *pb = RES && a.post.kind != kNormNone ? a.post.bias : nullptr;
-        static_for<CH>([&](auto C) __attribute__((always_inline)) {
-            constexpr int c = decltype(C)::value;
-            const int at = p[c].at;
-            const char *x = static_cast<const char *>(a.x) + row * a.ldx * XB + (int64_t)at * XB;
-            RawVec vg, vpw, vpb, vw, vb, vs, vt;
-            if constexpr (RES) {
-                vg = vec_load(a.gate, a.gate_kind, gg * a.ld_gate, at, x);
-                vpw = vec_load(pw, a.post.vec_kind, 0, at, x);
-                vpb = vec_load(pb, a.post.vec_kind, 0, at, x);
-            }
-            if (next) {
-                vw = vec_load(a.next.weight, a.next.vec_kind, 0, at, x);
-                vb = vec_load(a.next.bias, a.next.vec_kind, 0, at, x);
-                vs = vec_load(a.next.scale, a.next.mod_kind, ng * a.next.ld_scale, at, x);
-                vt = vec_load(a.next.shift, a.next.mod_kind, ng * a.next.ld_shift, at, x);
-            }
-            if constexpr (RES) {
-                float w[8], b[8];
-                vec_values(a.gate, a.gate_kind, vg, 1.0f, g1[c]);
-                vec_values(pw, a.post.vec_kind, vpw, 1.0f, w);
-                vec_values(pb, a.post.vec_kind, vpb, 0.0f, b);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float g = a.branch_scale * g1[c][j];
-                    g1[c][j] = g * w[j];
-                    g0[c][j] = g * b[j];
-                }
-            }
-            if (next) {
-                float sc[8], sh[8];
-                vec_values(a.next.weight, a.next.vec_kind, vw, 1.0f, h1[c]);
-                vec_values(a.next.bias, a.next.vec_kind, vb, 0.0f, h0[c]);
-                vec_values(a.next.scale, a.next.mod_kind, vs, 0.0f, sc);
-                vec_values(a.next.shift, a.next.mod_kind, vt, 0.0f, sh);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    h1[c][j] = h1[c][j] * (1.0f + sc[j]);
-                    h0[c][j] = fmaf(h0[c][j], 1.0f + sc[j], sh[j]);
-                }
-            }
-        });
+        if constexpr (HOLD)
+            static_for<CH>([&](auto C) __attribute__((always_inline)) {
+                constexpr int c = decltype(C)::value;
+                factors(Yes{}, Yes{}, C, g1[c], g0[c], h1[c], h0[c]);
+            });
     };
     auto one_row = [&]() __attribute__((always_inline)) {
         float v[CH][8], b[RES ? CH : 1][8];
@@ -350,24 +362,28 @@ __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a
         if constexpr (RES) {
             if (a.post.kind != kNormNone)
                 normalize<CH, WAVES, WHOLE>(b, p, k_inv, a.post.kind, a.post.eps, part, turn);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
+            static_for<CH>([&](auto C) __attribute__((always_inline)) {
+                constexpr int c = decltype(C)::value, k = HOLD ? c : 0;
+                if constexpr (!HOLD)
+                    factors(Yes{}, No{}, C, g1[0], g0[0], h1[0], h0[0]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    v[c][j] = fmaf(b[c][j], g1[c][j], fmaf(a.residual_scale, v[c][j], g0[c][j]));
+                    v[c][j] = fmaf(b[c][j], g1[k][j], fmaf(a.residual_scale, v[c][j], g0[k][j]));
                 if (WHOLE || p[c].skip < 8)
                     piece_store<XE, WHOLE>(static_cast<char *>(a.r) + row * a.ldr * XB, p[c], v[c]);
-            }
+            });
             if constexpr (!next)
                 return;
         }
         normalize<CH, WAVES, WHOLE>(v, p, k_inv, a.next.kind, a.next.eps, part, turn);
         u32 m = 0;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
+        static_for<CH>([&](auto C) __attribute__((always_inline)) {
+            constexpr int c = decltype(C)::value, k = HOLD ? c : 0;
+            if constexpr (!HOLD)
+                factors(No{}, Yes{}, C, g1[0], g0[0], h1[0], h0[0]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[c][j] = fmaf(v[c][j], h1[c][j], h0[c][j]);
+                v[c][j] = fmaf(v[c][j], h1[k][j], h0[k][j]);
                 if constexpr (OUT == kOutCodes)
                     m = max(m, __float_as_uint(own_or_zero<WHOLE>(p[c], j, v[c][j])) & 0x7fffffffu);
             }
@@ -375,7 +391,7 @@ __global__ __launch_bounds__(TPR * R) void norm_rows_kernel(const NormRowsArgs a
                 store8<AE>(static_cast<char *>(a.out) + row * a.ldo * 2, p[c].at, p[c].at + 8, v[c]);
             else if (OUT == kOutFloat && (WHOLE || p[c].skip < 8))
                 piece_store<AE, WHOLE>(static_cast<char *>(a.out) + row * a.ldo * 2, p[c], v[c]);
-        }
+        });
         if constexpr (OUT != kOutCodes)
             return;
         float sc, inv;
@@ -594,12 +610,12 @@ struct Shape {
 // registers of one workgroup; M4096 K16000 in passes takes 1.4 to 1.8 times as
 // long).
 constexpr int64_t kHeldElements = 16384;
-template <int XE, int AE, bool RES, int OUT, int CH, int TPR, int R>
+template <int XE, int AE, bool RES, int OUT, int CH, int TPR, int R, bool HOLD = true>
 Shape shape(int64_t K)
 {
     static_assert(TPR * R <= (CH > 2 ? 512 : 1024), "a workgroup fits its share of a CU");
-    return {K == CH * TPR * 8 ? norm_rows_kernel<XE, AE, RES, OUT, CH, TPR, R, true>
-                              : norm_rows_kernel<XE, AE, RES, OUT, CH, TPR, R, false>, TPR * R, R,
+    return {K == CH * TPR * 8 ? norm_rows_kernel<XE, AE, RES, OUT, CH, TPR, R, true, HOLD>
+                              : norm_rows_kernel<XE, AE, RES, OUT, CH, TPR, R, false, HOLD>, TPR * R, R,
             (CH > 2 ? 512 : 1024) / (TPR * R)};
 }
 // One chunk per thread as far as 1024 threads reach, where a thread has the
@@ -612,6 +628,12 @@ Shape shape(int64_t K)
 // against 28.9 us, the same of one row 3.5 against 3.2 us; M4096 K6000, the
 // gated residual on 768 threads 37.1, on 1024 44.5 us.
 constexpr int64_t kFewRows = 512;
+// Both norms of a row of two chunks on 1024 threads do not fit the registers:
+// many rows are faster with some of the factors spilled, few with all of them
+// read again (measured on MI355X, K16384 bf16, read again against held: 64 rows
+// 10.8 against 18.1 us, 256 rows 13.2 against 33.4, 999 rows 47.0 against 48.7,
+// 2000 rows 86.5 against 68.8).
+constexpr int64_t kReadAgainRows = 1024;
 template <int XE, int AE, bool RES, int OUT>
 Shape pick(int64_t rows, int64_t K)
 {
@@ -649,6 +671,9 @@ Shape pick(int64_t rows, int64_t K)
         return shape<XE, AE, RES, OUT, 2, 640, 1>(K);
     if (chunks <= 1536)
         return shape<XE, AE, RES, OUT, 3, 512, 1>(K);
+    if constexpr (RES && OUT != kOutNone)
+        if (rows <= kReadAgainRows)
+            return shape<XE, AE, RES, OUT, 2, 1024, 1, false>(K);
     return shape<XE, AE, RES, OUT, 2, 1024, 1>(K);
 }
 
