@@ -133,3 +133,16 @@ def test_refusals():
         W8A8Linear.from_quantized(torch.zeros(1, 16), torch.zeros(1), scheme="fp8")
     with pytest.raises(ValueError, match="GPU"):
         quantize_linear_layers(torch.nn.Linear(64, 64), method="fp4")
+
+
+@pytest.mark.parametrize("scheme", ["int8", "fp8", "fp4"])
+def test_layer_refuses_a_bias_of_another_shape(scheme):
+    """The kernels read out_features elements of the bias, so the layer is not
+    built on any other number of them."""
+    packed = torch.zeros(16 * 64, dtype=torch.uint8)
+    scale = torch.zeros(256, dtype=torch.uint8) if scheme == "fp4" else torch.zeros(16)
+    for shape in ((), (1,), (15,), (17,), (1, 16), (16, 1)):
+        with pytest.raises(ValueError, match="bias"):
+            W8A8Linear(packed, scale, 16, 64, torch.zeros(shape), scheme)
+    layer = W8A8Linear(packed, scale, 16, 64, torch.zeros(32)[::2], scheme)
+    assert layer.bias.shape == (16,) and layer.bias.is_contiguous() and layer.bias_f16.is_contiguous()

@@ -395,3 +395,35 @@ def test_rows_that_hold_nan_next_to_others(ops):
         out, _, s = ops.fp4_quant_scaled_mm(x.to(DEV), *packed, n, bias)
         assert torch.isnan(out[0]).all() and torch.isnan(out[2]).all() and torch.isfinite(out[1]).all()
         assert torch.equal(out[3], bias) and s[0, 0] == 255 and s[2, -1] == 255 and (s[3] == 0).all()
+
+
+def test_layer_checks_its_bias_at_each_call(ops):
+    """A bias whose type, length, stride or device is not what the kernels read is
+    refused, as by the other schemes: after a cast of the layer's floats (the
+    codes stay as they are) and after an assignment."""
+    from w8a8_int8_dynamic_amd import W8A8Linear
+    n, k = 96, 160
+    w, b = rows(n, k, 11, torch.float32).to(DEV), torch.randn(n, generator=torch.Generator().manual_seed(2)).to(DEV)
+    make = lambda: W8A8Linear.from_float(w, b, scheme="fp4")  # noqa: E731
+    x = {dtype: rows(6, k, 12, dtype).to(DEV) for dtype in (torch.bfloat16, torch.float16)}
+    want = {dtype: make()(t) for dtype, t in x.items()}
+    for cast, good in (("float", None), ("half", torch.float16), ("bfloat16", torch.bfloat16), ("double", None)):
+        layer = getattr(make(), cast)()
+        for dtype, t in x.items():
+            if dtype == good:
+                assert torch.equal(layer(t), want[dtype]), cast
+            else:
+                with pytest.raises(ValueError, match="bias"):
+                    layer(t)
+    bf = b.bfloat16()
+    for bad in (bf[:-1], bf[:1], torch.cat((bf, bf)), torch.cat((bf, bf))[::2], bf[None], bf.cpu(), b):
+        layer = make()
+        layer.bias = bad
+        with pytest.raises(ValueError, match="bias|device"):
+            layer(x[torch.bfloat16])
+    layer = make()
+    layer.bias = torch.nn.Parameter(bf)
+    assert torch.equal(layer(x[torch.bfloat16]), want[torch.bfloat16])
+    layer.bias = None
+    out = layer(x[torch.bfloat16])
+    assert torch.equal(out, W8A8Linear.from_float(w, scheme="fp4")(x[torch.bfloat16]))

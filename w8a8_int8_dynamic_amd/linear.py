@@ -39,6 +39,8 @@ class W8A8Linear(torch.nn.Module):
         super().__init__()
         if scheme not in ("int8", "fp8", "fp4"):
             raise ValueError(f"scheme must be 'int8', 'fp8' or 'fp4', got {scheme!r}")
+        if bias is not None and bias.shape != (out_features,):
+            raise ValueError(f"bias must have shape {(out_features,)}, got {tuple(bias.shape)}")
         self.scheme = scheme
         self.in_features = in_features
         self.out_features = out_features
@@ -100,14 +102,12 @@ class W8A8Linear(torch.nn.Module):
             x2 = x2.contiguous()
         # The quant and the scaled matmul, as one library call; the output (and
         # bias) type is x's.
-        if self.scheme == "fp4":
-            dtype, b = x2.dtype, self._buffers
-            if dtype != torch.bfloat16 and dtype != torch.float16:
-                raise TypeError(f"the fp4 scheme takes bfloat16 or float16 activations, got {dtype}")
-            out = ops._fp4_linear(x2, b["w_packed"], b["w_scale"], self.out_features,
-                                  b["bias_f16"] if dtype == torch.float16 else b["bias"])
-            return out if x2 is x else out.reshape(*lead, self.out_features)
         bias = self.bias_f16 if x2.dtype == torch.float16 else self.bias
+        if self.scheme == "fp4":
+            if x2.dtype != torch.bfloat16 and x2.dtype != torch.float16:
+                raise TypeError(f"the fp4 scheme takes bfloat16 or float16 activations, got {x2.dtype}")
+            out = ops._fp4_linear(x2, self.w_packed, self.w_scale, self.out_features, bias)
+            return out if x2 is x else out.reshape(*lead, self.out_features)
         if self.scheme == "fp8":
             if x2.dtype != torch.bfloat16:
                 raise TypeError(f"the fp8 scheme takes bfloat16 activations, got {x2.dtype}")

@@ -685,6 +685,7 @@ def _fp4_linear(x: torch.Tensor, w_packed: torch.Tensor, s_packed: torch.Tensor,
     t, M, K, ld = _float_rows(x, "x")
     _check_fp4_packed(w_packed, s_packed, N, K, x)
     if bias is not None:
+        _vector(bias, N, "bias", x.dtype)
         _same_device(x, bias)
     x, ld = _vector_rows(x, t, ld)
     out = x.new_empty((M, N))
