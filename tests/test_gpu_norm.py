@@ -332,3 +332,37 @@ def test_rows_one_vector_each(ops):
     got_r, *codes = ops.gated_residual_norm_quant(x, y, ops.Norm("rms", **v), gate=gate, residual_scale=0.5)
     ref.check_float(got_r, r, err, F32, "r")
     ref.check_codes(*codes, h, h_err, 127, "codes")
+
+
+@pytest.mark.parametrize("k", [1, 7, 8, 96, 1000, 4096, 12296, 16384, 33000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_mean_squares_below_the_normal_range(ops, dtype, k):
+    """eps = 0 and rows of 2^-66 .. 2^-63, whose squares and their mean are fp32
+    subnormals: norms of about one, whichever kernel the width picks.
+    On top of the reference's bound: each of the K squares, and the mean, is
+    rounded to a multiple of 2^-149, so the mean is off by at most 2^-150 for
+    the squares and 2^-150 for itself; half of that, relative to the mean
+    square, is the deviation's error and so the norm's (taken twice here)."""
+    g = torch.Generator().manual_seed(k)
+    sign = torch.where(torch.rand(4, k, generator=g) < 0.5, -1.0, 1.0)
+    x = (sign * (1 + torch.rand(4, k, generator=g)) * 2.0 ** torch.tensor([[-66.0], [-65], [-64], [-64]]))
+    x = x.to(dtype).to(DEV)
+    z = torch.zeros(4, k, device=DEV, dtype=torch.float64)
+    for kind in ("rms", "layer") if k > 1 else ("rms",):
+        v = x.double()
+        d = v - v.mean(-1, keepdim=True) if kind == "layer" else v
+        low = 2.0 ** -149 / (d * d).mean(-1, keepdim=True)
+        if kind == "layer":
+            assert (low < 2.0 ** -8).all(), "rows of one value have no norm"
+        want, bound = ref.norm(v, z, kind, 0.0)
+        bound = bound + want.abs() * low
+        n = ops.Norm(kind, eps=0.0)
+        ref.check_float(ops.norm(x, n), want, bound, BF, kind)
+        ref.check_codes(*ops.norm_quant_per_token(x, n), want, bound, 127, kind)
+        ref.check_codes(*ops.fp8_norm_quant_per_token(x, n), want, bound, 448, kind)
+        # the same rows as a branch whose norm goes into the stream
+        y = x.bfloat16()
+        p, err = ref.norm(y.double(), z, kind, 0.0)
+        err = err + p.abs() * low * 1.1              # (y's mean square is x's but for its rounding to bf16)
+        ref.check_float(ops.gated_residual(torch.ones_like(y), y, post=n), 1 + p, err + 2 * ref.U * (1 + p.abs()), BF,
+                        "branch")

@@ -194,7 +194,7 @@ __device__ __forceinline__ void normalize(float (&v)[CH][8], const Piece (&p)[CH
             const float d = own_or_zero<WHOLE>(p[c], j, v[c][j]);
             q = fmaf(d, d, q);
         }
-    const float inv = __builtin_amdgcn_rsqf(row_sum<WAVES>(q, part, turn) * k_inv + eps);   // within 1 ulp
+    const float inv = rsqrt_of(row_sum<WAVES>(q, part, turn) * k_inv + eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll

@@ -120,6 +120,15 @@ __device__ __forceinline__ void store8(void *row, int64_t e, int64_t K, const fl
         }
 }
 
+// 1 / sqrt(v) within 1 ulp. v_rsq_f32 takes a subnormal for zero, so one is
+// lifted into the normal range first, by a power of two whose root is exact;
+// other values are multiplied by 1.
+__device__ __forceinline__ float rsqrt_of(float v)
+{
+    const bool low = v < 0x1p-126f;
+    return __builtin_amdgcn_rsqf(low ? v * 0x1p24f : v) * (low ? 0x1p12f : 1.0f);
+}
+
 // Sum over a wavefront, the same in every lane and every run: within rows of
 // 16 lanes by exchanges, then the four row sums in one fixed order.
 __device__ __forceinline__ float wave_sum(float v)
