@@ -366,3 +366,20 @@ def test_mean_squares_below_the_normal_range(ops, dtype, k):
         err = err + p.abs() * low * 1.1              # (y's mean square is x's but for its rounding to bf16)
         ref.check_float(ops.gated_residual(torch.ones_like(y), y, post=n), 1 + p, err + 2 * ref.U * (1 + p.abs()), BF,
                         "branch")
+
+
+def test_no_rows_and_a_vector_for_each(ops):
+    """A batch of no tokens whose modulation and gate come per token: [0, K]."""
+    k = 64
+    x, v = torch.zeros(0, k, dtype=BF, device=DEV), torch.zeros(0, k, device=DEV)
+    n = ops.Norm("layer", scale=v, shift=v)
+    assert ops.norm(x, n).shape == (0, k)
+    q, s = ops.norm_quant_per_token(x, n)
+    assert q.shape == (0, k) and s.shape == (0,)
+    r, h = ops.gated_residual_norm(x, x, n, gate=v)
+    assert r.shape == h.shape == (0, k)
+    assert ops.gated_residual(x, x, gate=v).shape == (0, k)
+    with pytest.raises(ValueError, match="rows"):
+        ops.norm(torch.zeros(3, k, dtype=BF, device=DEV), n)
+    with pytest.raises(ValueError):
+        ops.norm(x, ops.Norm(scale=torch.zeros(0, k + 1, device=DEV)))

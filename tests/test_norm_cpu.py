@@ -112,3 +112,15 @@ def test_reference_by_hand():
     assert torch.allclose(n, torch.tensor([[(-2 * s + 1) * 2 + 0.5, 4 * s], [1.5, 0.0]], dtype=torch.float64))
     r, _ = ref.residual(x, torch.ones_like(x), gate=torch.tensor([2.0, 0.0]), residual_scale=0.5, branch_scale=3.0)
     assert r.tolist() == [[7.5, 2.0], [6.5, 0.5]]
+
+
+def test_groups_of_no_rows():
+    """No rows split into any number of groups, none among them."""
+    ref_rows = torch.zeros(0, 64, dtype=torch.bfloat16)
+    for G in (0, 1, 5):
+        groups, ld = ops._groups(torch.zeros(G, 64), 0, 64, ref_rows, "scale")
+        assert groups >= 1 and ld >= 64
+    with pytest.raises(ValueError, match="rows"):
+        ops._groups(torch.zeros(0, 64), 4, 64, torch.zeros(4, 64), "scale")
+    with pytest.raises(ValueError):
+        ops._groups(torch.zeros(0, 63), 0, 64, ref_rows, "scale")

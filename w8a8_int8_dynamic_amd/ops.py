@@ -766,6 +766,8 @@ def _groups(t: torch.Tensor, M: int, K: int, ref: torch.Tensor, name: str) -> Tu
     if len(shape) == 1:
         return 1, K
     G = shape[0]
+    if M == 0:                                         # any number of groups, as none has a row
+        return 1, K
     if G < 1 or M % G != 0:
         raise ValueError(f"{M} rows do not split into the {G} rows of {name}")
     return G, (t.stride(0) if G > 1 else K)
