@@ -4,6 +4,10 @@ activation_scheme). Argument refusals run on the CPU; the conversion and the
 converted model's forward run on the GPU."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -60,3 +64,19 @@ def test_convert_and_run(method):
     odd = torch.nn.Sequential(torch.nn.Linear(40, 8)).cuda()
     with pytest.raises(ValueError, match="'0'"):
         quantize_linear_layers(odd, method=method)
+
+
+def test_import_on_a_torch_without_gpu_support():
+    """The package loads, and refuses host tensors, where torch has none of its
+    GPU functions."""
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_')]:\n"
+            "    delattr(torch._C, name)\n"
+            "from w8a8_int8_dynamic_amd import ops\n"
+            "try:\n"
+            "    ops.norm(torch.zeros(2, 64, dtype=torch.bfloat16), ops.Norm())\n"
+            "except ValueError as e:\n"
+            "    print(e)\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "device tensor" in r.stdout, r.stderr

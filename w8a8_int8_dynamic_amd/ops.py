@@ -438,8 +438,9 @@ def fp8_quant_scaled_mm(x: torch.Tensor, w_packed: torch.Tensor, ws: Optional[to
 _DTYPE = {torch.bfloat16: _lib.W8A8_T_BF16, torch.float16: _lib.W8A8_T_F16, torch.float32: _lib.W8A8_T_F32}
 _FP4_BLOCK = 32
 _entry = {}
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (absent where torch has no GPU support, as every tensor they are called for)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _run(x: torch.Tensor, name: str, *args, tile: Tuple[int, ...] = ()) -> None:
