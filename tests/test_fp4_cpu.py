@@ -4,6 +4,9 @@ without a GPU fails with W8A8_ERR_DEVICE), the reference rule on values
 worked out by hand, and the layer's refusals."""
 from __future__ import annotations
 
+import os
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -11,6 +14,7 @@ import torch
 from tests import fp4_reference as ref
 from tests.test_abi_cpu import A, ALIGN, DEVICE, HEADER, L, MODE, NULL, OK, SHAPE
 from w8a8_int8_dynamic_amd import W8A8Linear, _lib, ops, quantize_linear_layers
+from w8a8_int8_dynamic_amd.build import CSRC, hipcc
 
 NO_GPU = not torch.cuda.is_available()
 
@@ -146,3 +150,17 @@ def test_layer_refuses_a_bias_of_another_shape(scheme):
             W8A8Linear(packed, scale, 16, 64, torch.zeros(shape), scheme)
     layer = W8A8Linear(packed, scale, 16, 64, torch.zeros(32)[::2], scheme)
     assert layer.bias.shape == (16,) and layer.bias.is_contiguous() and layer.bias_f16.is_contiguous()
+
+
+def test_tiles_that_the_scale_rings_do_not_fit_are_not_compiled(tmp_path):
+    """With two k-groups the second chunk of channel scales is loaded three steps
+    ahead of the loop, so a tile that begins later must not compile."""
+    for tile, fits in (("64, 64, 1, 2, 2, 3, 3", True), ("64, 64, 1, 2, 2, 1, 3", False),
+                       ("64, 64, 2, 2, 1, 1, 3", True)):
+        src = tmp_path / "tile.hip"
+        src.write_text('#include "mm_kernel.hpp"\nnamespace w8a8 { namespace {\n'
+                       f"static_assert(sizeof(Tile<{tile}>) > 0);\n}} }}\n")
+        r = subprocess.run([hipcc(), "--cuda-host-only", "--offload-arch=gfx950", "-std=c++17", "-fsyntax-only", f"-I{CSRC}",
+                            "-I" + os.path.dirname(HEADER), str(src)], capture_output=True, text=True)
+        assert (r.returncode == 0) == fits, (tile, r.stderr[-2000:])
+        assert fits or "scales" in r.stderr, r.stderr[-2000:]

@@ -251,10 +251,21 @@ struct Tile {
     static_assert(VM < 64 && (LT + 1) * LPW < 64 && (LW + 1) * LPW < 64, "vmcnt range");
     static_assert(LDS <= 160 * 1024 && LDS4 <= 160 * 1024, "LDS budget");
     static_assert(LT <= 3 && LW <= 3 && SX_STAGES >= 4 && SC_LEAD * SC_STAGES >= 4, "scales land a slot's stages before their use");
+    // Before the loop the prologue loads slot 0 itself and its LT virtual steps
+    // the rest; the step that loads slot 1 of the channels is one of them.
+    static_assert((SC_LEAD - 1) * SC_STAGES + 1 <= LT, "scales of the first slots are loaded before the loop");
     // Loads that step v issues for the scales.
     static constexpr bool sc_step(int v) { return (v + 1 + 64) % SC_STAGES == 0; }
     static constexpr bool sx_step(int v) { return (v + 1 + 64) % SX_STAGES == 0; }
     static constexpr int scale_loads(int v) { return (sc_step(v) ? SC_LPW : 0) + (sx_step(v) ? SX_LPW : 0); }
+    // ... and those that the LT virtual steps before the loop issue.
+    static constexpr int prologue_scale_loads()
+    {
+        int n = 0;
+        for (int v = -LT; v < 0; ++v)
+            n += scale_loads(v);
+        return n;
+    }
     // VM for the 4-bit kernel at step u (modulo GROUP): the same wait with the
     // scale loads counted (a step issues images, scales, weights).
     static constexpr int vm_fp4(int u)
@@ -735,7 +746,7 @@ __global__ __launch_bounds__(T::THREADS) void scaled_mm_kernel(const MmArgs args
         if constexpr (!T::WLDS)
             load_b(v + T::LW, bq[(v + T::LW) % T::NB]);
     });
-    wait_vm_lgkm0<T::LT * T::LPW + (FP4 ? T::scale_loads(-1) + T::scale_loads(-2) + T::scale_loads(-3) : 0)>();
+    wait_vm_lgkm0<T::LT * T::LPW + (FP4 ? T::prologue_scale_loads() : 0)>();
     __builtin_amdgcn_s_barrier();
     read(0, xf[0]);
     if constexpr (T::WLDS)
