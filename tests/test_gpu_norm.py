@@ -383,3 +383,27 @@ def test_no_rows_and_a_vector_for_each(ops):
         ops.norm(torch.zeros(3, k, dtype=BF, device=DEV), n)
     with pytest.raises(ValueError):
         ops.norm(x, ops.Norm(scale=torch.zeros(0, k + 1, device=DEV)))
+
+
+@pytest.mark.parametrize("k", [96, 100, 4096, 33000])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_rows_beside_one_that_is_not_finite(ops, kind, k):
+    """NaN and infinities stay in their rows: the others' results are, bit for
+    bit, those of a call without them, of each entry point."""
+    m = 9
+    clean, y = rows(m, k, 1), rows(m, k, 2)
+    x, yx = clean.clone(), y.clone()
+    x[2, 5], x[4, k - 1], x[7, 0] = float("nan"), float("inf"), float("-inf")
+    yx[5, k // 2] = float("nan")
+    good, n, p = [0, 1, 3, 6, 8], ops.Norm(kind, scale=vec(k, 3, F32)), ops.Norm(kind)
+    calls = [lambda a, b: (ops.norm(a, n),), lambda a, b: ops.norm_quant_per_token(a, n),
+             lambda a, b: ops.fp8_norm_quant_per_token(a, n), lambda a, b: (ops.gated_residual(a, b, post=p),),
+             lambda a, b: ops.gated_residual_norm(a, b, n, post=p), lambda a, b: ops.gated_residual_norm(a, b, n),
+             lambda a, b: ops.gated_residual_norm_quant(a, b, n, post=p),
+             lambda a, b: ops.fp8_gated_residual_norm_quant(a, b, n)]
+    for i, f in enumerate(calls):
+        for u, v in zip(f(x, yx), f(clean, y)):
+            assert torch.equal(u[good], v[good]), i
+    r, h = ops.gated_residual_norm(x, yx, n, post=p)
+    assert all(not torch.isfinite(t[j]).all() for t in (r, h) for j in (2, 4, 5, 7))
+    assert not torch.isfinite(ops.gated_residual_norm_quant(x, yx, n, post=p)[2][[2, 4, 5, 7]]).any()
