@@ -102,12 +102,20 @@ class W8A8Linear(torch.nn.Module):
             x2 = x2.contiguous()
         # The quant and the scaled matmul, as one library call; the output (and
         # bias) type is x's.
-        bias = self.bias_f16 if x2.dtype == torch.float16 else self.bias
         if self.scheme == "fp4":
-            if x2.dtype != torch.bfloat16 and x2.dtype != torch.float16:
-                raise TypeError(f"the fp4 scheme takes bfloat16 or float16 activations, got {x2.dtype}")
-            out = ops._fp4_linear(x2, self.w_packed, self.w_scale, self.out_features, bias)
+            dtype = x2.dtype
+            if dtype != torch.bfloat16 and dtype != torch.float16:
+                raise TypeError(f"the fp4 scheme takes bfloat16 or float16 activations, got {dtype}")
+            name = "bias_f16" if dtype == torch.float16 else "bias"
+            try:
+                # (a Module's own lookup of a buffer costs about 0.4 us)
+                b = self._buffers
+                args = b["w_packed"], b["w_scale"], self.out_features, b[name]
+            except KeyError:                           # one of them was replaced by a Parameter
+                args = self.w_packed, self.w_scale, self.out_features, getattr(self, name)
+            out = ops._fp4_linear(x2, *args)
             return out if x2 is x else out.reshape(*lead, self.out_features)
+        bias = self.bias_f16 if x2.dtype == torch.float16 else self.bias
         if self.scheme == "fp8":
             if x2.dtype != torch.bfloat16:
                 raise TypeError(f"the fp8 scheme takes bfloat16 activations, got {x2.dtype}")

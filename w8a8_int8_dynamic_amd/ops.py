@@ -685,7 +685,8 @@ def _fp4_linear(x: torch.Tensor, w_packed: torch.Tensor, s_packed: torch.Tensor,
     they go through one buffer)."""
     t, M, K, ld = _float_rows(x, "x")
     _check_fp4_packed(w_packed, s_packed, N, K, x)
-    if bias is not None:
+    if bias is not None and (bias.dtype != x.dtype or bias.size() != (N,) or not bias.is_contiguous() or
+                             bias.get_device() != x.get_device()):
         _vector(bias, N, "bias", x.dtype)
         _same_device(x, bias)
     x, ld = _vector_rows(x, t, ld)
