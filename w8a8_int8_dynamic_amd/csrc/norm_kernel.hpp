@@ -15,11 +15,12 @@
 // Rows too long for that take norm_rows_looped_kernel, one workgroup a row,
 // which reads the row again (from L2) for each of its passes. Neither writes
 // an element before it has read it for the last time, so r may be x itself.
-// Measured on MI355X, bf16, from rotating buffers: M8192 K4096 layer norm with
-// scale and shift 25.6 us (5.2 TB/s; a large copy makes 5.1); M8192 K12288 rms to
-// e4m3 codes 56.5 us (5.3); M8192 K4096 gated residual with post norm and next
-// norm 44.4 us (6.0); M999 K5001 fp16 into an fp32 stream 13.4 us (3.7: four
-// rows to a workgroup); one row of 4096 to int8 codes 3.1 us.
+// Measured on MI355X, bf16, from rotating buffers (median and range of a trace;
+// a copy kernel makes 6.05 TB/s over 0.5 GB): M8192 K4096 layer norm with scale
+// and shift 25.7 us (24.7-27.7; 5.2 TB/s); M8192 K12288 rms to e4m3 codes 58.3 us
+// (56.0-61.7; 5.2); M8192 K4096 gated residual with post norm and next norm 44.4
+// us (43.8-47.0; 6.0); M999 K5001 fp16 into an fp32 stream 15.1 us (13.2-15.8;
+// 3.3: four rows to a workgroup); one row of 4096 to int8 codes 3.1 us.
 #pragma once
 
 #include <algorithm>

@@ -13,11 +13,12 @@
 // as long over them.
 //
 // What bounds it, measured on MI355X. M512 N12288 K4096 (128x192 tiles, one
-// round of 256 workgroups): 20.2 us, 2.55 PFLOP/s; of it the loop 12.9 us, at
+// round of 256 workgroups): 20.5 us, 2.5 PFLOP/s; of it the loop 12.9 us, at
 // 653-730 cycles per k-block where the MFMAs are 384: the 21.5 KB that a CU
-// reads for one pass at about 31 bytes a cycle, near what the path from L2
-// gives; then 2.8 us of first loads and 2.2 of stores. M8192 N4096 K12288
-// (256x256, two rounds): 188-203 us, 4.1-4.4 PFLOP/s; 1310-1377 cycles per
+// reads for one, at about 31 bytes a cycle. The int8 loop over the same operand
+// bytes takes 10 to 20 % less: the rest is the loads of the block scales.
+// Then 2.8 us of first loads and 2.2 of stores. M8192 N4096 K12288
+// (256x256, two rounds): 188-204 us, 4.0-4.4 PFLOP/s; 1310-1377 cycles per
 // k-block where the MFMAs are 1024, at 1.45-1.8 GHz, the clock that power
 // leaves for random codes (the MFMAs alone, from registers, make 5.9-6.4
 // PFLOP/s of those, 9.0 of zeros).
@@ -59,8 +60,9 @@ const char *fp4_tile_name(int tile) { return fp4_entry(tile).name; }
 //   small-M: fixed + per workgroup and k-block + per chunk of 512 elements in
 //            a wave's chain, for up to 256 token rows.
 // The rates (us) are fitted to the times of every tile on 643 shapes (M 8-8192,
-// N 512-12288, K 512-12288, weights from HBM) on MI355X; over them the chosen
-// tile takes 0.9 % more than the best on average, 21 % at most.
+// N 512-12288, K 512-12288, weights from HBM) on MI355X, by
+// tests/probes/fp4_tile_grid.py; over them the chosen tile takes 1.3 % more than
+// the best on average, 23 % at most.
 struct MainCost {
     double fixed, kblock, round, weight, out;
 };

@@ -21,7 +21,8 @@
 //     this, M 16 K 512 (two steps) 4.7 against 3.5 us, M 8 K 2048 (four) 5.3
 //     against 4.3, M 16 K 2048 (eight) 5.4 against 5.9. One row, N 12288, K
 //     4096: a row quantized by each lane in place of its own operand takes 10.6
-//     us, this 6.5, two launches 8.7.
+//     us, this 6.5 to 8.0 (7.3 in the median of a trace, 3.7 TB/s of weights),
+//     two launches 8.7.
 // Ragged tails: token rows past M read row M-1 and channels past N the last
 // image (never stored); blocks past the row's last read the last one again, as
 // 1.0-scaled operands of zero weights.

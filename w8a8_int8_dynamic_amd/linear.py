@@ -133,7 +133,8 @@ class W8A8Linear(torch.nn.Module):
         ops that end in quant_per_token for "int8" and "fp8", by
         fp4_quant_per_block for "fp4"): codes [M, K] (fp4: [M, K/2]) and their
         scales to [M, N] in out_dtype (bf16 or fp16). It uses no workspace of the
-        layer, so calls on several streams may run at once."""
+        layer, so calls on several streams may run at once; ops.scaled_mm takes
+        one for a split of K at few rows (scheme "int8")."""
         if out_dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"out_dtype must be bfloat16 or float16, got {out_dtype}")
         K = xq.shape[-1] * (2 if self.scheme == "fp4" else 1)

@@ -894,7 +894,8 @@ def gated_residual(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor
     """A block's output y [M, K] (bf16 or fp16) back into the residual stream x
     (y's type or fp32): residual_scale * x + branch_scale * gate * post(y), in
     x's type. gate: [K] or [G, K] as a Norm's scale (None: 1). post: a Norm
-    with weight and bias, or None (y itself). out may be x itself."""
+    with weight and bias, or None (y itself). out may be x itself; otherwise it
+    shares no memory with the other tensors."""
     return _residual_call(x, y, None, _lib.W8A8_NORM_OUT_16, gate, post, residual_scale, branch_scale, out)[0]
 
 
