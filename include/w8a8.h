@@ -13,7 +13,9 @@
  * the quant and the matmul in one call (int8_quant_scaled_mm), fp16
  * activations and outputs, the online weight quant straight into the
  * repacked layout, an FP8 (e4m3) twin of the whole path, a microscaled 4-bit
- * (MX FP4) layer, and the norms and gated residuals around such layers.
+ * (MX FP4) layer, an e4m3 layer with a scale per block of 128, a mixture of
+ * experts on it with its routing, and the norms and gated residuals around
+ * such layers.
  *
  * Conventions for every entry point:
  *   - Pointers to tensors are DEVICE pointers on the current HIP device.
@@ -548,6 +550,172 @@ w8a8_status_t fp4_quant_scaled_mm_tile(const void *x, int x_dtype, int64_t ldx, 
 int w8a8_fp4_tile_count(void);
 const char *w8a8_fp4_tile_name(int tile);
 int w8a8_fp4_tile_auto(int64_t M, int64_t N, int64_t K);
+
+/*
+ * ---- Block-scaled 8-bit floating point (e4m3, one scale per 128) ----
+ * The FP8 twin with a finer grid of scales: activations carry one fp32 scale
+ * per 128 elements along K, weights one per 128 x 128 block, so that an
+ * outlier costs precision to its own block alone. Over a block
+ *   a = max |x|;  a < 2^-100: scale 0, codes 0;
+ *   else scale = fl32(a / 448), q = e4m3(clamp(fl32(x * f), +-448)),
+ *        f = fl32(448 * fl32(1 / a)),
+ * the rule of fp8_quant_per_token but for the factor's last bit. K is a multiple of 16, in [16,
+ * W8A8_MAX_K]; the last block of a row or channel group may be part full.
+ *
+ * fp8_quant_per_block - rows x [M, ldx] (x_dtype) to e4m3 codes xq [M, ldq]
+ * and scales x_scale [M, lds] (ceil(K/128) a row). A block that holds an
+ * infinity or NaN gets a scale that is not finite.
+ * fp8_block_dequant - codes and scales back to the values they stand for,
+ * code * scale rounded once to out_dtype.
+ * Requirements: M >= 0 (0 is a no-op); rows of x and out 16-byte aligned (ld
+ * a multiple of 8, of 4 for fp32); codes 8-byte aligned, ldq a multiple of 8.
+ */
+w8a8_status_t fp8_quant_per_block(const void *x, int x_dtype, int64_t M, int64_t K, int64_t ldx,
+                                  uint8_t *xq, int64_t ldq, float *x_scale, int64_t lds,
+                                  void *stream);
+w8a8_status_t fp8_block_dequant(const uint8_t *xq, int64_t ldq, const float *x_scale, int64_t lds,
+                                int64_t M, int64_t K, int out_dtype, void *out, int64_t ldo,
+                                void *stream);
+
+/* Bytes of the packed form of `experts` weights [N, K] (1 for a layer): N
+ * rounded up to 16 times K rounded up to 128 for each; 0 when out of range. */
+size_t fp8_block_prepack_weight_bytes(int64_t experts, int64_t N, int64_t K);
+
+/*
+ * fp8_block_prepack_weight - load-time repack of weights quantized before:
+ * codes wq, `experts` matrices [N, ldq] one behind the other (no alignment
+ * rule). Their scales [experts, scale rows, ceil(K/128)] stay as they are.
+ * gated: a matrix holds the gate rows, then as many up rows (N a multiple of
+ * 32), and each half has scale rows of its own: 2 * ceil(N/2/128) of them,
+ * otherwise ceil(N/128).
+ * fp8_block_quant_prepack_weight - the quant rule applied to bf16 or fp32
+ * weights w [experts][N, ldw] (w_dtype: W8A8_W_*), written straight into the
+ * packed form, with the scales. Rows 16-byte aligned, ldw a multiple of 8 (4
+ * for fp32).
+ * fp8_block_unpack_weight - the inverse of both repacks.
+ * Requirements: w_packed 16-byte aligned and as long as the function above says.
+ */
+w8a8_status_t fp8_block_prepack_weight(const uint8_t *wq, int64_t ldq, int64_t experts, int64_t N,
+                                       int64_t K, int gated, void *w_packed, void *stream);
+w8a8_status_t fp8_block_quant_prepack_weight(const void *w, int w_dtype, int64_t ldw,
+                                             int64_t experts, int64_t N, int64_t K, int gated,
+                                             void *w_packed, float *w_scale, void *stream);
+w8a8_status_t fp8_block_unpack_weight(const void *w_packed, int64_t experts, int64_t N, int64_t K,
+                                      int gated, uint8_t *wq, int64_t ldq, void *stream);
+
+/*
+ * fp8_block_scaled_mm - the product of quantized rows with a packed weight:
+ *   acc[m,n] = sum over blocks b of x_scale[m,b] * w_scale[n/128,b] *
+ *              sum over k in b of e4m3(xq[m,k]) * e4m3(wq[n,k])
+ * a block's sum as the e4m3 matrix instruction gives it, the sum over blocks
+ * in fp32;
+ *   W8A8_OUT_BF16 / W8A8_OUT_F16: acc + bias[n] (bias in the output's type,
+ *   or NULL) in fp32, rounded to nearest even;  W8A8_OUT_I32: acc as fp32.
+ * Requirements: M >= 0 (0 is a no-op), N >= 1, K <= ldq <= W8A8_MAX_LDQ,
+ * ceil(K/128) <= lds <= W8A8_MAX_LDQ, ldo >= N; xq and w_packed 16-byte
+ * aligned, ldq a multiple of 16; the others aligned to their element size.
+ * w_scale [ceil(N/128), ceil(K/128)] without gaps.
+ * fp8_block_quant_scaled_mm - fp8_quant_per_block of x [M, ldx], then
+ * fp8_block_scaled_mm of the result, in one call; xq and x_scale are written.
+ * ..._tile: with an explicit tile (0 <= tile < w8a8_fp8_block_tile_count()) or
+ * -1. Tiles may differ in the order of their fp32 sums.
+ */
+w8a8_status_t fp8_block_scaled_mm(const uint8_t *xq, int64_t ldq, const float *x_scale, int64_t lds,
+                                  const void *w_packed, const float *w_scale, const uint16_t *bias,
+                                  int64_t M, int64_t N, int64_t K, int mode, void *out, int64_t ldo,
+                                  void *stream);
+w8a8_status_t fp8_block_scaled_mm_tile(const uint8_t *xq, int64_t ldq, const float *x_scale,
+                                       int64_t lds, const void *w_packed, const float *w_scale,
+                                       const uint16_t *bias, int64_t M, int64_t N, int64_t K,
+                                       int mode, void *out, int64_t ldo, void *stream, int tile);
+w8a8_status_t fp8_block_quant_scaled_mm(const void *x, int x_dtype, int64_t ldx, uint8_t *xq,
+                                        int64_t ldq, float *x_scale, int64_t lds,
+                                        const void *w_packed, const float *w_scale,
+                                        const uint16_t *bias, int64_t M, int64_t N, int64_t K,
+                                        int mode, void *out, int64_t ldo, void *stream);
+w8a8_status_t fp8_block_quant_scaled_mm_tile(const void *x, int x_dtype, int64_t ldx, uint8_t *xq,
+                                             int64_t ldq, float *x_scale, int64_t lds,
+                                             const void *w_packed, const float *w_scale,
+                                             const uint16_t *bias, int64_t M, int64_t N, int64_t K,
+                                             int mode, void *out, int64_t ldo, void *stream,
+                                             int tile);
+
+/* Tiles of the block-scaled matmul: their number, a name of each, and the
+ * automatic choice. */
+int w8a8_fp8_block_tile_count(void);
+const char *w8a8_fp8_block_tile_name(int tile);
+int w8a8_fp8_block_tile_auto(int64_t M, int64_t N, int64_t K);
+
+/*
+ * ---- A mixture of experts on the block-scaled layer ----
+ * Routing: from a router's logits to the experts of each token.
+ *   score_e  = softmax(logits)_e, or 1 / (1 + e^-logit_e)
+ *   choice_e = score_e + bias_e
+ *   with groups > 1: the experts stand in that many equal groups, a group's
+ *   worth is the sum of its group_top (1 or 2) largest choices, and the
+ *   top_groups best groups stay;
+ *   ids = the top_k experts by choice among those that stayed, the best
+ *   first;  weights = their scores, over their sum with renormalize, times
+ *   scale.
+ * Ties go to the lowest index. An expert whose logit (or bias) is NaN or
+ * -infinity is left out; a row with fewer than top_k experts left ends in
+ * ids -1 with weight 0. Scores, sums and choices are computed in 64 bits.
+ */
+typedef enum w8a8_score {
+    W8A8_SCORE_SOFTMAX = 0,
+    W8A8_SCORE_SIGMOID = 1
+} w8a8_score_t;
+
+typedef struct w8a8_routing {
+    const float *bias;      /* [experts] or NULL */
+    int score;              /* w8a8_score_t */
+    int top_k;              /* 1 .. 64, at most the experts of top_groups groups */
+    int groups;             /* 1 .. 64, a divisor of the number of experts */
+    int top_groups;         /* 1 .. groups */
+    int group_top;          /* 1 or 2 */
+    int renormalize;        /* 0 or 1 */
+    float scale;            /* finite */
+} w8a8_routing_t;
+
+/*
+ * route_experts - logits [tokens, ld] (dtype) over `experts` (1 .. 1024)
+ * experts to ids and weights [tokens, top_k].
+ */
+w8a8_status_t route_experts(const void *logits, int dtype, int64_t ld, int64_t tokens, int experts,
+                            const w8a8_routing_t *routing, int32_t *ids, float *weights,
+                            void *stream);
+
+/* The experts' weights: gate and up as one gated packed weight [2 * inner, K]
+ * per expert, down [K, inner], with their block scales. */
+typedef struct w8a8_experts {
+    const void *gate_up;
+    const float *gate_up_scale;   /* [experts, 2 * ceil(inner/128), ceil(K/128)] */
+    const void *down;
+    const float *down_scale;      /* [experts, ceil(K/128), ceil(inner/128)] */
+    int64_t K;
+    int64_t inner;
+    int experts;                  /* 1 .. 1024 */
+} w8a8_experts_t;
+
+/*
+ * fp8_block_experts - for each token t with experts e_j = ids[t,j] and weights
+ * w_j (any number of them alike; an id outside [0, experts) stands for none)
+ *   h_j = silu(gate_e x) * (up_e x)   in fp32, silu(v) = v / (1 + e^-v)
+ *   out_t = sum over j of w_j * down_e q(h_j)   in fp32, rounded once
+ * where x and h pass through fp8_quant_per_block's codes. x [tokens, ldx] and
+ * out [tokens, ldo] in x_dtype; ids and weights [tokens, top_k].
+ * Requirements: tokens >= 0 (0 is a no-op); K and inner multiples of 16 in
+ * [16, W8A8_MAX_K]; top_k 1 .. 64; rows of x and out 16-byte aligned (ld a
+ * multiple of 8, of 4 for fp32); the workspace 256-byte aligned and as long as
+ * the function below says (0: out of range), of any content and free for
+ * other use once the stream has passed the call.
+ */
+size_t fp8_block_experts_workspace_bytes(int64_t tokens, int64_t K, int64_t inner, int experts,
+                                         int top_k);
+w8a8_status_t fp8_block_experts(const w8a8_experts_t *layer, const void *x, int x_dtype,
+                                int64_t ldx, int64_t tokens, const int32_t *ids,
+                                const float *weights, int top_k, void *out, int64_t ldo,
+                                void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * ---- Norms around a layer ----

@@ -36,8 +36,14 @@ W8A8_NORM_OUT_INT8 = 1
 W8A8_NORM_OUT_FP8 = 2
 
 
-# w8a8_norm_t and w8a8_residual_t, packed in the C layout (passed as bytes)
+W8A8_SCORE_SOFTMAX = 0
+W8A8_SCORE_SIGMOID = 1
+
+# w8a8_norm_t, w8a8_residual_t, w8a8_routing_t and w8a8_experts_t, packed in the
+# C layout (passed as bytes)
 NORM_STRUCT = struct.Struct("@if4P3q2i")
+ROUTING_STRUCT = struct.Struct("@P6if4x")
+EXPERTS_STRUCT = struct.Struct("@4P2qi4x")
 RESIDUAL_STRUCT = struct.Struct("@3P3qP2q2f3i4x")
 
 # name -> (restype, argtypes), in the order of include/w8a8.h
@@ -98,6 +104,27 @@ SIGNATURES = {
                                    _i64, _int, _vp, _i64, _vp]),
     "fp4_quant_scaled_mm_tile": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
                                         _i64, _i64, _int, _vp, _i64, _vp, _int]),
+    "fp8_quant_per_block": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "fp8_block_dequant": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _int, _vp, _i64, _vp]),
+    "fp8_block_prepack_weight_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "fp8_block_prepack_weight": (_int, [_vp, _i64, _i64, _i64, _i64, _int, _vp, _vp]),
+    "fp8_block_quant_prepack_weight": (_int, [_vp, _int, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp]),
+    "fp8_block_unpack_weight": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _i64, _vp]),
+    "fp8_block_scaled_mm": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp,
+                                   _i64, _vp]),
+    "fp8_block_scaled_mm_tile": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _int,
+                                        _vp, _i64, _vp, _int]),
+    "fp8_block_quant_scaled_mm": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
+                                         _i64, _i64, _int, _vp, _i64, _vp]),
+    "fp8_block_quant_scaled_mm_tile": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                              _i64, _i64, _i64, _int, _vp, _i64, _vp, _int]),
+    "w8a8_fp8_block_tile_count": (_int, []),
+    "w8a8_fp8_block_tile_name": (ctypes.c_char_p, [_int]),
+    "w8a8_fp8_block_tile_auto": (_int, [_i64, _i64, _i64]),
+    "route_experts": (_int, [_vp, _int, _i64, _i64, _int, _vp, _vp, _vp, _vp]),
+    "fp8_block_experts_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64, _int, _int]),
+    "fp8_block_experts": (_int, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _int, _vp, _i64, _vp,
+                                 ctypes.c_size_t, _vp]),
     "norm_rows": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _int, _vp, _i64, _vp, _vp]),
     "gated_residual_rows": (_int, [_vp, _vp, _i64, _i64, _vp, _int, _vp, _i64, _vp, _vp]),
     "w8a8_fp4_tile_count": (_int, []),

@@ -1,0 +1,250 @@
+// The mixture of experts: for each token t with chosen experts e_j and weights
+// w_j (an id outside [0, experts) stands for no expert)
+//   h_j = silu(gate_e x) * (up_e x)                     fp32
+//   out_t = sum over j of w_j * down_e q(h_j)           fp32, rounded once
+// with x and h as block-scaled e4m3 rows (fp8_block_rule.hpp) and the experts'
+// weights block-scaled e4m3 matrices.
+//
+// The plan sets the slots (token, choice) out by expert, so that each expert's
+// rows are one run, cut into row tiles; the products then run over all
+// experts' tiles in one launch each, the first gathering its rows by token,
+// the second scattering them back to slots. The sum over a token's slots comes
+// last, in the slots' order, so that no result depends on an order of atomics.
+#include <algorithm>
+
+#include "experts.hpp"
+#include "fp8_block_device.hpp"
+
+namespace w8a8 {
+namespace {
+
+using namespace fp8_block;
+
+constexpr int kPlanThreads = 1024;
+
+// One workgroup per expert: where its rows begin (the slots of lower experts
+// come first), its slots in ascending order, and its row tiles. Every
+// workgroup counts all experts by itself (LDS counters: their sums do not
+// depend on the order), so that none waits for another. The last one marks the
+// launch's remaining row tiles as empty.
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int *__restrict__ ids, int slots, int experts,
+                                                            int bm, int *__restrict__ order,
+                                                            BlockTile *__restrict__ tiles, int tiles_m)
+{
+    __shared__ int count[kMaxExperts];
+    __shared__ int sums[2];
+    __shared__ int in_wave[kPlanThreads / 64];
+    const int t = threadIdx.x, e = blockIdx.x, wave = t >> 6;
+    if (t < experts)
+        count[t] = 0;
+    if (t < 2)
+        sums[t] = 0;
+    __syncthreads();
+    for (int i = t; i < slots; i += kPlanThreads) {
+        const int id = ids[i];
+        if (id >= 0 && id < experts)
+            atomicAdd(&count[id], 1);
+    }
+    __syncthreads();
+    if (t < e) {
+        atomicAdd(&sums[0], count[t]);
+        atomicAdd(&sums[1], (count[t] + bm - 1) / bm);
+    }
+    __syncthreads();
+    const int first = sums[0], tile0 = sums[1], rows = count[e], mine = (rows + bm - 1) / bm;
+    for (int i = t; i < mine; i += kPlanThreads)
+        tiles[tile0 + i] = BlockTile{e, first + i * bm, min(bm, rows - i * bm)};
+    if (e == experts - 1)
+        for (int i = tile0 + mine + t; i < tiles_m; i += kPlanThreads)
+            tiles[i] = BlockTile{-1, 0, 0};
+    if (rows == 0)
+        return;
+    int at = first;
+    for (int i0 = 0; i0 < slots; i0 += kPlanThreads) {
+        const int i = i0 + t;
+        const bool hit = i < slots && ids[i] == e;
+        const unsigned long long mask = __ballot(hit);
+        if ((t & 63) == 0)
+            in_wave[wave] = __popcll(mask);
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 64; ++w) {
+            before += w < wave ? in_wave[w] : 0;
+            all += in_wave[w];
+        }
+        if (hit)
+            order[at + before + __popcll(mask & ((1ull << (t & 63)) - 1))] = i;
+        at += all;
+        __syncthreads();
+    }
+}
+
+// out[t] = sum over the token's slots of weight * y[slot]: four columns a
+// thread. A slot without an expert has no row.
+template <int E>
+__global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ y, const int *__restrict__ ids,
+                                                      const float *__restrict__ weights, int top_k, int experts,
+                                                      int K, void *__restrict__ out, int64_t ldo, int segs)
+{
+    const int64_t token = blockIdx.x / segs;
+    const int col = ((int)(blockIdx.x - token * segs) * 256 + (int)threadIdx.x) * 4;
+    if (col >= K)
+        return;
+    f32x4 acc = {};
+    for (int j = 0; j < top_k; ++j) {
+        const int64_t slot = token * top_k + j;
+        const int id = ids[slot];
+        if (id < 0 || id >= experts)
+            continue;
+        const float w = weights[slot];
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(y + slot * K + col);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            acc[r] = __builtin_fmaf(w, v[r], acc[r]);
+    }
+    if constexpr (E == kF32)
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(out) + token * ldo + col) = acc;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + token * ldo + col) =
+            make_uint2(pack2<E == kF16>(acc[0], acc[1]), pack2<E == kF16>(acc[2], acc[3]));
+}
+
+// Tokens of one pass: what bounds the workspace and keeps every row offset of
+// the codes within 31 bits.
+int64_t tokens_at_once(int64_t tokens, int top_k, int64_t K)
+{
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(65536 / top_k, (int64_t(1) << 30) / K));
+    return std::min(tokens, most);
+}
+
+struct Layout {
+    size_t xq, xs, order, tiles, hq, hs, h, y, end;
+    int64_t tiles_m;
+};
+
+Layout layout_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner, int bm)
+{
+    Layout l;
+    const int64_t slots = tokens * top_k;
+    l.tiles_m = slots / bm + std::min<int64_t>(experts, slots);
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t p = at;
+        at += (size_t)round_up(bytes, 256);
+        return p;
+    };
+    l.xq = take(tokens * K);
+    l.xs = take(tokens * ceil_div(K, kBlock) * 4);
+    l.order = take(slots * 4);
+    l.tiles = take(l.tiles_m * (int64_t)sizeof(BlockTile));
+    l.hq = take(slots * inner);
+    l.hs = take(slots * ceil_div(inner, kBlock) * 4);
+    l.h = take(slots * inner * 4);
+    l.y = take(slots * K * 4);
+    l.end = at;
+    return l;
+}
+
+}  // namespace
+
+size_t experts_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
+{
+    const BlockTileEntry &e = fp8_block_small(0);
+    return layout_of(tokens_at_once(tokens, top_k, K), top_k, experts, K, inner, e.bm).end;
+}
+
+bool experts_fit(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
+{
+    const BlockTileEntry &e = fp8_block_small(0);
+    const int64_t step = tokens_at_once(tokens, top_k, K);
+    const int64_t tiles_m = step * top_k / e.bm + std::min<int64_t>(experts, step * top_k);
+    return mm_grid_fits(tiles_m * ceil_div(std::max(2 * inner, K), e.bn), e.threads);
+}
+
+hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t stream)
+{
+    const BlockTileEntry &e = fp8_block_small(0);
+    const int64_t step = tokens_at_once(args.tokens, args.top_k, args.K);
+    const Layout l = layout_of(step, args.top_k, args.experts, args.K, args.inner, e.bm);
+    char *work = static_cast<char *>(workspace);
+    const int x_bytes = args.kind == kElemF32 ? 4 : 2;
+    const int blocks = (int)ceil_div(args.K, kBlock), inner_blocks = (int)ceil_div(args.inner, kBlock);
+    uint8_t *xq = reinterpret_cast<uint8_t *>(work + l.xq), *hq = reinterpret_cast<uint8_t *>(work + l.hq);
+    float *xs = reinterpret_cast<float *>(work + l.xs), *hs = reinterpret_cast<float *>(work + l.hs);
+    float *h = reinterpret_cast<float *>(work + l.h), *y = reinterpret_cast<float *>(work + l.y);
+    int *order = reinterpret_cast<int *>(work + l.order);
+    BlockTile *tiles = reinterpret_cast<BlockTile *>(work + l.tiles);
+
+    for (int64_t t0 = 0; t0 < args.tokens; t0 += step) {
+        const int64_t tokens = std::min(args.tokens - t0, step);
+        const int slots = (int)(tokens * args.top_k);
+        const int *ids = args.ids + t0 * args.top_k;
+        hipError_t err = launch_quant_fp8_block(static_cast<const char *>(args.x) + t0 * args.ldx * x_bytes, args.kind,
+                                                tokens, args.K, args.ldx, xq, args.K, xs, blocks, stream);
+        if (err != hipSuccess)
+            return err;
+        const int tiles_m = (int)(slots / e.bm + std::min(args.experts, slots));
+        hipLaunchKernelGGL(plan_kernel, dim3(args.experts), dim3(kPlanThreads), 0, stream, ids, slots, args.experts,
+                           e.bm, order, tiles, tiles_m);
+
+        BlockMmArgs m{};
+        m.tiles = tiles;
+        m.tiles_m = tiles_m;
+        m.order = order;
+        m.top_k = args.top_k;
+        m.vec_store = 1;
+        m.xq = xq;
+        m.xs = xs;
+        m.ldq = args.K;
+        m.lds = blocks;
+        m.wp = args.gate_up;
+        m.ws = args.gate_up_scale;
+        m.out = h;
+        m.ldo = args.inner;
+        m.M = slots;
+        m.N = (int)(2 * args.inner);
+        m.K = (int)args.K;
+        m.blocks = blocks;
+        m.frags = (int)fp8_block_frags(m.N, true);
+        m.half_scales = inner_blocks;
+        m.expert_bytes = (int64_t)m.frags * blocks * kFrag;
+        m.expert_scales = (int64_t)2 * inner_blocks * blocks;
+        hipLaunchKernelGGL(e.gate_up, dim3((unsigned)(tiles_m * ceil_div(m.frags, e.bn / 16))), dim3(e.threads), 0,
+                           stream, m);
+        err = launch_quant_fp8_block(h, kElemF32, slots, args.inner, args.inner, hq, args.inner, hs, inner_blocks,
+                                     stream);
+        if (err != hipSuccess)
+            return err;
+        m.xq = hq;
+        m.xs = hs;
+        m.ldq = args.inner;
+        m.lds = inner_blocks;
+        m.wp = args.down;
+        m.ws = args.down_scale;
+        m.out = y;
+        m.ldo = args.K;
+        m.N = (int)args.K;
+        m.K = (int)args.inner;
+        m.blocks = inner_blocks;
+        m.frags = (int)fp8_block_frags(m.N, false);
+        m.half_scales = 0;
+        m.expert_bytes = (int64_t)m.frags * inner_blocks * kFrag;
+        m.expert_scales = fp8_block_scale_rows(m.N, false) * inner_blocks;
+        hipLaunchKernelGGL(e.down, dim3((unsigned)(tiles_m * ceil_div(m.frags, e.bn / 16))), dim3(e.threads), 0,
+                           stream, m);
+
+        const int segs = (int)ceil_div(args.K, 1024);
+        auto combine = args.kind == kElemF32 ? combine_kernel<kF32>
+                     : args.kind == kElemF16 ? combine_kernel<kF16> : combine_kernel<kBF16>;
+        hipLaunchKernelGGL(combine, dim3((unsigned)(tokens * segs)), dim3(256), 0, stream, y, ids,
+                           args.weights + t0 * args.top_k, args.top_k, args.experts, (int)args.K,
+                           static_cast<char *>(args.out) + t0 * args.ldo * x_bytes, args.ldo, segs);
+        err = hipGetLastError();
+        if (err != hipSuccess)
+            return err;
+    }
+    return hipSuccess;
+}
+
+}  // namespace w8a8

@@ -1,0 +1,79 @@
+// Declarations shared by the translation units of the block-scaled 8-bit layer
+// and the mixture of experts.
+#pragma once
+
+#include "internal.hpp"
+
+namespace w8a8 {
+
+// Packed fragments (16 channels) and scale rows (128 channels) of a weight of
+// N rows; gated: N = 2I rows, each half with fragments and scale rows of its own.
+inline int64_t fp8_block_frags(int64_t N, bool gated) { return gated ? 2 * ceil_div(N / 2, 16) : ceil_div(N, 16); }
+inline int64_t fp8_block_scale_rows(int64_t N, bool gated)
+{
+    return gated ? 2 * ceil_div(N / 2, 128) : ceil_div(N, 128);
+}
+
+// ---- rows and weights (quant_fp8_block.hip) ----
+// K is a multiple of 16; rows of x and out 16-byte aligned, codes 8-byte.
+hipError_t launch_quant_fp8_block(const void *x, int kind, int64_t rows, int64_t K, int64_t ldx, uint8_t *q,
+                                  int64_t ldq, float *s, int64_t lds, hipStream_t stream);
+hipError_t launch_dequant_fp8_block(const uint8_t *q, int64_t ldq, const float *s, int64_t lds, int64_t rows,
+                                    int64_t K, int kind, void *out, int64_t ldo, hipStream_t stream);
+// `experts` weights [N, ldw], one behind the other. pack: codes w into the
+// packed layout; otherwise back from it.
+hipError_t launch_repack_fp8_block(uint8_t *w, int64_t ldw, int64_t experts, int64_t N, int64_t K, bool gated,
+                                   void *packed, bool pack, hipStream_t stream);
+hipError_t launch_quant_prepack_fp8_block(const void *w, bool w_f32, int64_t ldw, int64_t experts, int64_t N,
+                                          int64_t K, bool gated, void *packed, float *scale, hipStream_t stream);
+
+// ---- the product (small_fp8_block.hip) ----
+// What a launch computes: a layer's product; the gated products of each
+// expert's rows (rows of tokens by order / top_k, out fp32 silu(gate) * up in
+// sorted rows); or the down products of sorted rows (out fp32, to the rows
+// that order names).
+constexpr int kJobDense = 0, kJobGateUp = 1, kJobDown = 2;
+
+// A run of rows of one expert (expert < 0: none).
+struct BlockTile {
+    int expert, row0, rows;
+};
+
+struct BlockMmArgs {
+    const uint8_t *xq;
+    const float *xs;
+    const uint8_t *wp;
+    const float *ws;
+    const uint16_t *bias;
+    void *out;
+    int64_t ldq, lds, ldo;
+    int M, N, K;
+    int blocks;          // ceil(K / 128)
+    int frags;           // packed fragments along N
+    int half_scales;     // gated: scale rows of one half
+    int vec_store;       // 1 when out rows allow stores of 4 consecutive elements
+    int vec16;           // 1 when out rows start on 16-byte boundaries
+    int tiles_m;         // row tiles of the launch
+    // Experts:
+    const BlockTile *tiles;
+    const int *order;    // slot (token * top_k + choice) of each sorted row
+    int top_k;
+    int64_t expert_bytes, expert_scales;   // from one expert's weight and scales to the next's
+};
+
+typedef void (*BlockMmKernel)(const BlockMmArgs);
+struct BlockTileEntry {
+    const char *name;
+    int bm, bn, threads;
+    bool small;
+    BlockMmKernel dense[kOutKinds], gate_up, down;
+};
+int fp8_block_small_count();
+const BlockTileEntry &fp8_block_small(int i);
+
+int fp8_block_tile_count();
+const BlockTileEntry &fp8_block_tile(int tile);
+int fp8_block_tile_auto(int64_t M, int64_t N, int64_t K);
+hipError_t launch_fp8_block_mm(BlockMmArgs a, int mode, int tile, hipStream_t stream);
+
+}  // namespace w8a8

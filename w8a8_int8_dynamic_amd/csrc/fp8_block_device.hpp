@@ -1,0 +1,77 @@
+// What the kernels of the block-scaled product share.
+#pragma once
+
+#include "fp8_block.hpp"
+#include "fp8_block_rule.hpp"
+
+namespace w8a8 {
+namespace fp8_block {
+
+// The 128 products of each of 16 channels with each of 16 tokens, summed: a
+// fragment's operand and the tokens', each lane the k-chunks l/16 and 4 + l/16
+// of its channel and token l%16. (Its error measured on MI355X over random
+// codes: 1.3e-5 of the sums' rms, at most 9.4e-5, the same as of the other
+// e4m3 instructions.)
+__device__ __forceinline__ f32x4 block_product(const v4i (&w)[2], const v4i (&x)[2])
+{
+    const v8i ww = __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    const v8i xx = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ww, xx, f32x4{}, 0, 0, 0, 127, 0, 127);
+}
+
+// Scale row of packed fragment nb.
+template <int JOB>
+__device__ __forceinline__ int scale_row(int nb, int half_scales)
+{
+    return JOB == kJobGateUp ? (nb & 1) * half_scales + (nb >> 4) : nb >> 3;
+}
+
+// v / (1 + e^-v), on the hardware's 2^x and reciprocal (1 ulp each; their
+// argument's rounding adds |v| * 2^-24): within 2^-19 for |v| up to 16, where
+// the products that v is a sum of carry 2^-16.
+__device__ __forceinline__ float silu(float v)
+{
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+}
+
+// Four consecutive outputs of a row from channel n on, with the bias, as OUT
+// says (kOutI32: raw fp32).
+template <int OUT>
+__device__ __forceinline__ void store4(const BlockMmArgs &a, int64_t row, int n, f32x4 v)
+{
+    const bool whole = a.vec_store && n + 3 < a.N;
+    if constexpr (OUT == kOutI32) {
+        float *o = static_cast<float *>(a.out) + row * a.ldo + n;
+        if (whole) {
+            *reinterpret_cast<f32x4 *>(o) = v;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (n + r < a.N)
+                    o[r] = v[r];
+        }
+    } else {
+        constexpr bool F16 = OUT == kOutF16;
+        if (a.bias) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const unsigned b = a.bias[min(n + r, a.N - 1)];
+                v[r] += F16 ? quant_rule::f16_to_float(b) : __uint_as_float(b << 16);
+            }
+        }
+        const u32 lo = pack2<F16>(v[0], v[1]), hi = pack2<F16>(v[2], v[3]);
+        uint16_t *o = static_cast<uint16_t *>(a.out) + row * a.ldo + n;
+        if (whole) {
+            *reinterpret_cast<uint2 *>(o) = make_uint2(lo, hi);
+        } else {
+            const u32 hv[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (n + r < a.N)
+                    o[r] = (uint16_t)hv[r];
+        }
+    }
+}
+
+}  // namespace fp8_block
+}  // namespace w8a8

@@ -18,6 +18,20 @@ from . import ops
 __all__ = ["W8A8Linear", "quantize_linear_layers"]
 
 
+def _codes(wq: torch.Tensor) -> torch.Tensor:
+    """e4m3 codes as uint8."""
+    return wq.view(torch.uint8) if wq.dtype == torch.float8_e4m3fn else wq
+
+
+def _block_scales(ws: torch.Tensor, shape: Sequence[int]) -> torch.Tensor:
+    """Block scales [*shape] as contiguous fp32, checked."""
+    if ws.shape != tuple(shape):
+        raise ValueError(f"weight scales must have shape {tuple(shape)}, got {tuple(ws.shape)}")
+    if not torch.isfinite(ws).all():
+        raise ValueError("weight scales must be finite")
+    return ws.to(torch.float32).contiguous()
+
+
 class W8A8Linear(torch.nn.Module):
     """y = q(x) @ q(W)^T * x_scale * w_scale (+ bias), in x's type.
 
@@ -27,18 +41,22 @@ class W8A8Linear(torch.nn.Module):
     scheme "fp4": weights and activations in microscaled 4-bit floating point
     (MX FP4: e2m1 codes, a power-of-two scale per 32 elements along K), bf16 or
     fp16 activations; in_features a multiple of 32.
+    scheme "fp8_block": e4m3 with an fp32 scale per 128 elements of an activation
+    row and per 128 x 128 block of the weight, bf16 or fp16 activations.
 
     Build with ``from_float`` (online weight quantization on the GPU, written
     straight into the load-time layout) or ``from_quantized`` (weights and
     scales already made offline: int8 and fp32, or for "fp4" the uint8 codes
-    [N, K/2] and scale bytes [N, K/32] of ops.fp4_quant_per_block).
+    [N, K/2] and scale bytes [N, K/32] of ops.fp4_quant_per_block, or for
+    "fp8_block" e4m3 codes [N, K] as uint8 or float8_e4m3fn and fp32 scales
+    [ceil(N/128), ceil(K/128)]).
     """
 
     def __init__(self, w_packed: torch.Tensor, w_scale: torch.Tensor, out_features: int,
                  in_features: int, bias: Optional[torch.Tensor] = None, scheme: str = "int8"):
         super().__init__()
-        if scheme not in ("int8", "fp8", "fp4"):
-            raise ValueError(f"scheme must be 'int8', 'fp8' or 'fp4', got {scheme!r}")
+        if scheme not in ("int8", "fp8", "fp4", "fp8_block"):
+            raise ValueError(f"scheme must be 'int8', 'fp8', 'fp4' or 'fp8_block', got {scheme!r}")
         if bias is not None and bias.shape != (out_features,):
             raise ValueError(f"bias must have shape {(out_features,)}, got {tuple(bias.shape)}")
         self.scheme = scheme
@@ -61,9 +79,12 @@ class W8A8Linear(torch.nn.Module):
     @classmethod
     def from_quantized(cls, wq: torch.Tensor, w_scale: torch.Tensor,
                        bias: Optional[torch.Tensor] = None, scheme: str = "int8") -> "W8A8Linear":
-        if scheme not in ("int8", "fp4"):
-            raise ValueError(f"scheme must be 'int8' or 'fp4', got {scheme!r}")
+        if scheme not in ("int8", "fp4", "fp8_block"):
+            raise ValueError(f"scheme must be 'int8', 'fp4' or 'fp8_block', got {scheme!r}")
         N, K = wq.shape
+        if scheme == "fp8_block":
+            w_scale = _block_scales(w_scale, (-(-N // 128), -(-K // 128)))
+            return cls(ops.fp8_block_prepack_weight(_codes(wq)), w_scale, N, K, bias, scheme)
         if scheme == "fp4":
             if (w_scale == 255).any():
                 raise ValueError("weight scales must be finite")
@@ -87,6 +108,9 @@ class W8A8Linear(torch.nn.Module):
             if (ws == 255).any():
                 raise ValueError("weight scales must be finite")
             return cls(packed, ws, N, K, bias, scheme)
+        if scheme == "fp8_block":
+            packed, ws = ops.fp8_block_quant_prepack_weight(w.contiguous())
+            return cls(packed, _block_scales(ws, ws.shape), N, K, bias, scheme)
         quant = ops.fp8_quant_prepack_weight if scheme == "fp8" else ops.quant_prepack_weight
         packed, ws = quant(w.contiguous())
         if not torch.isfinite(ws).all():
@@ -102,10 +126,10 @@ class W8A8Linear(torch.nn.Module):
             x2 = x2.contiguous()
         # The quant and the scaled matmul, as one library call; the output (and
         # bias) type is x's.
-        if self.scheme == "fp4":
+        if self.scheme == "fp4" or self.scheme == "fp8_block":
             dtype = x2.dtype
             if dtype != torch.bfloat16 and dtype != torch.float16:
-                raise TypeError(f"the fp4 scheme takes bfloat16 or float16 activations, got {dtype}")
+                raise TypeError(f"the {self.scheme} scheme takes bfloat16 or float16 activations, got {dtype}")
             name = "bias_f16" if dtype == torch.float16 else "bias"
             try:
                 # (a Module's own lookup of a buffer costs about 0.4 us)
@@ -113,7 +137,7 @@ class W8A8Linear(torch.nn.Module):
                 args = b["w_packed"], b["w_scale"], self.out_features, b[name]
             except KeyError:                           # one of them was replaced by a Parameter
                 args = self.w_packed, self.w_scale, self.out_features, getattr(self, name)
-            out = ops._fp4_linear(x2, *args)
+            out = (ops._fp4_linear if self.scheme == "fp4" else ops._fp8_block_linear)(x2, *args)
             return out if x2 is x else out.reshape(*lead, self.out_features)
         bias = self.bias_f16 if x2.dtype == torch.float16 else self.bias
         if self.scheme == "fp8":
@@ -131,7 +155,7 @@ class W8A8Linear(torch.nn.Module):
                           out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """The layer's product alone, for activations quantized elsewhere (by the
         ops that end in quant_per_token for "int8" and "fp8", by
-        fp4_quant_per_block for "fp4"): codes [M, K] (fp4: [M, K/2]) and their
+        fp4_quant_per_block for "fp4", by fp8_quant_per_block for "fp8_block"): codes [M, K] (fp4: [M, K/2]) and their
         scales to [M, N] in out_dtype (bf16 or fp16). It uses no workspace of the
         layer, so calls on several streams may run at once; ops.scaled_mm takes
         one for a split of K at few rows (scheme "int8")."""
@@ -143,6 +167,8 @@ class W8A8Linear(torch.nn.Module):
         bias = self.bias_f16 if out_dtype == torch.float16 else self.bias
         if self.scheme == "fp4":
             return ops.fp4_scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype)
+        if self.scheme == "fp8_block":
+            return ops.fp8_block_scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype)
         if self.scheme == "fp8":
             return ops.fp8_scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype)
         return ops.scaled_mm(xq, xs, self.w_packed, self.w_scale, self.out_features, bias, out_dtype)
@@ -158,7 +184,7 @@ def quantize_linear_layers(module: torch.nn.Module, method: str = "int8",
     """Replace the torch.nn.Linear layers of `module` by W8A8Linear layers.
 
     The selection follows the page "Online Quantization" (Parameters table):
-    `method` is "int8", "fp8" or "fp4"; `activation_scheme` must be "dynamic"
+    `method` is "int8", "fp8", "fp4" or "fp8_block"; `activation_scheme` must be "dynamic"
     (activation scales computed at run time, the only scheme implemented);
     `ignored_layers` holds name patterns of layers to keep in their float
     type. A layer is kept when its qualified name (as in
@@ -167,8 +193,8 @@ def quantize_linear_layers(module: torch.nn.Module, method: str = "int8",
     Anything the path cannot run raises ValueError naming the layer: a layer
     on the CPU, or in_features not a multiple of 16 (32 for "fp4"). Returns
     `module`, or the replacement when `module` is itself a Linear."""
-    if method not in ("int8", "fp8", "fp4"):
-        raise ValueError(f"method must be 'int8', 'fp8' or 'fp4', got {method!r}")
+    if method not in ("int8", "fp8", "fp4", "fp8_block"):
+        raise ValueError(f"method must be 'int8', 'fp8', 'fp4' or 'fp8_block', got {method!r}")
     if activation_scheme != "dynamic":
         raise ValueError(f"only activation_scheme='dynamic' is implemented, got {activation_scheme!r}")
     patterns = [p for p in ignored_layers if p]

@@ -23,7 +23,10 @@ __all__ = ["quant_per_token", "quant_per_channel", "prepack_weight", "quant_prep
            "fp8_quant_prepack_weight", "fp8_scaled_mm", "fp8_quant_scaled_mm", "fp8_tile_count",
            "fp4_quant_per_block", "fp4_dequant", "fp4_prepack_weight", "fp4_quant_prepack_weight",
            "fp4_unpack_weight", "fp4_scaled_mm", "fp4_quant_scaled_mm", "fp4_tile_count", "fp4_tile_name",
-           "fp4_tile_auto", "Norm", "norm", "norm_quant_per_token", "fp8_norm_quant_per_token", "gated_residual",
+           "fp4_tile_auto", "fp8_quant_per_block", "fp8_block_dequant", "fp8_block_prepack_weight",
+           "fp8_block_quant_prepack_weight", "fp8_block_unpack_weight", "fp8_block_scaled_mm",
+           "fp8_block_quant_scaled_mm", "fp8_block_tile_count", "fp8_block_tile_name", "fp8_block_tile_auto",
+           "Routing", "route_experts", "fp8_block_experts", "Norm", "norm", "norm_quant_per_token", "fp8_norm_quant_per_token", "gated_residual",
            "gated_residual_norm", "gated_residual_norm_quant", "fp8_gated_residual_norm_quant"]
 
 
@@ -710,6 +713,336 @@ def fp4_tile_name(tile: int) -> str:
 
 def fp4_tile_auto(M: int, N: int, K: int) -> int:
     return _lib.lib().w8a8_fp4_tile_auto(M, N, K)
+
+
+# ---- the block-scaled 8-bit (e4m3) layer ----------------------------------
+_SCALE_BLOCK = 128
+
+
+def _blocks_of(n: int) -> int:
+    return -(-n // _SCALE_BLOCK)
+
+
+def _block_k(K: int) -> int:
+    if K < 16 or K > _lib.W8A8_MAX_K or K % 16 != 0:
+        raise ValueError(f"K must be a multiple of 16 in [16, {_lib.W8A8_MAX_K}], got {K}")
+    return K
+
+
+def _block_rows(xq: torch.Tensor, xs: torch.Tensor) -> Tuple[int, int]:
+    """(M, K) of e4m3 codes [M, K] and their scales [M, ceil(K/128)]."""
+    _matrix(xq, "xq", torch.uint8)
+    _matrix(xs, "xs", torch.float32)
+    M, K = xq.shape
+    if xs.shape != (M, _blocks_of(_block_k(K))):
+        raise ValueError(f"xs must have shape {(M, _blocks_of(K))}, got {tuple(xs.shape)}")
+    if xs.get_device() != xq.get_device():
+        _same_device(xq, xs)
+    return M, K
+
+
+def fp8_quant_per_block(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
+                        xs: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Block-scaled quantization of bf16, fp16 or fp32 x [M, K] (K a multiple of
+    16): (uint8 e4m3 codes [M, K], fp32 scales [M, ceil(K/128)], one per 128
+    elements)."""
+    t, M, K, ld = _float_rows(x, "x")
+    _block_k(K)
+    x, ld = _vector_rows(x, t, ld)
+    ldq, lds = K, _blocks_of(K)
+    own = xq is None and xs is None
+    xq = x.new_empty((M, K), dtype=torch.uint8) if xq is None else xq
+    xs = x.new_empty((M, lds), dtype=torch.float32) if xs is None else xs
+    if not own:
+        if _block_rows(xq, xs) != (M, K):
+            raise ValueError(f"xq must have shape {(M, K)}")
+        _same_device(x, xq)
+        ldq, lds = _ld(xq), _ld(xs)
+    _run(x, "fp8_quant_per_block", x.data_ptr(), t, M, K, ld, xq.data_ptr(), ldq, xs.data_ptr(), lds)
+    return xq, xs
+
+
+def fp8_block_dequant(xq: torch.Tensor, xs: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The values [M, K] that e4m3 codes and block scales stand for, rounded once to dtype."""
+    if dtype not in _DTYPE:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    M, K = _block_rows(xq, xs)
+    if xq.data_ptr() % 8 != 0 or _ld(xq) % 8 != 0:
+        xq = _rows_aligned(xq, 16)
+    out = xq.new_empty((M, K), dtype=dtype)
+    _run(xq, "fp8_block_dequant", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), M, K, _DTYPE[dtype],
+         out.data_ptr(), K)
+    return out
+
+
+def _block_weights(w: torch.Tensor, name: str, gated: bool) -> Tuple[torch.Tensor, int, int, int]:
+    """(w, E, N, K) of a weight [N, K], or of experts' weights [E, N, K]; rows contiguous,
+    one matrix behind the other."""
+    if not w.is_cuda:
+        raise ValueError(f"{name} must be a device tensor, got {w.device}")
+    if w.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [N, K] or [E, N, K], got shape {tuple(w.shape)}")
+    N, K = w.shape[-2:]
+    E = w.shape[0] if w.dim() == 3 else 1
+    _block_k(K)
+    if N < 1 or E < 1 or (gated and N % 32 != 0):
+        raise ValueError(f"{name}: no packed form of shape {tuple(w.shape)}"
+                         f"{' (gated: N must be a multiple of 32)' if gated else ''}")
+    if w.stride(-1) != 1 or (w.dim() == 3 and w.stride(0) != N * w.stride(1)):
+        w = w.contiguous()
+    return w, E, N, K
+
+
+def _block_packed(E: int, N: int, K: int, ref: torch.Tensor) -> torch.Tensor:
+    n = _lib.lib().fp8_block_prepack_weight_bytes(E, N, K)
+    if n == 0:
+        raise ValueError(f"no packed size for E={E}, N={N}, K={K}")
+    return ref.new_empty((n,), dtype=torch.uint8)
+
+
+def _block_scale_rows(N: int, gated: bool) -> int:
+    return 2 * _blocks_of(N // 2) if gated else _blocks_of(N)
+
+
+def fp8_block_prepack_weight(wq: torch.Tensor, gated: bool = False) -> torch.Tensor:
+    """Repack e4m3 codes [N, K] (uint8), or [E, N, K] of experts, into the layout
+    that fp8_block_scaled_mm reads. gated: a matrix holds the gate rows, then
+    as many up rows (the first weight of fp8_block_experts)."""
+    if wq.dtype != torch.uint8:
+        raise TypeError(f"wq must be torch.uint8, got {wq.dtype}")
+    wq, E, N, K = _block_weights(wq, "wq", gated)
+    packed = _block_packed(E, N, K, wq)
+    _run(wq, "fp8_block_prepack_weight", wq.data_ptr(), _row_pitch(wq), E, N, K, int(gated), packed.data_ptr())
+    return packed
+
+
+def _row_pitch(w: torch.Tensor) -> int:
+    return max(w.stride(-2), w.shape[-1])
+
+
+def fp8_block_quant_prepack_weight(w: torch.Tensor, gated: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Online quantization of a bf16 or fp32 weight [N, K] ([E, N, K]) in blocks of
+    128 x 128: (packed codes, fp32 scales [ceil(N/128), ceil(K/128)]; of each
+    expert, and of a gated weight [2*ceil(N/2/128), ceil(K/128)])."""
+    if w.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"w must be bfloat16 or float32, got {w.dtype}")
+    w, E, N, K = _block_weights(w, "w", gated)
+    f32 = w.dtype == torch.float32
+    if w.data_ptr() % 16 != 0 or _row_pitch(w) % (4 if f32 else 8) != 0:
+        w = w.clone(memory_format=torch.contiguous_format)
+    packed = _block_packed(E, N, K, w)
+    shape = (_block_scale_rows(N, gated), _blocks_of(K))
+    ws = w.new_empty(shape if w.dim() == 2 else (E, *shape), dtype=torch.float32)
+    _run(w, "fp8_block_quant_prepack_weight", w.data_ptr(), 0 if f32 else 1, _row_pitch(w), E, N, K, int(gated),
+         packed.data_ptr(), ws.data_ptr())
+    return packed, ws
+
+
+def _check_block_packed(w_packed: torch.Tensor, ws: torch.Tensor, N: int, K: int, ref: torch.Tensor) -> None:
+    """The packed buffer and scales of a weight [N, K], on ref's device."""
+    if N < 1:
+        raise ValueError(f"N must be at least 1, got {N}")
+    device = ref.get_device()
+    if device < 0 or w_packed.get_device() != device or ws.get_device() != device:
+        raise ValueError(f"all tensors must be on one GPU, and x is on {ref.device}")
+    if w_packed.dtype != torch.uint8 or w_packed.numel() < _round_up(N, 16) * _round_up(K, 128) or \
+            not w_packed.is_contiguous():
+        raise ValueError("w_packed must be a uint8 device buffer of the packed layout (N, K)")
+    if ws.dtype != torch.float32 or ws.shape != (_blocks_of(N), _blocks_of(K)) or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous fp32 {(_blocks_of(N), _blocks_of(K))}, got {ws.dtype} "
+                         f"{tuple(ws.shape)}")
+
+
+def fp8_block_unpack_weight(w_packed: torch.Tensor, N: int, K: int, gated: bool = False,
+                            experts: Optional[int] = None) -> torch.Tensor:
+    """Inverse of fp8_block_prepack_weight: codes [N, K], or [experts, N, K]."""
+    E = 1 if experts is None else experts
+    n = _lib.lib().fp8_block_prepack_weight_bytes(E, N, _block_k(K))
+    if n == 0 or (gated and N % 32 != 0):
+        raise ValueError(f"no packed size for E={E}, N={N}, K={K}")
+    if not w_packed.is_cuda or w_packed.dtype != torch.uint8 or w_packed.numel() < n or not w_packed.is_contiguous():
+        raise ValueError("w_packed must be a uint8 device buffer of the packed layout (N, K)")
+    wq = w_packed.new_empty((N, K) if experts is None else (E, N, K))
+    _run(w_packed, "fp8_block_unpack_weight", w_packed.data_ptr(), E, N, K, int(gated), wq.data_ptr(), K)
+    return wq
+
+
+def fp8_block_scaled_mm(xq: torch.Tensor, xs: torch.Tensor, w_packed: torch.Tensor, ws: torch.Tensor, N: int,
+                        bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                        out: Optional[torch.Tensor] = None, tile: int = -1) -> torch.Tensor:
+    """The product [M, N] of block-scaled rows (e4m3 codes xq [M, K], scales xs
+    [M, ceil(K/128)]) with a packed weight and its scales ws [ceil(N/128),
+    ceil(K/128)], plus bias, rounded to out_dtype (bf16 or fp16; the bias in the
+    same type), or the raw fp32 sums."""
+    M, K = _block_rows(xq, xs)
+    _check_block_packed(w_packed, ws, N, K, xq)
+    mode, out = _fp4_out(M, N, bias, out_dtype, out, xq)
+    xq = _rows_aligned(xq, 16)
+    _run(xq, "fp8_block_scaled_mm_tile", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), w_packed.data_ptr(),
+         ws.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, mode, out.data_ptr(), _ld(out),
+         tile=(tile,))
+    return out
+
+
+def fp8_block_quant_scaled_mm(x: torch.Tensor, w_packed: torch.Tensor, ws: torch.Tensor, N: int,
+                              bias: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                              out: Optional[torch.Tensor] = None, tile: int = -1
+                              ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """fp8_quant_per_block of x [M, K] and fp8_block_scaled_mm in one call: (out,
+    xq, xs). out_dtype defaults to x's type, bf16 for fp32 x."""
+    t, M, K, ld = _float_rows(x, "x")
+    _block_k(K)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if t == _lib.W8A8_T_F32 else x.dtype
+    _check_block_packed(w_packed, ws, N, K, x)
+    mode, out = _fp4_out(M, N, bias, out_dtype, out, x)
+    x, ld = _vector_rows(x, t, ld)
+    xq = x.new_empty((M, K), dtype=torch.uint8)
+    xs = x.new_empty((M, _blocks_of(K)), dtype=torch.float32)
+    _run(x, "fp8_block_quant_scaled_mm_tile", x.data_ptr(), t, ld, xq.data_ptr(), K, xs.data_ptr(), _blocks_of(K),
+         w_packed.data_ptr(), ws.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, mode, out.data_ptr(),
+         _ld(out), tile=(tile,))
+    return out, xq, xs
+
+
+def _fp8_block_linear(x: torch.Tensor, w_packed: torch.Tensor, ws: torch.Tensor, N: int,
+                      bias: Optional[torch.Tensor]) -> torch.Tensor:
+    """fp8_block_quant_scaled_mm's out alone, for a layer (which has no use for the
+    codes: they go through one buffer)."""
+    t, M, K, ld = _float_rows(x, "x")
+    _check_block_packed(w_packed, ws, N, K, x)
+    if bias is not None and (bias.dtype != x.dtype or bias.size() != (N,) or not bias.is_contiguous() or
+                             bias.get_device() != x.get_device()):
+        _vector(bias, N, "bias", x.dtype)
+        _same_device(x, bias)
+    x, ld = _vector_rows(x, t, ld)
+    out = x.new_empty((M, N))
+    xq = x.new_empty((M * (K + 4 * _blocks_of(K)),), dtype=torch.uint8)
+    at = xq.data_ptr()
+    _run(x, "fp8_block_quant_scaled_mm", x.data_ptr(), t, ld, at, K, at + M * K, _blocks_of(K), w_packed.data_ptr(),
+         ws.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, _OUT_MODE[x.dtype], out.data_ptr(), N)
+    return out
+
+
+def fp8_block_tile_count() -> int:
+    return _lib.lib().w8a8_fp8_block_tile_count()
+
+
+def fp8_block_tile_name(tile: int) -> str:
+    return _lib.lib().w8a8_fp8_block_tile_name(tile).decode()
+
+
+def fp8_block_tile_auto(M: int, N: int, K: int) -> int:
+    return _lib.lib().w8a8_fp8_block_tile_auto(M, N, K)
+
+
+# ---- a mixture of experts -------------------------------------------------
+@dataclass(eq=False)
+class Routing:
+    """How a router's logits choose top_k experts for each token:
+
+        score  = softmax(logits) or sigmoid(logits)             score "softmax" or "sigmoid"
+        choice = score + bias                                   bias fp32 [E] or None
+        groups > 1: the experts stand in equal groups; a group's worth is the sum
+        of its group_top (1 or 2) largest choices; the top_groups best stay
+        ids = the top_k best choices, best first, ties to the lowest index
+        weights = their scores, over their sum (renormalize), times scale
+
+    Experts whose logit (or bias) is NaN or -infinity are left out; a row with
+    fewer than top_k left ends in ids -1 with weight 0."""
+    top_k: int
+    score: str = "softmax"
+    bias: Optional[torch.Tensor] = None
+    groups: int = 1
+    top_groups: int = 1
+    group_top: int = 2
+    renormalize: bool = True
+    scale: float = 1.0
+
+
+_SCORE = {"softmax": _lib.W8A8_SCORE_SOFTMAX, "sigmoid": _lib.W8A8_SCORE_SIGMOID}
+
+
+def route_experts(logits: torch.Tensor, routing: Routing) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The experts of each token by its logits [T, E] (bf16, fp16 or fp32; E up to
+    1024): (int32 ids [T, top_k], fp32 weights [T, top_k])."""
+    t, T, E, ld = _float_rows(logits, "logits")
+    r = routing
+    score = _SCORE.get(r.score)
+    if score is None:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {r.score!r}")
+    bias = r.bias
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,) or not bias.is_contiguous() or
+                             bias.get_device() != logits.get_device()):
+        raise ValueError(f"bias must be contiguous fp32 [{E}] on {logits.device}")
+    if r.top_k < 1:
+        raise ValueError(f"top_k must be at least 1, got {r.top_k}")
+    ids = logits.new_empty((T, r.top_k), dtype=torch.int32)
+    weights = logits.new_empty((T, r.top_k), dtype=torch.float32)
+    how = _lib.ROUTING_STRUCT.pack(0 if bias is None else bias.data_ptr(), score, r.top_k, r.groups, r.top_groups,
+                                   r.group_top, int(r.renormalize), r.scale)
+    _run(logits, "route_experts", logits.data_ptr(), t, max(ld, E), T, E, how, ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def fp8_block_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: torch.Tensor,
+                      gate_up_scale: torch.Tensor, down: torch.Tensor, down_scale: torch.Tensor, inner: int,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A mixture of experts over tokens x [T, K] (bf16, fp16 or fp32), in x's type:
+
+        out[t] = sum over j of weights[t, j] * down_e(silu(gate_e x[t]) * up_e x[t]),   e = ids[t, j]
+
+    ids int32 and weights fp32 [T, top_k] (route_experts' results); an id outside
+    [0, E) stands for no expert. gate_up: fp8_block_prepack_weight of codes
+    [E, 2 * inner, K] (gated), gate_up_scale [E, 2*ceil(inner/128), ceil(K/128)];
+    down: of codes [E, K, inner], down_scale [E, ceil(K/128), ceil(inner/128)].
+    x and the inner rows pass through fp8_quant_per_block's codes."""
+    t, T, K, ld = _float_rows(x, "x")
+    device = x.get_device()
+    _block_k(K)
+    _block_k(inner)
+    if ids.dim() != 2 or ids.shape[0] != T or weights.shape != ids.shape:
+        raise ValueError(f"ids and weights must be [{T}, top_k], got {tuple(ids.shape)} and {tuple(weights.shape)}")
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise TypeError(f"ids must be int32 and weights fp32, got {ids.dtype} and {weights.dtype}")
+    for name, s in (("gate_up_scale", gate_up_scale), ("down_scale", down_scale)):
+        if s.dtype != torch.float32 or s.dim() != 3 or not s.is_contiguous():
+            raise ValueError(f"{name} must be contiguous fp32 [E, rows, blocks]")
+    E = gate_up_scale.shape[0]
+    if E < 1 or gate_up_scale.shape[1:] != (2 * _blocks_of(inner), _blocks_of(K)) or \
+            down_scale.shape != (E, _blocks_of(K), _blocks_of(inner)):
+        raise ValueError(f"scales {tuple(gate_up_scale.shape)} and {tuple(down_scale.shape)} do not belong to "
+                         f"experts of K={K}, inner={inner}")
+    for name, w, least in (("gate_up", gate_up, 2 * inner * _round_up(K, 128)),
+                           ("down", down, K * _round_up(inner, 128))):
+        if w.dtype != torch.uint8 or w.numel() < E * least or not w.is_contiguous():
+            raise ValueError(f"{name} must be a uint8 device buffer of the packed layout")
+    for o in (ids, weights, gate_up, gate_up_scale, down, down_scale):
+        if o.get_device() != device:
+            _same_device(x, o)
+    ids, weights = ids.contiguous(), weights.contiguous()
+    x, ld = _vector_rows(x, t, ld)
+    if out is None:
+        out = r = x.new_empty((T, K))
+    else:
+        _matrix(out, "out", x.dtype)
+        if out.shape != (T, K):
+            raise ValueError(f"out must have shape {(T, K)}")
+        _same_device(x, out)
+        step = 4 if t == _lib.W8A8_T_F32 else 8
+        r = out if out.data_ptr() % 16 == 0 and _ld(out) % step == 0 else x.new_empty((T, K))
+    top_k = ids.shape[1]
+    need = _lib.lib().fp8_block_experts_workspace_bytes(T, K, inner, E, top_k)
+    if need == 0 and T > 0:
+        raise ValueError(f"out of range: {T} tokens, {E} experts, top_k {top_k}")
+    work = x.new_empty((need,), dtype=torch.uint8)
+    layer = _lib.EXPERTS_STRUCT.pack(gate_up.data_ptr(), gate_up_scale.data_ptr(), down.data_ptr(),
+                                     down_scale.data_ptr(), K, inner, E)
+    _run(x, "fp8_block_experts", layer, x.data_ptr(), t, ld, T, ids.data_ptr(), weights.data_ptr(), top_k,
+         r.data_ptr(), _ld(r), work.data_ptr(), need)
+    if r is not out:
+        out.copy_(r)
+    return out
 
 
 def fp8_tile_count() -> int:
