@@ -612,9 +612,10 @@ w8a8_status_t fp8_block_unpack_weight(const void *w_packed, int64_t experts, int
  *   W8A8_OUT_BF16 / W8A8_OUT_F16: acc + bias[n] (bias in the output's type,
  *   or NULL) in fp32, rounded to nearest even;  W8A8_OUT_I32: acc as fp32.
  * Requirements: M >= 0 (0 is a no-op), N >= 1, K <= ldq <= W8A8_MAX_LDQ,
- * ceil(K/128) <= lds <= W8A8_MAX_LDQ, ldo >= N; xq and w_packed 16-byte
- * aligned, ldq a multiple of 16; the others aligned to their element size.
- * w_scale [ceil(N/128), ceil(K/128)] without gaps.
+ * ceil(K/128) <= lds <= W8A8_MAX_LDQ/4, ldo >= N; xq and w_packed 16-byte
+ * aligned, ldq a multiple of 16; x_scale 16-byte aligned, lds a multiple of 4
+ * and M * lds floats readable (what lies past ceil(K/128) of a row has no
+ * effect); the others aligned to their element size. w_scale [ceil(N/128), ceil(K/128)] without gaps.
  * fp8_block_quant_scaled_mm - fp8_quant_per_block of x [M, ldx], then
  * fp8_block_scaled_mm of the result, in one call; xq and x_scale are written.
  * ..._tile: with an explicit tile (0 <= tile < w8a8_fp8_block_tile_count()) or

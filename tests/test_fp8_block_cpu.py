@@ -26,11 +26,11 @@ def dequant(q=A, ldq=144, s=A, lds=2, M=4, K=144, t=0, o=A, ldo=144):
     return L.fp8_block_dequant(q, ldq, s, lds, M, K, t, o, ldo, None)
 
 
-def mm(xq=A, ldq=144, xs=A, lds=2, wp=A, ws=A, bias=None, M=4, N=16, K=144, mode=0, out=A, ldo=16, tile=-1):
+def mm(xq=A, ldq=144, xs=A, lds=4, wp=A, ws=A, bias=None, M=4, N=16, K=144, mode=0, out=A, ldo=16, tile=-1):
     return L.fp8_block_scaled_mm_tile(xq, ldq, xs, lds, wp, ws, bias, M, N, K, mode, out, ldo, None, tile)
 
 
-def qmm(x=A, t=0, ldx=144, xq=A, ldq=144, xs=A, lds=2, wp=A, ws=A, bias=None, M=4, N=16, K=144, mode=0, out=A,
+def qmm(x=A, t=0, ldx=144, xq=A, ldq=144, xs=A, lds=4, wp=A, ws=A, bias=None, M=4, N=16, K=144, mode=0, out=A,
         ldo=16, tile=-1):
     return L.fp8_block_quant_scaled_mm_tile(x, t, ldx, xq, ldq, xs, lds, wp, ws, bias, M, N, K, mode, out, ldo, None,
                                             tile)
@@ -76,11 +76,11 @@ def test_mm_checks():
         assert f(M=-1) == SHAPE and f(N=0) == SHAPE and f(K=8) == SHAPE and f(K=136) == SHAPE
         assert f(ldq=128) == SHAPE and f(lds=1) == SHAPE and f(ldo=15) == SHAPE
         assert f(K=BIG, ldq=BIG, lds=BIG, **({"ldx": BIG} if f is qmm else {})) == SHAPE
-        assert f(ldq=_lib.W8A8_MAX_LDQ + 16) == SHAPE and f(lds=_lib.W8A8_MAX_LDQ + 16) == SHAPE
+        assert f(ldq=_lib.W8A8_MAX_LDQ + 16) == SHAPE and f(lds=_lib.W8A8_MAX_LDQ // 4 + 4) == SHAPE
         for name in ("xq", "xs", "wp", "ws", "out"):
             assert f(**{name: None}) == NULL, name
         assert f(xq=A + 8) == ALIGN and f(ldq=152) == ALIGN and f(wp=A + 8) == ALIGN and f(ws=A + 2) == ALIGN
-        assert f(xs=A + 2) == ALIGN and f(out=A + 1) == ALIGN and f(out=A + 2, mode=1) == ALIGN and f(bias=A + 1) == ALIGN
+        assert f(xs=A + 4) == ALIGN and f(lds=6) == ALIGN and f(out=A + 1) == ALIGN and f(out=A + 2, mode=1) == ALIGN and f(bias=A + 1) == ALIGN
         n = 2 ** 31 - 1
         assert f(M=n, N=n, ldo=n) == SHAPE                  # no launch holds that many tiles
         none = dict(xq=None, xs=None, wp=None, ws=None, out=None)
@@ -142,8 +142,8 @@ def test_experts_checks():
                 dict(dn=A + 8), dict(work=A + 128), dict(ids=A + 2), dict(w=A + 2), dict(gs=A + 2), dict(ds=A + 2)):
         assert experts(**bad) == ALIGN, bad
     most = _lib.W8A8_MAX_K
-    assert experts(K=most, inner=most, ldx=most, ldo=most, E=1024, T=4096, k=64) == SHAPE   # no launch holds it
-    assert L.fp8_block_experts_workspace_bytes(4096, most, most, 1024, 64) == 0
+    assert experts(K=most, inner=most, ldx=most, ldo=most, E=1024, T=8192, k=1) == SHAPE    # no launch holds it
+    assert L.fp8_block_experts_workspace_bytes(8192, most, most, 1024, 1) == 0
     need = L.fp8_block_experts_workspace_bytes(4, 144, 80, 4, 2)
     assert need > 0 and experts(size=need - 1) == SHAPE
     assert L.fp8_block_experts_workspace_bytes(4, 136, 80, 4, 2) == 0

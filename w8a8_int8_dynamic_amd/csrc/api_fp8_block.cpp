@@ -79,8 +79,8 @@ w8a8_status_t mm_args(const uint8_t *xq, int64_t ldq, const float *x_scale, int6
         return st;
     if (ldq < K || lds < w8a8::ceil_div(K, kBlock) || ldo < N)
         return fail(W8A8_ERR_SHAPE, "%s: leading dimension too small", what);
-    if (ldq > W8A8_MAX_LDQ || lds > W8A8_MAX_LDQ)
-        return fail(W8A8_ERR_SHAPE, "%s: ldq or lds above %d", what, W8A8_MAX_LDQ);
+    if (ldq > W8A8_MAX_LDQ || lds > W8A8_MAX_LDQ / 4)
+        return fail(W8A8_ERR_SHAPE, "%s: ldq above %d or lds above a quarter of that", what, W8A8_MAX_LDQ);
     a = w8a8::BlockMmArgs{};
     t = -1;
     if (M == 0)
@@ -90,9 +90,11 @@ w8a8_status_t mm_args(const uint8_t *xq, int64_t ldq, const float *x_scale, int6
     if (!aligned(xq, 16) || ldq % 16 != 0 || !aligned(w_packed, 16))
         return fail(W8A8_ERR_ALIGN, "%s: codes and the packed weight must be 16-byte aligned, ldq a multiple of 16",
                     what);
+    if (!aligned(x_scale, 16) || lds % 4 != 0)
+        return fail(W8A8_ERR_ALIGN, "%s: token scales must be 16-byte aligned with lds a multiple of 4", what);
     const bool raw = mode == W8A8_OUT_I32;
     const uintptr_t esz = raw ? 4 : 2;
-    if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(out, esz) || (!raw && bias && !aligned(bias, 2)))
+    if (!aligned(w_scale, 4) || !aligned(out, esz) || (!raw && bias && !aligned(bias, 2)))
         return fail(W8A8_ERR_ALIGN, "%s: scales, out and bias must be aligned to their element size", what);
     t = tile >= 0 ? tile : w8a8::fp8_block_tile_auto(M, N, K);
     const w8a8::BlockTileEntry &e = w8a8::fp8_block_tile(t);

@@ -25,8 +25,7 @@ constexpr int kPlanThreads = 1024;
 // One workgroup per expert: where its rows begin (the slots of lower experts
 // come first), its slots in ascending order, and its row tiles. Every
 // workgroup counts all experts by itself (LDS counters: their sums do not
-// depend on the order), so that none waits for another. The last one marks the
-// launch's remaining row tiles as empty.
+// depend on the order), so that none waits for another.
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int *__restrict__ ids, int slots, int experts,
                                                             int bm, int *__restrict__ order,
                                                             BlockTile *__restrict__ tiles, int tiles_m)
@@ -54,9 +53,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int *__restric
     const int first = sums[0], tile0 = sums[1], rows = count[e], mine = (rows + bm - 1) / bm;
     for (int i = t; i < mine; i += kPlanThreads)
         tiles[tile0 + i] = BlockTile{e, first + i * bm, min(bm, rows - i * bm)};
-    if (e == experts - 1)
-        for (int i = tile0 + mine + t; i < tiles_m; i += kPlanThreads)
-            tiles[i] = BlockTile{-1, 0, 0};
+    if (e == experts - 1 && t == 0)
+        tiles[tiles_m] = BlockTile{-1, 0, tile0 + mine};
     if (rows == 0)
         return;
     int at = first;
@@ -118,14 +116,19 @@ int64_t tokens_at_once(int64_t tokens, int top_k, int64_t K)
     return std::min(tokens, most);
 }
 
+// Scales per row of codes, in whole 16 bytes.
+int64_t scale_pitch(int64_t K) { return round_up(ceil_div(K, kBlock), 4); }
+
 struct Layout {
     size_t xq, xs, order, tiles, hq, hs, h, y, end;
     int64_t tiles_m;
 };
 
-Layout layout_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner, int bm)
+Layout layout_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner, const BlockTileEntry &e)
 {
     Layout l;
+    const int bm = e.bm;
+    const bool small = e.small;
     const int64_t slots = tokens * top_k;
     l.tiles_m = slots / bm + std::min<int64_t>(experts, slots);
     size_t at = 0;
@@ -135,38 +138,44 @@ Layout layout_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inne
         return p;
     };
     l.xq = take(tokens * K);
-    l.xs = take(tokens * ceil_div(K, kBlock) * 4);
+    l.xs = take(tokens * scale_pitch(K) * 4);
     l.order = take(slots * 4);
-    l.tiles = take(l.tiles_m * (int64_t)sizeof(BlockTile));
+    l.tiles = take((l.tiles_m + 1) * (int64_t)sizeof(BlockTile));
     l.hq = take(slots * inner);
-    l.hs = take(slots * ceil_div(inner, kBlock) * 4);
-    l.h = take(slots * inner * 4);
+    l.hs = take(slots * scale_pitch(inner) * 4);
+    l.h = take(small ? slots * inner * 4 : 0);
     l.y = take(slots * K * 4);
     l.end = at;
     return l;
+}
+
+const BlockTileEntry &tile_of_call(int64_t tokens, int top_k, int experts)
+{
+    const int64_t rows = tokens * top_k / experts;       // of an expert, on average
+    return rows > 128 ? fp8_block_main(0) : rows > 32 ? fp8_block_main(1) : fp8_block_small(0);
 }
 
 }  // namespace
 
 size_t experts_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
 {
-    const BlockTileEntry &e = fp8_block_small(0);
-    return layout_of(tokens_at_once(tokens, top_k, K), top_k, experts, K, inner, e.bm).end;
+    const int64_t step = tokens_at_once(tokens, top_k, K);
+    return layout_of(step, top_k, experts, K, inner, tile_of_call(step, top_k, experts)).end;
 }
 
 bool experts_fit(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
 {
-    const BlockTileEntry &e = fp8_block_small(0);
     const int64_t step = tokens_at_once(tokens, top_k, K);
+    const BlockTileEntry &e = tile_of_call(step, top_k, experts);
     const int64_t tiles_m = step * top_k / e.bm + std::min<int64_t>(experts, step * top_k);
     return mm_grid_fits(tiles_m * ceil_div(std::max(2 * inner, K), e.bn), e.threads);
 }
 
 hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t stream)
 {
-    const BlockTileEntry &e = fp8_block_small(0);
     const int64_t step = tokens_at_once(args.tokens, args.top_k, args.K);
-    const Layout l = layout_of(step, args.top_k, args.experts, args.K, args.inner, e.bm);
+    const BlockTileEntry &e = tile_of_call(step, args.top_k, args.experts);
+    const Layout l = layout_of(step, args.top_k, args.experts, args.K, args.inner, e);
     char *work = static_cast<char *>(workspace);
     const int x_bytes = args.kind == kElemF32 ? 4 : 2;
     const int blocks = (int)ceil_div(args.K, kBlock), inner_blocks = (int)ceil_div(args.inner, kBlock);
@@ -181,7 +190,8 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         const int slots = (int)(tokens * args.top_k);
         const int *ids = args.ids + t0 * args.top_k;
         hipError_t err = launch_quant_fp8_block(static_cast<const char *>(args.x) + t0 * args.ldx * x_bytes, args.kind,
-                                                tokens, args.K, args.ldx, xq, args.K, xs, blocks, stream);
+                                                tokens, args.K, args.ldx, xq, args.K, xs, scale_pitch(args.K),
+                                                stream);
         if (err != hipSuccess)
             return err;
         const int tiles_m = (int)(slots / e.bm + std::min(args.experts, slots));
@@ -197,11 +207,13 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         m.xq = xq;
         m.xs = xs;
         m.ldq = args.K;
-        m.lds = blocks;
+        m.lds = scale_pitch(args.K);
         m.wp = args.gate_up;
         m.ws = args.gate_up_scale;
-        m.out = h;
+        m.out = e.small ? static_cast<void *>(h) : hq;
         m.ldo = args.inner;
+        m.out_scale = hs;
+        m.ld_out_scale = scale_pitch(args.inner);
         m.M = slots;
         m.N = (int)(2 * args.inner);
         m.K = (int)args.K;
@@ -212,14 +224,16 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         m.expert_scales = (int64_t)2 * inner_blocks * blocks;
         hipLaunchKernelGGL(e.gate_up, dim3((unsigned)(tiles_m * ceil_div(m.frags, e.bn / 16))), dim3(e.threads), 0,
                            stream, m);
-        err = launch_quant_fp8_block(h, kElemF32, slots, args.inner, args.inner, hq, args.inner, hs, inner_blocks,
-                                     stream);
-        if (err != hipSuccess)
-            return err;
+        if (e.small) {
+            err = launch_quant_fp8_block(h, kElemF32, slots, args.inner, args.inner, hq, args.inner, hs,
+                                         scale_pitch(args.inner), stream);
+            if (err != hipSuccess)
+                return err;
+        }
         m.xq = hq;
         m.xs = hs;
         m.ldq = args.inner;
-        m.lds = inner_blocks;
+        m.lds = scale_pitch(args.inner);
         m.wp = args.down;
         m.ws = args.down_scale;
         m.out = y;

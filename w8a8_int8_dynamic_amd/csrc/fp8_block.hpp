@@ -28,13 +28,13 @@ hipError_t launch_quant_prepack_fp8_block(const void *w, bool w_f32, int64_t ldw
                                           int64_t K, bool gated, void *packed, float *scale, hipStream_t stream);
 
 // ---- the product (small_fp8_block.hip) ----
-// What a launch computes: a layer's product; the gated products of each
-// expert's rows (rows of tokens by order / top_k, out fp32 silu(gate) * up in
-// sorted rows); or the down products of sorted rows (out fp32, to the rows
-// that order names).
+// What a launch computes: a layer's product; the gated products silu(gate) * up
+// of each expert's rows (rows of tokens by order / top_k, out in sorted rows:
+// fp32 from the small-M kernel, codes and scales from the main kernel); or the
+// down products of sorted rows (out fp32, to the rows that order names).
 constexpr int kJobDense = 0, kJobGateUp = 1, kJobDown = 2;
 
-// A run of rows of one expert (expert < 0: none).
+// A run of rows of one expert.
 struct BlockTile {
     int expert, row0, rows;
 };
@@ -53,9 +53,11 @@ struct BlockMmArgs {
     int half_scales;     // gated: scale rows of one half
     int vec_store;       // 1 when out rows allow stores of 4 consecutive elements
     int vec16;           // 1 when out rows start on 16-byte boundaries
-    int tiles_m;         // row tiles of the launch
+    int tiles_m;         // row tiles of the launch, at most
+    float *out_scale;    // gated, main kernel: out are e4m3 codes, these their scales [rows, ld_out_scale]
+    int64_t ld_out_scale;
     // Experts:
-    const BlockTile *tiles;
+    const BlockTile *tiles;   // then, at [tiles_m], their number as rows
     const int *order;    // slot (token * top_k + choice) of each sorted row
     int top_k;
     int64_t expert_bytes, expert_scales;   // from one expert's weight and scales to the next's
@@ -68,6 +70,8 @@ struct BlockTileEntry {
     bool small;
     BlockMmKernel dense[kOutKinds], gate_up, down;
 };
+int fp8_block_main_count();
+const BlockTileEntry &fp8_block_main(int i);
 int fp8_block_small_count();
 const BlockTileEntry &fp8_block_small(int i);
 

@@ -3,10 +3,17 @@
 
 namespace w8a8 {
 
-int fp8_block_tile_count() { return fp8_block_small_count(); }
-const BlockTileEntry &fp8_block_tile(int tile) { return fp8_block_small(tile); }
+int fp8_block_tile_count() { return fp8_block_main_count() + fp8_block_small_count(); }
+const BlockTileEntry &fp8_block_tile(int tile)
+{
+    const int n = fp8_block_main_count();
+    return tile < n ? fp8_block_main(tile) : fp8_block_small(tile - n);
+}
 
-int fp8_block_tile_auto(int64_t M, int64_t N, int64_t K) { return 0; }
+int fp8_block_tile_auto(int64_t M, int64_t N, int64_t K)
+{
+    return M <= 64 ? 2 : M <= 512 ? 1 : 0;
+}
 
 hipError_t launch_fp8_block_mm(BlockMmArgs a, int mode, int tile, hipStream_t stream)
 {

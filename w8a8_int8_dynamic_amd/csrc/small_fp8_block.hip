@@ -40,14 +40,13 @@ __global__ __launch_bounds__(S::THREADS) void block_mm_small_kernel(const BlockM
     const int wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, sub = lane >> 4;
     const int tiles_n = (a.frags + S::FN - 1) / S::FN;
-    const int t = xcd_remap(blockIdx.x, a.tiles_m * tiles_n);
-    const int tm = t % a.tiles_m, nb0 = (t / a.tiles_m) * S::FN;
-    BlockTile tile{0, tm * S::BM, min(S::BM, a.M - tm * S::BM)};
-    if constexpr (JOB != kJobDense) {
-        tile = a.tiles[tm];
-        if (tile.expert < 0)
-            return;
-    }
+    // (an experts' launch holds room for more row tiles than there are)
+    const int tiles_m = JOB == kJobDense ? a.tiles_m : a.tiles[a.tiles_m].rows;
+    if (JOB != kJobDense && (int)blockIdx.x >= tiles_m * tiles_n)
+        return;
+    const int t = xcd_remap(blockIdx.x, tiles_m * tiles_n);
+    const int tm = t % tiles_m, nb0 = (t / tiles_m) * S::FN;
+    const BlockTile tile = JOB == kJobDense ? BlockTile{0, tm * S::BM, min(S::BM, a.M - tm * S::BM)} : a.tiles[tm];
     const uint8_t *wp = a.wp + tile.expert * a.expert_bytes;
     const float *ws = a.ws + tile.expert * a.expert_scales;
 

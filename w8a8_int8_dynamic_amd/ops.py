@@ -741,6 +741,26 @@ def _block_rows(xq: torch.Tensor, xs: torch.Tensor) -> Tuple[int, int]:
     return M, K
 
 
+def _block_scale_buffer(M: int, n: int, ref: torch.Tensor) -> torch.Tensor:
+    """fp32 [M, n] whose rows start on, and are readable to, 16-byte boundaries."""
+    if n % 4 == 0:
+        return ref.new_empty((M, n), dtype=torch.float32)
+    return ref.new_empty((M, _round_up(n, 4)), dtype=torch.float32)[:, :n]
+
+
+def _block_scale_rows_of(xs: torch.Tensor) -> Tuple[torch.Tensor, int]:
+    """xs and its pitch when its rows start on 16-byte boundaries and the last one can
+    be read to a whole 16 bytes, else those of a copy into a row-padded buffer."""
+    M, n = xs.shape
+    ld = xs.stride(0) if M > 1 else _round_up(n, 4)
+    if xs.data_ptr() % 16 == 0 and ld % 4 == 0 and ld >= n and \
+            xs.untyped_storage().nbytes() // 4 - xs.storage_offset() >= M * ld:
+        return xs, ld
+    buf = _block_scale_buffer(M, n, xs)
+    buf.copy_(xs)
+    return buf, _round_up(n, 4)
+
+
 def fp8_quant_per_block(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
                         xs: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Block-scaled quantization of bf16, fp16 or fp32 x [M, K] (K a multiple of
@@ -749,10 +769,10 @@ def fp8_quant_per_block(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
     t, M, K, ld = _float_rows(x, "x")
     _block_k(K)
     x, ld = _vector_rows(x, t, ld)
-    ldq, lds = K, _blocks_of(K)
+    ldq, lds = K, _round_up(_blocks_of(K), 4)
     own = xq is None and xs is None
     xq = x.new_empty((M, K), dtype=torch.uint8) if xq is None else xq
-    xs = x.new_empty((M, lds), dtype=torch.float32) if xs is None else xs
+    xs = _block_scale_buffer(M, _blocks_of(K), x) if xs is None else xs
     if not own:
         if _block_rows(xq, xs) != (M, K):
             raise ValueError(f"xq must have shape {(M, K)}")
@@ -877,8 +897,8 @@ def fp8_block_scaled_mm(xq: torch.Tensor, xs: torch.Tensor, w_packed: torch.Tens
     M, K = _block_rows(xq, xs)
     _check_block_packed(w_packed, ws, N, K, xq)
     mode, out = _fp4_out(M, N, bias, out_dtype, out, xq)
-    xq = _rows_aligned(xq, 16)
-    _run(xq, "fp8_block_scaled_mm_tile", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), w_packed.data_ptr(),
+    xq, (xs, lds) = _rows_aligned(xq, 16), _block_scale_rows_of(xs)
+    _run(xq, "fp8_block_scaled_mm_tile", xq.data_ptr(), _ld(xq), xs.data_ptr(), lds, w_packed.data_ptr(),
          ws.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, mode, out.data_ptr(), _ld(out),
          tile=(tile,))
     return out
@@ -898,8 +918,9 @@ def fp8_block_quant_scaled_mm(x: torch.Tensor, w_packed: torch.Tensor, ws: torch
     mode, out = _fp4_out(M, N, bias, out_dtype, out, x)
     x, ld = _vector_rows(x, t, ld)
     xq = x.new_empty((M, K), dtype=torch.uint8)
-    xs = x.new_empty((M, _blocks_of(K)), dtype=torch.float32)
-    _run(x, "fp8_block_quant_scaled_mm_tile", x.data_ptr(), t, ld, xq.data_ptr(), K, xs.data_ptr(), _blocks_of(K),
+    xs = _block_scale_buffer(M, _blocks_of(K), x)
+    lds = _round_up(_blocks_of(K), 4)
+    _run(x, "fp8_block_quant_scaled_mm_tile", x.data_ptr(), t, ld, xq.data_ptr(), K, xs.data_ptr(), lds,
          w_packed.data_ptr(), ws.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, mode, out.data_ptr(),
          _ld(out), tile=(tile,))
     return out, xq, xs
@@ -917,9 +938,10 @@ def _fp8_block_linear(x: torch.Tensor, w_packed: torch.Tensor, ws: torch.Tensor,
         _same_device(x, bias)
     x, ld = _vector_rows(x, t, ld)
     out = x.new_empty((M, N))
-    xq = x.new_empty((M * (K + 4 * _blocks_of(K)),), dtype=torch.uint8)
+    lds = _round_up(_blocks_of(K), 4)
+    xq = x.new_empty((M * (K + 4 * lds),), dtype=torch.uint8)
     at = xq.data_ptr()
-    _run(x, "fp8_block_quant_scaled_mm", x.data_ptr(), t, ld, at, K, at + M * K, _blocks_of(K), w_packed.data_ptr(),
+    _run(x, "fp8_block_quant_scaled_mm", x.data_ptr(), t, ld, at, K, at + M * K, lds, w_packed.data_ptr(),
          ws.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K, _OUT_MODE[x.dtype], out.data_ptr(), N)
     return out
 
