@@ -78,34 +78,62 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int *__restric
     }
 }
 
-// out[t] = sum over the token's slots of weight * y[slot]: four columns a
-// thread. A slot without an expert has no row.
-template <int E>
-__global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ y, const int *__restrict__ ids,
+// out[t] = sum over the token's slots of weight * y[slot], y fp32 rows or fp16
+// rows under a scale per 128 columns: eight columns a thread. A slot without an
+// expert has no row.
+template <int E, bool Y16>
+__global__ __launch_bounds__(256) void combine_kernel(const void *__restrict__ y, const float *__restrict__ y_scale,
+                                                      int ld_scale, const int *__restrict__ ids,
                                                       const float *__restrict__ weights, int top_k, int experts,
                                                       int K, void *__restrict__ out, int64_t ldo, int segs)
 {
     const int64_t token = blockIdx.x / segs;
-    const int col = ((int)(blockIdx.x - token * segs) * 256 + (int)threadIdx.x) * 4;
+    const int col = ((int)(blockIdx.x - token * segs) * 256 + (int)threadIdx.x) * 8;
     if (col >= K)
         return;
-    f32x4 acc = {};
+    float acc[8] = {};
     for (int j = 0; j < top_k; ++j) {
         const int64_t slot = token * top_k + j;
         const int id = ids[slot];
         if (id < 0 || id >= experts)
             continue;
-        const float w = weights[slot];
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(y + slot * K + col);
+        float w = weights[slot], v[8];
+        if constexpr (Y16) {
+            w *= y_scale[slot * ld_scale + col / kBlock];
+            const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(y) + slot * K + col);
+            const u32 d[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 8; ++r)
+                v[r] = quant_rule::f16_to_float(d[r >> 1] >> (16 * (r & 1)));
+        } else {
+            const f32x4 *q = reinterpret_cast<const f32x4 *>(static_cast<const float *>(y) + slot * K + col);
+            const f32x4 lo = q[0], hi = q[1];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                v[r] = lo[r];
+                v[4 + r] = hi[r];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
             acc[r] = __builtin_fmaf(w, v[r], acc[r]);
     }
-    if constexpr (E == kF32)
-        *reinterpret_cast<f32x4 *>(static_cast<float *>(out) + token * ldo + col) = acc;
-    else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + token * ldo + col) =
-            make_uint2(pack2<E == kF16>(acc[0], acc[1]), pack2<E == kF16>(acc[2], acc[3]));
+    if constexpr (E == kF32) {
+        f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(out) + token * ldo + col);
+        o[0] = f32x4{acc[0], acc[1], acc[2], acc[3]};
+        o[1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
+    } else {
+        constexpr bool H = E == kF16;
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + token * ldo + col) =
+            make_uint4(pack2<H>(acc[0], acc[1]), pack2<H>(acc[2], acc[3]), pack2<H>(acc[4], acc[5]),
+                       pack2<H>(acc[6], acc[7]));
+    }
+}
+
+template <int E>
+auto combine_pick(bool y16)
+{
+    return y16 ? combine_kernel<E, true> : combine_kernel<E, false>;
 }
 
 // Tokens of one pass: what bounds the workspace and keeps every row offset of
@@ -120,7 +148,7 @@ int64_t tokens_at_once(int64_t tokens, int top_k, int64_t K)
 int64_t scale_pitch(int64_t K) { return round_up(ceil_div(K, kBlock), 4); }
 
 struct Layout {
-    size_t xq, xs, order, tiles, hq, hs, h, y, end;
+    size_t xq, xs, order, tiles, hq, hs, h, y, ys, end;
     int64_t tiles_m;
 };
 
@@ -144,7 +172,8 @@ Layout layout_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inne
     l.hq = take(slots * inner);
     l.hs = take(slots * scale_pitch(inner) * 4);
     l.h = take(small ? slots * inner * 4 : 0);
-    l.y = take(slots * K * 4);
+    l.y = take(slots * K * (small ? 4 : 2));
+    l.ys = take(small ? 0 : slots * ceil_div(K, kBlock) * 4);
     l.end = at;
     return l;
 }
@@ -181,7 +210,8 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
     const int blocks = (int)ceil_div(args.K, kBlock), inner_blocks = (int)ceil_div(args.inner, kBlock);
     uint8_t *xq = reinterpret_cast<uint8_t *>(work + l.xq), *hq = reinterpret_cast<uint8_t *>(work + l.hq);
     float *xs = reinterpret_cast<float *>(work + l.xs), *hs = reinterpret_cast<float *>(work + l.hs);
-    float *h = reinterpret_cast<float *>(work + l.h), *y = reinterpret_cast<float *>(work + l.y);
+    float *h = reinterpret_cast<float *>(work + l.h), *ys = reinterpret_cast<float *>(work + l.ys);
+    void *y = work + l.y;
     int *order = reinterpret_cast<int *>(work + l.order);
     BlockTile *tiles = reinterpret_cast<BlockTile *>(work + l.tiles);
 
@@ -238,6 +268,9 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         m.ws = args.down_scale;
         m.out = y;
         m.ldo = args.K;
+        m.vec16 = 1;
+        m.out_scale = ys;
+        m.ld_out_scale = blocks;
         m.N = (int)args.K;
         m.K = (int)args.inner;
         m.blocks = inner_blocks;
@@ -248,10 +281,10 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         hipLaunchKernelGGL(e.down, dim3((unsigned)(tiles_m * ceil_div(m.frags, e.bn / 16))), dim3(e.threads), 0,
                            stream, m);
 
-        const int segs = (int)ceil_div(args.K, 1024);
-        auto combine = args.kind == kElemF32 ? combine_kernel<kF32>
-                     : args.kind == kElemF16 ? combine_kernel<kF16> : combine_kernel<kBF16>;
-        hipLaunchKernelGGL(combine, dim3((unsigned)(tokens * segs)), dim3(256), 0, stream, y, ids,
+        const int segs = (int)ceil_div(args.K, 2048);
+        auto combine = args.kind == kElemF32 ? combine_pick<kF32>(!e.small)
+                     : args.kind == kElemF16 ? combine_pick<kF16>(!e.small) : combine_pick<kBF16>(!e.small);
+        hipLaunchKernelGGL(combine, dim3((unsigned)(tokens * segs)), dim3(256), 0, stream, y, ys, blocks, ids,
                            args.weights + t0 * args.top_k, args.top_k, args.experts, (int)args.K,
                            static_cast<char *>(args.out) + t0 * args.ldo * x_bytes, args.ldo, segs);
         err = hipGetLastError();

@@ -31,7 +31,9 @@ hipError_t launch_quant_prepack_fp8_block(const void *w, bool w_f32, int64_t ldw
 // What a launch computes: a layer's product; the gated products silu(gate) * up
 // of each expert's rows (rows of tokens by order / top_k, out in sorted rows:
 // fp32 from the small-M kernel, codes and scales from the main kernel); or the
-// down products of sorted rows (out fp32, to the rows that order names).
+// down products of sorted rows, to the rows that order names (fp32 from the
+// small-M kernel, fp16 under a scale per row and 128 channels from the main
+// kernel).
 constexpr int kJobDense = 0, kJobGateUp = 1, kJobDown = 2;
 
 // A run of rows of one expert.
@@ -54,7 +56,7 @@ struct BlockMmArgs {
     int vec_store;       // 1 when out rows allow stores of 4 consecutive elements
     int vec16;           // 1 when out rows start on 16-byte boundaries
     int tiles_m;         // row tiles of the launch, at most
-    float *out_scale;    // gated, main kernel: out are e4m3 codes, these their scales [rows, ld_out_scale]
+    float *out_scale;    // experts, main kernel: the scales [rows, ld_out_scale] of out
     int64_t ld_out_scale;
     // Experts:
     const BlockTile *tiles;   // then, at [tiles_m], their number as rows

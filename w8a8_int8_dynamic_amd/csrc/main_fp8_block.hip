@@ -10,7 +10,7 @@ constexpr BlockTileEntry entry(const char *name)
     return BlockTileEntry{name, T::BM, T::BN, T::THREADS, false,
                           {block_mm_kernel<T, kJobDense, kOutBF16>, block_mm_kernel<T, kJobDense, kOutI32>,
                            block_mm_kernel<T, kJobDense, kOutF16>},
-                          block_mm_kernel<T, kJobGateUp, kOutI32>, block_mm_kernel<T, kJobDown, kOutI32>};
+                          block_mm_kernel<T, kJobGateUp, kOutI32>, block_mm_kernel<T, kJobDown, kOutF16>};
 }
 
 // token rows x channels / wave rows and columns / LDS stages

@@ -23,9 +23,13 @@
 //     operand reads (row l%16, chunks l/16 and 4 + l/16) meet all banks. Weights
 //     come as the packed fragments are.
 //   - A wave owns TM x TN tiles: the TN weight operands of a block stay in
-//     registers, the token operands come one tile ahead. Once every wave holds
-//     its last token operand of a stage, one barrier frees the stage for the
-//     block after next and makes the next one visible.
+//     registers, the token operands come one tile ahead. A stage is freed and
+//     refilled in two parts, each at a barrier of its own: part A, the weights
+//     and the first half of the token rows, once every wave has read those (half
+//     way through the step); part B, the other rows, at the step's end. Each
+//     then has NS - 1/2 steps to land, where refilling whole stages leaves NS -
+//     1 (M8192 N4096 K12288, two stages of 64 KB, a step of 2048 matrix core
+//     cycles: 367 us so, @@ now).
 //   - Token scales go through LDS too, 16 bytes (four blocks) a row at a time;
 //     the weight's are one or two numbers per wave and block, held by the lanes
 //     of a register for 64 blocks and read from there.
@@ -45,13 +49,15 @@ namespace {
 
 using namespace fp8_block;
 
+constexpr int cmin(int a, int b) { return a < b ? a : b; }
+
 template <int BM_, int BN_, int WM_, int WN_, int NS_>
 struct BlockMain {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
     static constexpr int NW = WM * WN, THREADS = NW * 64;
     static constexpr int TM = BM / 16 / WM, TN = BN / 16 / WN;   // 16 x 16 tiles per wave
     static constexpr int LX = BM / 8 / NW, LWG = BN / 8 / NW;    // 1 KB loads per wave and stage
-    static constexpr int LPW = LX + LWG;
+    static constexpr int LPW = LX + LWG, LA = LX / 2 + LWG;      // ... of the two parts, and of part A
     static constexpr int TOK = BM * 128, STAGE = TOK + BN * 128; // bytes
     static constexpr int SX_UNITS = BM / 64, SX_SLOT = BM * 16;
     static constexpr int SX = NS * STAGE;                        // two slots of token scales
@@ -60,12 +66,23 @@ struct BlockMain {
     static constexpr int PITCH_Q = BN / 2 + 16;                  // staged row of codes (gated)
     static constexpr int TOPS = BM * PITCH_Q;                    // then WN block maxima per row
     static constexpr int LDS = cmax(cmax(RING, BM * PITCH), TOPS + WN * BM * 4);
-    static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "tile");
-    static_assert(TM % 2 == 0 && BM % 64 == 0 && NW >= SX_UNITS, "token operands alternate; scales in one load");
+    static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0 &&
+                      NS * LPW < 64, "tile");
+    static_assert(TM % 2 == 0 && LX % 2 == 0 && BM % 64 == 0 && NW >= SX_UNITS, "token operands alternate; scales in one load");
     static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
-__device__ __forceinline__ int row_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+// Where chunk c of row r (of 16) of a token image lies: slot 8r + (c ^
+// row_swz(r)). Linear in r's bits, so that the 16 bytes of each 8 or 16 lanes
+// that LDS serves together (neighbours, or 0-3, 12-15 and 20-27 with the next
+// chunk) fall in different banks whichever they are: rows 0-7, 0-3 with 12-15,
+// and even and odd rows, with and without the chunk's low bit, all get
+// different values. (With (r ^ r/8) & 7, right for neighbours alone, a third of
+// the LDS cycles were conflicts.)
+__device__ __forceinline__ int row_swz(int r)
+{
+    return ((r & 1) * 5) ^ (r & 6) ^ ((r >> 3) * 5);
+}
 
 template <class T, int JOB, int OUT>
 __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs args)
@@ -119,7 +136,7 @@ __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs 
 #pragma unroll
     for (int i = 0; i < T::LX; ++i)
         xoff[i] = token_row((i * T::NW + wave) * 8 + (lane >> 3)) * (int)a.ldq;
-    const int xchunk = ((lane & 7) ^ (lane >> 3) ^ (wave & 1)) * 16;   // (NW is even: image g's parity is the wave's)
+    const int xchunk = ((lane & 7) ^ row_swz((wave & 1) * 8 + (lane >> 3))) * 16;   // (NW is even: so is g - wave)
     const int sunit = min(wave, T::SX_UNITS - 1);
     const int soff = token_row(sunit * 64 + lane) * (int)a.lds * 4;
     const char *wb = reinterpret_cast<const char *>(a.wp) + expert * a.expert_bytes + (int64_t)f0 * S * kFrag;
@@ -157,16 +174,26 @@ __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs 
     auto dma_sx = [&](int t) __attribute__((always_inline)) {
         dma16(sxb, soff + min(t, (S - 1) & ~3) * 4, shared + T::SX + ((t >> 2) & 1) * T::SX_SLOT + sunit * 1024);
     };
-    auto dma = [&](int t, int slot) __attribute__((always_inline)) {
+    // Loads N0 .. N1-1 of part A (the first half's token images, then the weights)
+    // and of part B (the other token images).
+    auto dma_a = [&](int t, int slot, auto n0_c, auto n1_c) __attribute__((always_inline)) {
         char *st = shared + slot * T::STAGE;
         t = min(t, S - 1);
         const int kc = min(t * kBlock + xchunk, a.K - 16);
+        static_for<decltype(n1_c)::value - decltype(n0_c)::value>([&](auto U) __attribute__((always_inline)) {
+            constexpr int n = decltype(n0_c)::value + decltype(U)::value;
+            if constexpr (n < T::LX / 2)
+                dma16(xb, xoff[n] + kc, st + (n * T::NW + wave) * 1024);
+            else
+                dma16(wb, woff[n - T::LX / 2] + t * kFrag, st + T::TOK + ((n - T::LX / 2) * T::NW + wave) * 1024);
+        });
+    };
+    auto dma_b = [&](int t, int slot) __attribute__((always_inline)) {
+        char *st = shared + slot * T::STAGE;
+        const int kc = min(min(t, S - 1) * kBlock + xchunk, a.K - 16);
 #pragma unroll
-        for (int i = 0; i < T::LX; ++i)
+        for (int i = T::LX / 2; i < T::LX; ++i)
             dma16(xb, xoff[i] + kc, st + (i * T::NW + wave) * 1024);
-#pragma unroll
-        for (int i = 0; i < T::LWG; ++i)
-            dma16(wb, woff[i] + t * kFrag, st + T::TOK + (i * T::NW + wave) * 1024);
     };
 
     f32x4 acc[TM][TN];
@@ -178,6 +205,11 @@ __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs 
     v4i w[TN][2], x[2][2];
     float sx[2];
     f32x4 p[2][TN];
+    // Down: the sums of a token's scales, to bound its results by.
+    float bound[JOB == kJobDown ? TM : 1];
+#pragma unroll
+    for (int i = 0; i < (JOB == kJobDown ? TM : 1); ++i)
+        bound[i] = 0.0f;
 
     // Operands from LDS: fragment wn*TN + j, units l and 64 + l; token tile i's
     // row l%16, chunks l/16 and 4 + l/16, and its scale.
@@ -198,12 +230,13 @@ __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs 
 
     load_ws(0);
     dma_sx(0);
-    dma(0, 0);
-    if constexpr (T::NS == 3)
-        dma(1, 1);
-    wait_vm_lgkm0<0>();
+    static_for<T::NS>([&](auto U) __attribute__((always_inline)) {
+        dma_a(decltype(U)::value, decltype(U)::value, std::integral_constant<int, 0>{},
+              std::integral_constant<int, T::LA>{});
+        dma_b(decltype(U)::value, decltype(U)::value);
+    });
+    wait_vm_lgkm0<T::LX - T::LX / 2 + (T::NS - 1) * T::LPW>();   // part A of stage 0
     __builtin_amdgcn_s_barrier();
-    dma(T::NS - 1, T::NS - 1);
 #pragma unroll
     for (int j = 0; j < TN; ++j)
         read_w(shared, j);
@@ -212,6 +245,22 @@ __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs 
     // The K loop over the first LIVE token tiles of the wave.
     auto loop = [&](auto live_c) __attribute__((always_inline)) {
         constexpr int LIVE = decltype(live_c)::value;
+        static_assert(LIVE % 2 == 0, "products and scales alternate across steps too");
+        float sc[2][2] = {};                              // scales of the products in p
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            p[1][j] = f32x4{};
+        // acc += p * scale for tile i's products
+        auto add = [&](auto I) __attribute__((always_inline)) {
+            constexpr int i = decltype(I)::value;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const float s = TWO && second[j] ? sc[i & 1][1] : sc[i & 1][0];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[i][j][r] = __builtin_fmaf(p[i & 1][j][r], s, acc[i][j][r]);
+            }
+        };
         int slot = 0;
         for (int t = 0; t < S; ++t) {
             // What not every step does comes first: a branch further down would
@@ -227,52 +276,58 @@ __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs 
             float sw[2];
             sw[0] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv[0]), t & 63));
             sw[1] = TWO ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wsv[1]), t & 63)) : 0.0f;
-            float sc[2][2];
-            // acc += p * scale for tile i's products
-            auto add = [&](auto I) __attribute__((always_inline)) {
-                constexpr int i = decltype(I)::value;
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const float s = TWO && second[j] ? sc[i & 1][1] : sc[i & 1][0];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][j][r] = __builtin_fmaf(p[i & 1][j][r], s, acc[i][j][r]);
-                }
-            };
             static_for<LIVE>([&](auto I) __attribute__((always_inline)) {
                 constexpr int i = decltype(I)::value;
                 constexpr bool LAST = i == LIVE - 1;
-                if constexpr (LAST) {
-                    // Every token operand of this stage is in registers, and
-                    // the next stage has landed.
-                    wait_vm_lgkm0<T::NS == 3 ? T::LPW : 0>();
+                // Half way: every wave has its weights and the first half's
+                // tokens in registers, and this stage's part B has landed.
+                constexpr int MID = LIVE > TM / 2 ? TM / 2 - 1 : LIVE - 1;
+                if constexpr (i == MID) {
+                    wait_vm_lgkm0<(T::NS - 1) * T::LPW>();
                     __builtin_amdgcn_s_barrier();
-                    dma(t + T::NS, slot);
+                }
+                // Part A's loads are spread over the tiles up to the end.
+                constexpr int OVER = LIVE - 1 - MID;
+                constexpr int A0 = OVER == 0 ? 0 : cmin(i - MID, OVER) * T::LA / cmax(OVER, 1);
+                constexpr int A1 = OVER == 0 ? T::LA : cmin(i + 1 - MID, OVER) * T::LA / cmax(OVER, 1);
+                constexpr int LOADS = i < MID ? 0 : A1 - A0;
+                if constexpr (LOADS > 0)
+                    dma_a(t + T::NS, slot, std::integral_constant<int, A0>{}, std::integral_constant<int, A1>{});
+                if constexpr (LAST) {
+                    // The end: every token operand of this stage is in
+                    // registers, and the next stage's part A has landed.
+                    wait_vm_lgkm0<(T::NS - 1) * T::LPW>();
+                    __builtin_amdgcn_s_barrier();
+                    dma_b(t + T::NS, slot);
                     read_x(stn, t + 1, 0, x[0], sx[0]);
                 } else {
                     read_x(st, t, i + 1, x[(i + 1) & 1], sx[(i + 1) & 1]);
                 }
                 sc[i & 1][0] = sx[i & 1] * sw[0];
                 sc[i & 1][1] = TWO ? sx[i & 1] * sw[1] : 0.0f;
+                if constexpr (JOB == kJobDown)
+                    bound[i] += __builtin_fabsf(sc[i & 1][0]);
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
                     p[i & 1][j] = block_product(w[j], x[i & 1]);
                     if constexpr (LAST)
                         read_w(stn, j);
                 }
-                if constexpr (i > 0)
-                    add(std::integral_constant<int, i - 1>{});
-                // Behind each MFMA the previous tile's multiply-adds.
+                constexpr int PER = (LOADS + (LAST ? T::LX - T::LX / 2 : 0) + TN - 1) / TN;
+                // Behind each MFMA the previous tile's multiply-adds (the first
+                // tile's: the last one's of the step before).
+                add(std::integral_constant<int, i == 0 ? LIVE - 1 : i - 1>{});
                 static_for<TN>([&](auto) __attribute__((always_inline)) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);            // MFMA
+                    __builtin_amdgcn_sched_group_barrier(0x020, PER, 0);          // VMEM read
                     __builtin_amdgcn_sched_group_barrier(0x100, LAST ? 2 : 1, 0); // DS read
                     __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);            // VALU
                 });
                 __builtin_amdgcn_sched_barrier(0);
             });
-            add(std::integral_constant<int, LIVE - 1>{});
             slot = next;
         }
+        add(std::integral_constant<int, LIVE - 1>{});
     };
     if constexpr (JOB == kJobDense) {
         loop(std::integral_constant<int, TM>{});
@@ -294,21 +349,7 @@ __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs 
     // ---- epilogue ----
     // Register r of acc[i][j], lane l: channel 4*(l/16) + r of fragment wn*TN +
     // j, token 16*(i*WM + wm) + l%16 of the tile.
-    if constexpr (JOB == kJobDown) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int m = 16 * (i * T::WM + wm) + r16;
-            if (m >= rows)
-                continue;
-            const int64_t orow = a.order[row0 + m];
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const int n = 16 * (wf + j) + 4 * sub;
-                if (n < a.N)
-                    store4<OUT>(a, orow, n, acc[i][j]);
-            }
-        }
-    } else if constexpr (JOB == kJobGateUp) {
+    if constexpr (JOB == kJobGateUp) {
         // The tile's BN / 2 = 128 columns are one block of the down product's
         // rows: silu(gate) * up, the block's maximum over the WN waves that
         // share a row, and codes and scale from here, so that the inner rows
@@ -357,7 +398,8 @@ __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs 
             for (int m = threadIdx.x >> 3; m < rows; m += T::THREADS / 8)
                 *reinterpret_cast<uint4 *>(out + (int64_t)m * a.ldo) =
                     *reinterpret_cast<const uint4 *>(shared + m * T::PITCH_Q + piece);
-    } else {
+    } else if constexpr (OUT == kOutI32) {
+        // Raw sums, straight from registers.
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int m = 16 * (i * T::WM + wm) + r16;
@@ -368,6 +410,65 @@ __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs 
                 const int n = 16 * (wf + j) + 4 * sub;
                 if (n < a.N)
                     store4<OUT>(a, (int64_t)row0 + m, n, acc[i][j]);
+            }
+        }
+    } else {
+        // 16-bit rows, staged in LDS and written whole, 16 bytes a lane (M4096
+        // N4096: 9 us of 8-byte stores from registers, @@ so). Down: fp16 under a
+        // power of two per row and block of channels, so that a slot's row
+        // costs half of fp32's bytes and a quarter of the 2^-9 that bf16 would
+        // lose: |acc| <= 448 * 448 * 128 * the sum of its scales, brought below
+        // 2^15; values 2^-29 of that bound and less leave fp16's normal range.
+        constexpr bool F16 = OUT == kOutF16;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int m = 16 * (i * T::WM + wm) + r16;
+            float down = 1.0f;
+            if constexpr (JOB == kJobDown) {
+                const float top = bound[i] * (448.0f * 448.0f * 128.0f);
+                const int e = (int)((__float_as_uint(top) >> 23) & 255u) - 126 - 15;   // top < 2^(e + 15)
+                const bool odd = !(top > 0x1p-100f && top < 0x1p126f);   // zero, not finite, or out of reach
+                down = odd ? 1.0f : __uint_as_float((u32)(127 - e) << 23);
+                if (sub == 0 && (wn * TN) % 8 == 0 && m < rows && wf < a.frags)
+                    a.out_scale[(int64_t)a.order[row0 + m] * a.ld_out_scale + (wf >> 3)] =
+                        odd ? 1.0f : __uint_as_float((u32)(127 + e) << 23);
+            }
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                f32x4 v = acc[i][j];
+                if constexpr (JOB == kJobDown) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[r] *= down;
+                } else if (a.bias) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const unsigned b = a.bias[min(16 * (wf + j) + 4 * sub + r, a.N - 1)];
+                        v[r] += F16 ? quant_rule::f16_to_float(b) : __uint_as_float(b << 16);
+                    }
+                }
+                *reinterpret_cast<uint2 *>(shared + m * T::PITCH + (wn * TN + j) * 32 + sub * 8) =
+                    make_uint2(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]));
+            }
+        }
+        __syncthreads();
+        constexpr int P16 = T::BN / 8, RPP = T::THREADS / P16;   // pieces per row, rows per pass
+        const int c = threadIdx.x % P16, n = f0 * 16 + c * 8;
+        uint16_t *out = static_cast<uint16_t *>(a.out) + n;
+        if (n >= a.N)
+            return;
+        const bool whole = a.vec16 && n + 8 <= a.N;
+        for (int m = threadIdx.x / P16; m < rows; m += RPP) {
+            const int64_t orow = JOB == kJobDown ? a.order[row0 + m] : row0 + m;
+            uint16_t *o = out + orow * a.ldo;
+            const v4u v = *reinterpret_cast<const v4u *>(shared + m * T::PITCH + c * 16);
+            if (whole) {
+                __builtin_nontemporal_store(v, reinterpret_cast<v4u *>(o));
+            } else {
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (n + r < a.N)
+                        o[r] = (uint16_t)(v[r >> 1] >> (16 * (r & 1)));
             }
         }
     }
