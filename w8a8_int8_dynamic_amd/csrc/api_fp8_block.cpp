@@ -266,7 +266,12 @@ W8A8_API w8a8_status_t fp8_block_quant_scaled_mm_tile(const void *x, int x_dtype
     if (st != W8A8_OK)
         return st;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    hipError_t err = w8a8::launch_quant_fp8_block(x, x_dtype, M, K, ldx, xq, ldq, x_scale, lds, s);
+    a.x = x;
+    a.ldx = ldx;
+    hipError_t err = w8a8::launch_fp8_block_quant_mm(a, x_dtype, mode, t, s);
+    if (err != hipErrorNotSupported)
+        return launched(err, what);
+    err = w8a8::launch_quant_fp8_block(x, x_dtype, M, K, ldx, xq, ldq, x_scale, lds, s);
     if (err != hipSuccess)
         return launched(err, what);
     return launched(w8a8::launch_fp8_block_mm(a, mode, t, s), what);

@@ -14,68 +14,114 @@
 
 #include "experts.hpp"
 #include "fp8_block_device.hpp"
+#include "quant_fp8_block.hpp"
 
 namespace w8a8 {
 namespace {
 
 using namespace fp8_block;
 
-constexpr int kPlanThreads = 1024;
+constexpr int kThreads = 256, kPlanAhead = 4;
 
-// One workgroup per expert: where its rows begin (the slots of lower experts
-// come first), its slots in ascending order, and its row tiles. Every
-// workgroup counts all experts by itself (LDS counters: their sums do not
-// depend on the order), so that none waits for another.
-__global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int *__restrict__ ids, int slots, int experts,
-                                                            int bm, int *__restrict__ order,
-                                                            BlockTile *__restrict__ tiles, int tiles_m)
+// The plan of expert e by one workgroup: where its rows begin (the slots of
+// lower experts come first), its slots in ascending order, and its row tiles of
+// bm rows. Every workgroup counts all experts by itself (LDS counters: their
+// sums do not depend on the order), so that none waits for another. The last
+// one writes the number of row tiles behind them.
+__device__ __forceinline__ void plan_expert(int e, const int *__restrict__ ids, int slots, int experts, int bm,
+                                            int *__restrict__ order, BlockTile *__restrict__ tiles, int tiles_m)
 {
     __shared__ int count[kMaxExperts];
     __shared__ int sums[2];
-    __shared__ int in_wave[kPlanThreads / 64];
-    const int t = threadIdx.x, e = blockIdx.x, wave = t >> 6;
-    if (t < experts)
-        count[t] = 0;
+    __shared__ int in_wave[kPlanAhead][kThreads / 64];
+    const int t = threadIdx.x, wave = t >> 6;
+    for (int i = t; i < experts; i += kThreads)
+        count[i] = 0;
     if (t < 2)
         sums[t] = 0;
     __syncthreads();
-    for (int i = t; i < slots; i += kPlanThreads) {
-        const int id = ids[i];
-        if (id >= 0 && id < experts)
-            atomicAdd(&count[id], 1);
+    int id[kPlanAhead];
+    auto load = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < kPlanAhead; ++q) {
+            const int i = i0 + q * kThreads + t;
+            id[q] = i < slots ? ids[i] : -1;
+        }
+    };
+    for (int i0 = 0; i0 < slots; i0 += kPlanAhead * kThreads) {
+        load(i0);
+#pragma unroll
+        for (int q = 0; q < kPlanAhead; ++q)
+            if (id[q] >= 0 && id[q] < experts)
+                atomicAdd(&count[id[q]], 1);
     }
     __syncthreads();
+    int before = 0, before_tiles = 0;
+    for (int i = t; i < e; i += kThreads) {
+        before += count[i];
+        before_tiles += (count[i] + bm - 1) / bm;
+    }
     if (t < e) {
-        atomicAdd(&sums[0], count[t]);
-        atomicAdd(&sums[1], (count[t] + bm - 1) / bm);
+        atomicAdd(&sums[0], before);
+        atomicAdd(&sums[1], before_tiles);
     }
     __syncthreads();
     const int first = sums[0], tile0 = sums[1], rows = count[e], mine = (rows + bm - 1) / bm;
-    for (int i = t; i < mine; i += kPlanThreads)
+    for (int i = t; i < mine; i += kThreads)
         tiles[tile0 + i] = BlockTile{e, first + i * bm, min(bm, rows - i * bm)};
     if (e == experts - 1 && t == 0)
         tiles[tiles_m] = BlockTile{-1, 0, tile0 + mine};
     if (rows == 0)
         return;
     int at = first;
-    for (int i0 = 0; i0 < slots; i0 += kPlanThreads) {
-        const int i = i0 + t;
-        const bool hit = i < slots && ids[i] == e;
-        const unsigned long long mask = __ballot(hit);
-        if ((t & 63) == 0)
-            in_wave[wave] = __popcll(mask);
-        __syncthreads();
-        int before = 0, all = 0;
+    for (int i0 = 0; i0 < slots; i0 += kPlanAhead * kThreads) {
+        if (slots > kPlanAhead * kThreads)                // (a single run is still in registers)
+            load(i0);
+        unsigned long long mask[kPlanAhead];
 #pragma unroll
-        for (int w = 0; w < kPlanThreads / 64; ++w) {
-            before += w < wave ? in_wave[w] : 0;
-            all += in_wave[w];
+        for (int q = 0; q < kPlanAhead; ++q) {
+            mask[q] = __ballot(id[q] == e);
+            if ((t & 63) == 0)
+                in_wave[q][wave] = __popcll(mask[q]);
         }
-        if (hit)
-            order[at + before + __popcll(mask & ((1ull << (t & 63)) - 1))] = i;
-        at += all;
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kPlanAhead; ++q) {
+            int lower = 0, all = 0;
+#pragma unroll
+            for (int w = 0; w < kThreads / 64; ++w) {
+                lower += w < wave ? in_wave[q][w] : 0;
+                all += in_wave[q][w];
+            }
+            if (id[q] == e)
+                order[at + lower + __popcll(mask[q] & ((1ull << (t & 63)) - 1))] = i0 + q * kThreads + t;
+            at += all;
+        }
         __syncthreads();
     }
+}
+
+// The plan, one workgroup per expert, and beside it the quantization of the
+// tokens' rows: neither waits for the other.
+template <int E, int U>
+__global__ __launch_bounds__(kThreads) void prepare_kernel(const int *__restrict__ ids, int slots, int experts, int bm,
+                                                           int *__restrict__ order, BlockTile *__restrict__ tiles,
+                                                           int tiles_m, const char *__restrict__ x, int64_t rows,
+                                                           int units, int padded, int64_t ldx, uint8_t *__restrict__ q,
+                                                           int64_t ldq, float *__restrict__ s, int64_t lds, int segs,
+                                                           int rpb)
+{
+    if ((int)blockIdx.x < experts)
+        plan_expert(blockIdx.x, ids, slots, experts, bm, order, tiles, tiles_m);
+    else
+        quant_block_rows<E, U>(blockIdx.x - experts, x, rows, units, padded, ldx, q, ldq, s, lds, segs, rpb);
+}
+
+template <int E>
+auto prepare_pick(int u)
+{
+    return u == 1 ? prepare_kernel<E, 1> : u == 2 ? prepare_kernel<E, 2>
+         : u == 3 ? prepare_kernel<E, 3> : prepare_kernel<E, 4>;
 }
 
 // out[t] = sum over the token's slots of weight * y[slot], y fp32 rows or fp16
@@ -136,6 +182,11 @@ auto combine_pick(bool y16)
     return y16 ? combine_kernel<E, true> : combine_kernel<E, false>;
 }
 
+// Slots that are run without a plan, each with its expert's weights to itself:
+// the plan's launch costs about as much as reading a weight twice for one slot in
+// sixteen.
+constexpr int kDirectSlots = 16;
+
 // Tokens of one pass: what bounds the workspace and keeps every row offset of
 // the codes within 31 bits.
 int64_t tokens_at_once(int64_t tokens, int top_k, int64_t K)
@@ -149,39 +200,60 @@ int64_t scale_pitch(int64_t K) { return round_up(ceil_div(K, kBlock), 4); }
 
 struct Layout {
     size_t xq, xs, order, tiles, hq, hs, h, y, ys, end;
-    int64_t tiles_m;
 };
 
-Layout layout_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner, const BlockTileEntry &e)
+// How a pass runs: slots alone in two launches, or by a plan, on tiles of the
+// main kernel or of the small-M one (those of the up and the down products).
+struct Path {
+    bool direct;
+    const BlockTileEntry *up, *down;
+    bool small() const { return up->small; }
+};
+
+Path path_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
+{
+    const int64_t slots = tokens * top_k, rows = slots / experts;   // rows of an expert, on average
+    Path p{};
+    if (rows > 32) {
+        p.up = p.down = &fp8_block_main(rows > 128 ? 0 : rows > 64 ? 1 : 2);
+        return p;
+    }
+    p.direct = slots <= kDirectSlots && fp8_block_direct_fits(top_k, K, inner);
+    auto small = [](int64_t k) { return &fp8_block_small(k > 1024 ? 1 : 2); };
+    p.up = small(K);
+    p.down = small(inner);
+    return p;
+}
+
+// Row tiles of a launch, at most.
+int64_t most_tiles(int64_t slots, int experts, int bm) { return slots / bm + std::min<int64_t>(experts, slots); }
+
+Layout layout_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner, const Path &p)
 {
     Layout l;
-    const int bm = e.bm;
-    const bool small = e.small;
     const int64_t slots = tokens * top_k;
-    l.tiles_m = slots / bm + std::min<int64_t>(experts, slots);
+    const bool small = p.small();
     size_t at = 0;
     auto take = [&](int64_t bytes) {
-        const size_t p = at;
+        const size_t o = at;
         at += (size_t)round_up(bytes, 256);
-        return p;
+        return o;
     };
+    l.h = take(small ? slots * inner * 4 : 0);
+    if (p.direct) {
+        l.end = at;
+        return l;
+    }
     l.xq = take(tokens * K);
     l.xs = take(tokens * scale_pitch(K) * 4);
     l.order = take(slots * 4);
-    l.tiles = take((l.tiles_m + 1) * (int64_t)sizeof(BlockTile));
+    l.tiles = take((most_tiles(slots, experts, p.up->bm) + 1) * (int64_t)sizeof(BlockTile));
     l.hq = take(slots * inner);
     l.hs = take(slots * scale_pitch(inner) * 4);
-    l.h = take(small ? slots * inner * 4 : 0);
     l.y = take(slots * K * (small ? 4 : 2));
     l.ys = take(small ? 0 : slots * ceil_div(K, kBlock) * 4);
     l.end = at;
     return l;
-}
-
-const BlockTileEntry &tile_of_call(int64_t tokens, int top_k, int experts)
-{
-    const int64_t rows = tokens * top_k / experts;       // of an expert, on average
-    return rows > 128 ? fp8_block_main(0) : rows > 32 ? fp8_block_main(1) : fp8_block_small(0);
 }
 
 }  // namespace
@@ -189,104 +261,125 @@ const BlockTileEntry &tile_of_call(int64_t tokens, int top_k, int experts)
 size_t experts_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
 {
     const int64_t step = tokens_at_once(tokens, top_k, K);
-    return layout_of(step, top_k, experts, K, inner, tile_of_call(step, top_k, experts)).end;
+    return layout_of(step, top_k, experts, K, inner, path_of(step, top_k, experts, K, inner)).end;
 }
 
 bool experts_fit(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
 {
     const int64_t step = tokens_at_once(tokens, top_k, K);
-    const BlockTileEntry &e = tile_of_call(step, top_k, experts);
-    const int64_t tiles_m = step * top_k / e.bm + std::min<int64_t>(experts, step * top_k);
-    return mm_grid_fits(tiles_m * ceil_div(std::max(2 * inner, K), e.bn), e.threads);
+    const Path p = path_of(step, top_k, experts, K, inner);
+    const int64_t tiles_m = most_tiles(step * top_k, experts, p.up->bm);
+    return mm_grid_fits(tiles_m * ceil_div(2 * inner, p.up->bn), p.up->threads) &&
+           mm_grid_fits(tiles_m * ceil_div(K, p.down->bn), p.down->threads);
 }
 
 hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t stream)
 {
     const int64_t step = tokens_at_once(args.tokens, args.top_k, args.K);
-    const BlockTileEntry &e = tile_of_call(step, args.top_k, args.experts);
-    const Layout l = layout_of(step, args.top_k, args.experts, args.K, args.inner, e);
+    // (the last pass, if shorter, runs as the others do)
+    const Path p = path_of(step, args.top_k, args.experts, args.K, args.inner);
+    const Layout l = layout_of(step, args.top_k, args.experts, args.K, args.inner, p);
     char *work = static_cast<char *>(workspace);
     const int x_bytes = args.kind == kElemF32 ? 4 : 2;
     const int blocks = (int)ceil_div(args.K, kBlock), inner_blocks = (int)ceil_div(args.inner, kBlock);
-    uint8_t *xq = reinterpret_cast<uint8_t *>(work + l.xq), *hq = reinterpret_cast<uint8_t *>(work + l.hq);
-    float *xs = reinterpret_cast<float *>(work + l.xs), *hs = reinterpret_cast<float *>(work + l.hs);
-    float *h = reinterpret_cast<float *>(work + l.h), *ys = reinterpret_cast<float *>(work + l.ys);
-    void *y = work + l.y;
-    int *order = reinterpret_cast<int *>(work + l.order);
-    BlockTile *tiles = reinterpret_cast<BlockTile *>(work + l.tiles);
 
     for (int64_t t0 = 0; t0 < args.tokens; t0 += step) {
         const int64_t tokens = std::min(args.tokens - t0, step);
         const int slots = (int)(tokens * args.top_k);
         const int *ids = args.ids + t0 * args.top_k;
-        hipError_t err = launch_quant_fp8_block(static_cast<const char *>(args.x) + t0 * args.ldx * x_bytes, args.kind,
-                                                tokens, args.K, args.ldx, xq, args.K, xs, scale_pitch(args.K),
-                                                stream);
-        if (err != hipSuccess)
-            return err;
-        const int tiles_m = (int)(slots / e.bm + std::min(args.experts, slots));
-        hipLaunchKernelGGL(plan_kernel, dim3(args.experts), dim3(kPlanThreads), 0, stream, ids, slots, args.experts,
-                           e.bm, order, tiles, tiles_m);
+        const float *weights = args.weights + t0 * args.top_k;
+        const char *x = static_cast<const char *>(args.x) + t0 * args.ldx * x_bytes;
+        char *out = static_cast<char *>(args.out) + t0 * args.ldo * x_bytes;
 
-        BlockMmArgs m{};
-        m.tiles = tiles;
-        m.tiles_m = tiles_m;
-        m.order = order;
-        m.top_k = args.top_k;
-        m.vec_store = 1;
-        m.xq = xq;
-        m.xs = xs;
-        m.ldq = args.K;
-        m.lds = scale_pitch(args.K);
-        m.wp = args.gate_up;
-        m.ws = args.gate_up_scale;
-        m.out = e.small ? static_cast<void *>(h) : hq;
-        m.ldo = args.inner;
-        m.out_scale = hs;
-        m.ld_out_scale = scale_pitch(args.inner);
-        m.M = slots;
-        m.N = (int)(2 * args.inner);
-        m.K = (int)args.K;
-        m.blocks = blocks;
-        m.frags = (int)fp8_block_frags(m.N, true);
-        m.half_scales = inner_blocks;
-        m.expert_bytes = (int64_t)m.frags * blocks * kFrag;
-        m.expert_scales = (int64_t)2 * inner_blocks * blocks;
-        hipLaunchKernelGGL(e.gate_up, dim3((unsigned)(tiles_m * ceil_div(m.frags, e.bn / 16))), dim3(e.threads), 0,
-                           stream, m);
-        if (e.small) {
-            err = launch_quant_fp8_block(h, kElemF32, slots, args.inner, args.inner, hq, args.inner, hs,
+        BlockMmArgs up{}, down{};
+        up.top_k = down.top_k = args.top_k;
+        up.experts = down.experts = args.experts;
+        up.vec_store = down.vec_store = down.vec16 = 1;
+        up.M = down.M = slots;
+        up.wp = args.gate_up;
+        up.ws = args.gate_up_scale;
+        up.N = (int)(2 * args.inner);
+        up.K = (int)args.K;
+        up.blocks = blocks;
+        up.frags = (int)fp8_block_frags(up.N, true);
+        up.half_scales = inner_blocks;
+        up.expert_bytes = (int64_t)up.frags * blocks * kFrag;
+        up.expert_scales = (int64_t)2 * inner_blocks * blocks;
+        up.ldo = args.inner;
+        down.wp = args.down;
+        down.ws = args.down_scale;
+        down.N = (int)args.K;
+        down.K = (int)args.inner;
+        down.blocks = inner_blocks;
+        down.frags = (int)fp8_block_frags(down.N, false);
+        down.expert_bytes = (int64_t)down.frags * inner_blocks * kFrag;
+        down.expert_scales = fp8_block_scale_rows(down.N, false) * inner_blocks;
+
+        hipError_t err;
+        if (p.direct) {
+            up.ids = down.ids = ids;
+            up.x = x;
+            up.ldx = args.ldx;
+            up.out = work + l.h;
+            down.weights = weights;
+            down.x = work + l.h;
+            down.ldx = args.inner;
+            down.out = out;
+            down.ldo = args.ldo;
+            err = launch_fp8_block_direct(up, down, args.kind, (int)tokens, stream);
+            if (err != hipSuccess)
+                return err;
+            continue;
+        }
+
+        uint8_t *xq = reinterpret_cast<uint8_t *>(work + l.xq), *hq = reinterpret_cast<uint8_t *>(work + l.hq);
+        float *xs = reinterpret_cast<float *>(work + l.xs), *hs = reinterpret_cast<float *>(work + l.hs);
+        float *ys = reinterpret_cast<float *>(work + l.ys);
+        int *order = reinterpret_cast<int *>(work + l.order);
+        BlockTile *tiles = reinterpret_cast<BlockTile *>(work + l.tiles);
+        const int bm = p.up->bm, tiles_m = (int)most_tiles(slots, args.experts, bm);
+        const int units = (int)(args.K / 8), padded = blocks * 16;
+        const Cut c = cut_of(tokens, padded);
+        auto prepare = args.kind == kElemF32 ? prepare_pick<kF32>(c.u)
+                     : args.kind == kElemF16 ? prepare_pick<kF16>(c.u) : prepare_pick<kBF16>(c.u);
+        hipLaunchKernelGGL(prepare, dim3((unsigned)(args.experts + c.blocks)), dim3(kThreads), 0, stream, ids, slots,
+                           args.experts, bm, order, tiles, tiles_m, x, tokens, units, padded, args.ldx, xq, args.K, xs,
+                           scale_pitch(args.K), c.segs, c.rpb);
+
+        up.tiles = down.tiles = tiles;
+        up.tiles_m = down.tiles_m = tiles_m;
+        up.order = down.order = order;
+        up.xq = xq;
+        up.xs = xs;
+        up.ldq = args.K;
+        up.lds = scale_pitch(args.K);
+        up.out = p.small() ? static_cast<void *>(work + l.h) : hq;
+        up.out_scale = hs;
+        up.ld_out_scale = scale_pitch(args.inner);
+        hipLaunchKernelGGL(p.up->gate_up, dim3((unsigned)(tiles_m * ceil_div(up.frags, p.up->bn / 16))),
+                           dim3(p.up->threads), 0, stream, up);
+        if (p.small()) {
+            err = launch_quant_fp8_block(work + l.h, kElemF32, slots, args.inner, args.inner, hq, args.inner, hs,
                                          scale_pitch(args.inner), stream);
             if (err != hipSuccess)
                 return err;
         }
-        m.xq = hq;
-        m.xs = hs;
-        m.ldq = args.inner;
-        m.lds = scale_pitch(args.inner);
-        m.wp = args.down;
-        m.ws = args.down_scale;
-        m.out = y;
-        m.ldo = args.K;
-        m.vec16 = 1;
-        m.out_scale = ys;
-        m.ld_out_scale = blocks;
-        m.N = (int)args.K;
-        m.K = (int)args.inner;
-        m.blocks = inner_blocks;
-        m.frags = (int)fp8_block_frags(m.N, false);
-        m.half_scales = 0;
-        m.expert_bytes = (int64_t)m.frags * inner_blocks * kFrag;
-        m.expert_scales = fp8_block_scale_rows(m.N, false) * inner_blocks;
-        hipLaunchKernelGGL(e.down, dim3((unsigned)(tiles_m * ceil_div(m.frags, e.bn / 16))), dim3(e.threads), 0,
-                           stream, m);
+        down.xq = hq;
+        down.xs = hs;
+        down.ldq = args.inner;
+        down.lds = scale_pitch(args.inner);
+        down.out = work + l.y;
+        down.ldo = args.K;
+        down.out_scale = ys;
+        down.ld_out_scale = blocks;
+        hipLaunchKernelGGL(p.down->down, dim3((unsigned)(tiles_m * ceil_div(down.frags, p.down->bn / 16))),
+                           dim3(p.down->threads), 0, stream, down);
 
         const int segs = (int)ceil_div(args.K, 2048);
-        auto combine = args.kind == kElemF32 ? combine_pick<kF32>(!e.small)
-                     : args.kind == kElemF16 ? combine_pick<kF16>(!e.small) : combine_pick<kBF16>(!e.small);
-        hipLaunchKernelGGL(combine, dim3((unsigned)(tokens * segs)), dim3(256), 0, stream, y, ys, blocks, ids,
-                           args.weights + t0 * args.top_k, args.top_k, args.experts, (int)args.K,
-                           static_cast<char *>(args.out) + t0 * args.ldo * x_bytes, args.ldo, segs);
+        auto combine = args.kind == kElemF32 ? combine_pick<kF32>(!p.small())
+                     : args.kind == kElemF16 ? combine_pick<kF16>(!p.small()) : combine_pick<kBF16>(!p.small());
+        hipLaunchKernelGGL(combine, dim3((unsigned)(tokens * segs)), dim3(256), 0, stream, work + l.y, ys, blocks, ids,
+                           weights, args.top_k, args.experts, (int)args.K, out, args.ldo, segs);
         err = hipGetLastError();
         if (err != hipSuccess)
             return err;

@@ -61,7 +61,12 @@ struct BlockMmArgs {
     // Experts:
     const BlockTile *tiles;   // then, at [tiles_m], their number as rows
     const int *order;    // slot (token * top_k + choice) of each sorted row
-    int top_k;
+    int top_k, experts;
+    const int *ids;      // direct: the slots' experts, without a plan
+    const float *weights;
+    // Rows to quantize in the same launch (direct down: fp32 inner rows).
+    const void *x;
+    int64_t ldx;
     int64_t expert_bytes, expert_scales;   // from one expert's weight and scales to the next's
 };
 
@@ -76,10 +81,21 @@ int fp8_block_main_count();
 const BlockTileEntry &fp8_block_main(int i);
 int fp8_block_small_count();
 const BlockTileEntry &fp8_block_small(int i);
+// The quant of a.x (element kind x_kind) and small-M tile i in one launch;
+// hipErrorNotSupported (nothing launched) where a workgroup's rows are too many
+// to be quantized by each.
+hipError_t launch_fp8_block_small_quant(BlockMmArgs a, int x_kind, int mode, int i, hipStream_t stream);
+// Experts of a few tokens in two launches: the gated products of every slot
+// (up.M of them, rows of x quantized on the way, out fp32) and the down
+// products with the sum over slots. Whether rows of those lengths fit.
+bool fp8_block_direct_fits(int top_k, int64_t K, int64_t inner);
+hipError_t launch_fp8_block_direct(BlockMmArgs up, BlockMmArgs down, int x_kind, int tokens, hipStream_t stream);
 
 int fp8_block_tile_count();
 const BlockTileEntry &fp8_block_tile(int tile);
 int fp8_block_tile_auto(int64_t M, int64_t N, int64_t K);
+// The quant of a.x and the matmul in one launch, as launch_fp8_block_small_quant.
+hipError_t launch_fp8_block_quant_mm(const BlockMmArgs &a, int x_kind, int mode, int tile, hipStream_t stream);
 hipError_t launch_fp8_block_mm(BlockMmArgs a, int mode, int tile, hipStream_t stream);
 
 }  // namespace w8a8

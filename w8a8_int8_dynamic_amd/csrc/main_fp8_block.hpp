@@ -68,7 +68,8 @@ struct BlockMain {
     static constexpr int LDS = cmax(cmax(RING, BM * PITCH), TOPS + WN * BM * 4);
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0 &&
                       NS * LPW < 64, "tile");
-    static_assert(TM % 2 == 0 && LX % 2 == 0 && BM % 64 == 0 && NW >= SX_UNITS, "token operands alternate; scales in one load");
+    static_assert(TM % 2 == 0 && LX % 2 == 0 && BM % 64 == 0 && NW >= SX_UNITS && NW % 2 == 0 && NS <= 4,
+                  "token operands alternate; scales in one load, two slots of four blocks");
     static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
@@ -85,7 +86,7 @@ __device__ __forceinline__ int row_swz(int r)
 }
 
 template <class T, int JOB, int OUT>
-__global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs args)
+__global__ __launch_bounds__(T::THREADS, 2) void block_mm_kernel(const BlockMmArgs args)
 {
     __shared__ uint4 lds[T::LDS / 16];
     char *const shared = reinterpret_cast<char *>(lds);
@@ -206,6 +207,7 @@ __global__ __launch_bounds__(T::THREADS) void block_mm_kernel(const BlockMmArgs 
     float sx[2];
     f32x4 p[2][TN];
     // Down: the sums of a token's scales, to bound its results by.
+    static_assert(JOB != kJobDown || 8 % TN == 0, "a wave's channels share a block");
     float bound[JOB == kJobDown ? TM : 1];
 #pragma unroll
     for (int i = 0; i < (JOB == kJobDown ? TM : 1); ++i)

@@ -10,35 +10,12 @@
 // units in whole blocks (idle lanes count as zeros).
 #include <algorithm>
 
-#include "fp8_block.hpp"
-#include "fp8_block_rule.hpp"
+#include "quant_fp8_block.hpp"
 
 namespace w8a8 {
 namespace {
 
 using namespace fp8_block;
-
-// The row and first unit (8 elements; units of whole blocks) of this thread.
-struct Place {
-    int64_t row;
-    int unit0;
-    bool valid;
-};
-__device__ __forceinline__ Place place_of(int64_t b, int64_t rows, int padded, int segs, int rpb, int per_block)
-{
-    Place p;
-    if (rpb == 1) {
-        p.row = b / segs;
-        p.unit0 = (int)(b - p.row * segs) * per_block + (int)threadIdx.x;
-        p.valid = p.row < rows;
-    } else {
-        const int r = (int)threadIdx.x / padded;
-        p.row = b * rpb + r;
-        p.unit0 = (int)threadIdx.x - r * padded;
-        p.valid = r < rpb && p.row < rows;
-    }
-    return p;
-}
 
 template <int E, int U>
 __global__ __launch_bounds__(256) void quant_fp8_block_kernel(const char *__restrict__ x, int64_t rows, int units,
@@ -46,35 +23,7 @@ __global__ __launch_bounds__(256) void quant_fp8_block_kernel(const char *__rest
                                                               int64_t ldq, float *__restrict__ s, int64_t lds,
                                                               int segs, int rpb)
 {
-    const Place p = place_of(blockIdx.x, rows, padded, segs, rpb, 256 * U);
-    constexpr int BYTES = quant_rule::Elem<E>::BYTES;
-    uint4 lo[U], hi[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int u = p.unit0 + i * 256;
-        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
-        if (p.valid && u < units) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(x + (p.row * ldx + (int64_t)u * 8) * BYTES);
-            if (E == kF32) {
-                lo[i] = src[0];
-                hi[i] = src[1];
-            } else {
-                const quant_rule::v4u t = __builtin_nontemporal_load(reinterpret_cast<const quant_rule::v4u *>(src));
-                lo[i] = make_uint4(t[0], t[1], t[2], t[3]);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int u = p.unit0 + i * 256;
-        float sc, inv;
-        scale_of(row16_max(absmax8<E>(lo[i], hi[i])), sc, inv);
-        if (p.valid && u < units) {
-            *reinterpret_cast<uint2 *>(q + p.row * ldq + (int64_t)u * 8) = codes8<E>(lo[i], hi[i], inv);
-            if ((u & 15) == 0)
-                s[p.row * lds + (u >> 4)] = sc;
-        }
-    }
+    quant_block_rows<E, U>(blockIdx.x, x, rows, units, padded, ldx, q, ldq, s, lds, segs, rpb);
 }
 
 // 8 codes a thread back to their values, rounded to the output's type.
@@ -216,34 +165,6 @@ __global__ __launch_bounds__(256) void quant_prepack_fp8_block_kernel(const char
         const int64_t nb = half ? (col >> 4) * 2 + which : col >> 4;
         packed[((e * frags + nb) * blocks + kb) * 128 + c * 16 + (col & 15)] = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
-}
-
-// How rows of `units` units (`padded` with those of the last block) are cut
-// over workgroups of 256 threads with up to four units each: enough
-// workgroups first (one unit a thread below about 1024 of them), then as few
-// idle threads as four or three units leave.
-struct Cut {
-    int u, segs, rpb;
-    int64_t blocks;
-};
-Cut cut_of(int64_t rows, int padded)
-{
-    Cut c;
-    const int n = (int)ceil_div(padded, 256);
-    if (padded <= 128) {
-        c.u = 1;
-        c.segs = 1;
-        c.rpb = 256 / padded;
-        c.blocks = ceil_div(rows, c.rpb);
-        return c;
-    }
-    c.u = n <= 4 ? n : (round_up(n, 3) < round_up(n, 4) ? 3 : 4);
-    if (rows * ceil_div(n, c.u) < 1024)
-        c.u = 1;
-    c.segs = (int)ceil_div(n, c.u);
-    c.rpb = 1;
-    c.blocks = rows * c.segs;
-    return c;
 }
 
 template <int E>

@@ -12,7 +12,13 @@ const BlockTileEntry &fp8_block_tile(int tile)
 
 int fp8_block_tile_auto(int64_t M, int64_t N, int64_t K)
 {
-    return M <= 64 ? 2 : M <= 512 ? 1 : 0;
+    return M <= 64 ? (N * K > (16 << 20) && M <= 16 ? 8 : 7) : M <= 512 ? 1 : 0;
+}
+
+hipError_t launch_fp8_block_quant_mm(const BlockMmArgs &a, int x_kind, int mode, int tile, hipStream_t stream)
+{
+    const int n = fp8_block_main_count();
+    return tile < n ? hipErrorNotSupported : launch_fp8_block_small_quant(a, x_kind, mode, tile - n, stream);
 }
 
 hipError_t launch_fp8_block_mm(BlockMmArgs a, int mode, int tile, hipStream_t stream)

@@ -1,5 +1,6 @@
 // Small-M block-scaled e4m3 matmul, for gfx950: a handful of token rows
-// against a large weight, of a layer or of each expert that has rows.
+// against a large weight, of a layer or of each expert that has rows, with the
+// quantization of the rows in the same launch where they are few.
 //   acc[m,n] = sum over blocks b of 128 of
 //              xs[m,b] * ws[n/128,b] * sum over k in b of e4m3(xq[m,k]) * e4m3(wq[n,k])
 // The products of a block are one v_mfma_scale_f32_16x16x128_f8f6f4 with unit
@@ -7,12 +8,22 @@
 // fused multiply-add each with the block's scale, in fp32.
 //
 // The weight stream bounds it (1 byte per weight), so it is spread over as
-// many wavefronts as the shape gives: a workgroup owns 16*FN channels and 16
-// token rows, its WK wavefronts take the blocks of K in turn, U of them at a
-// time with every load issued before the first product, and the partial sums
-// meet in LDS once at the end. The packed fragment is the MFMA's A operand as
-// stored, the token rows its B operand, so a lane holds runs of four channels
-// of one token.
+// many wavefronts as the shape gives, each with U blocks of weights in flight
+// before its first product: a workgroup owns 16 token rows and 16*FN*WN
+// channels, its WK wavefronts along K take the blocks in turn, and the partial
+// sums meet in LDS once at the end. The packed fragment is the MFMA's A operand
+// as stored, the token rows its B operand, so a lane holds runs of four
+// channels of one token.
+//   - WK = 8 where K has many blocks, WK = 2 beside WN = 4 where it has few: a
+//     wave with a single block waits for it and then for its neighbours (48
+//     tokens to 64 experts, K 1024: @@ us with WK = 8, @@ so).
+//   - NT: weights that one row tile reads pass the caches by (M1 N12288 K4096:
+//     11.7 us without, 10.3 so, 4.9 TB/s; below 16 MB, which the caches may
+//     hold, 4.6 without and 5.0 so).
+//   - QK: the rows come as floats. Every workgroup quantizes them into LDS
+//     while its first weights are on their way, 8 elements a thread at a time
+//     (they are few and sit in L2); the workgroups of the first channels write
+//     codes and scales out. Up to kSlots such steps (as in the 4-bit layer's).
 // Ragged tails: token rows past the last read that one again and fragments
 // past the weight its last (never stored); k-chunks past K read the row's last
 // chunk, which meets zero weights.
@@ -25,35 +36,109 @@ namespace {
 
 using namespace fp8_block;
 
-template <int FN_, int WK_, int U_>
+template <int FN_, int WN_, int WK_, int U_, bool NT_>
 struct Small {
-    static constexpr int FN = FN_, WK = WK_, U = U_;
-    static constexpr int BM = 16, BN = 16 * FN, THREADS = 64 * WK;
+    static constexpr int FN = FN_, WN = WN_, WK = WK_, U = U_;
+    static constexpr bool NT = NT_;
+    static constexpr int BM = 16, BF = FN * WN, BN = 16 * BF, THREADS = 64 * WN * WK;
 };
 
-template <class S, int JOB, int OUT>
+constexpr int kCodes = -1;       // QK: codes and scales made before
+constexpr int kSlots = 4;        // units of 8 elements that a thread quantizes, at most
+
+// Bytes of LDS behind one quantized row: the codes of whole blocks, then the scales.
+__host__ __device__ constexpr int row_bytes(int blocks) { return blocks * 128 + (blocks * 4 + 15) / 16 * 16; }
+
+// `rows` rows of x (row r at source(r)) quantized by the workgroup into LDS, row
+// r at r * row_bytes, and with `writer` to xq and xs. The rows' units of 8
+// elements, in whole blocks, are one list, dealt out THREADS at a time; a
+// block's 16 are neighbouring lanes'.
+template <int THREADS, int E, class Source>
+__device__ __forceinline__ void quantize_rows(const BlockMmArgs &a, Source &&source, int rows, bool writer, int row0,
+                                              char *tok)
+{
+    constexpr int XB = quant_rule::Elem<E>::BYTES;
+    const int per_row = a.blocks * 16, total = rows * per_row;
+    uint4 lo[kSlots], hi[kSlots];
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+        const int at = s * THREADS + (int)threadIdx.x, r = at / per_row, u = at - r * per_row;
+        lo[s] = hi[s] = make_uint4(0, 0, 0, 0);
+        if (at < total && u * 8 < a.K) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(source(r) + (int64_t)u * 8 * XB);
+            lo[s] = src[0];
+            if (E == kF32)
+                hi[s] = src[1];
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+        if (s * THREADS >= total)
+            break;
+        const int at = s * THREADS + (int)threadIdx.x, r = at / per_row, u = at - r * per_row;
+        float sc, f;
+        scale_of(row16_max(absmax8<E>(lo[s], hi[s])), sc, f);
+        const uint2 c = codes8<E>(lo[s], hi[s], f);
+        if (at >= total)
+            continue;
+        char *row = tok + r * row_bytes(a.blocks);
+        *reinterpret_cast<uint2 *>(row + u * 8) = c;
+        if ((u & 15) == 0)
+            *reinterpret_cast<float *>(row + a.blocks * 128 + (u >> 4) * 4) = sc;
+        if (writer && u * 8 < a.K) {
+            *reinterpret_cast<uint2 *>(const_cast<uint8_t *>(a.xq) + (int64_t)(row0 + r) * a.ldq + u * 8) = c;
+            if ((u & 15) == 0)
+                const_cast<float *>(a.xs)[(int64_t)(row0 + r) * a.lds + (u >> 4)] = sc;
+        }
+    }
+}
+
+template <class S, int JOB, int OUT, int QK>
 __global__ __launch_bounds__(S::THREADS) void block_mm_small_kernel(const BlockMmArgs a)
 {
-    __shared__ f32x4 part[S::WK - 1][S::FN][64];
+    __shared__ f32x4 part[S::WN][S::WK - 1][S::FN][64];
+    extern __shared__ __attribute__((aligned(16))) char tok[];   // QK: the quantized rows
 
     const int lane = threadIdx.x & 63;
-    const int wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wk = wave % S::WK, wn = wave / S::WK;
     const int r16 = lane & 15, sub = lane >> 4;
-    const int tiles_n = (a.frags + S::FN - 1) / S::FN;
-    // (an experts' launch holds room for more row tiles than there are)
-    const int tiles_m = JOB == kJobDense ? a.tiles_m : a.tiles[a.tiles_m].rows;
-    if (JOB != kJobDense && (int)blockIdx.x >= tiles_m * tiles_n)
-        return;
-    const int t = xcd_remap(blockIdx.x, tiles_m * tiles_n);
-    const int tm = t % tiles_m, nb0 = (t / tiles_m) * S::FN;
-    const BlockTile tile = JOB == kJobDense ? BlockTile{0, tm * S::BM, min(S::BM, a.M - tm * S::BM)} : a.tiles[tm];
+    const int tiles_n = (a.frags + S::BF - 1) / S::BF;
+    BlockTile tile;
+    int tn;
+    if constexpr (JOB == kJobGateUp && QK != kCodes) {
+        // A slot is a tile of its own: its expert by its id.
+        const int t = xcd_remap(blockIdx.x, a.M * tiles_n), slot = t % a.M;
+        tn = t / a.M;
+        tile = BlockTile{a.ids[slot], slot, 1};
+        if (tile.expert < 0 || tile.expert >= a.experts)
+            return;
+    } else {
+        // (an experts' launch holds room for more row tiles than there are)
+        const int tiles_m = JOB == kJobDense ? a.tiles_m : a.tiles[a.tiles_m].rows;
+        if (JOB != kJobDense && (int)blockIdx.x >= tiles_m * tiles_n)
+            return;
+        const int t = xcd_remap(blockIdx.x, tiles_m * tiles_n);
+        const int tm = t % tiles_m;
+        tn = t / tiles_m;
+        tile = JOB == kJobDense ? BlockTile{0, tm * S::BM, min(S::BM, a.M - tm * S::BM)} : a.tiles[tm];
+    }
+    const int nb0 = tn * S::BF + wn * S::FN;
     const uint8_t *wp = a.wp + tile.expert * a.expert_bytes;
     const float *ws = a.ws + tile.expert * a.expert_scales;
 
-    const int row = tile.row0 + min(r16, tile.rows - 1);
-    const int64_t src = JOB == kJobGateUp ? a.order[row] / a.top_k : row;
-    const uint8_t *xrow = a.xq + src * a.ldq;
-    const float *xsrow = a.xs + src * a.lds;
+    const int r = min(r16, tile.rows - 1);
+    const char *xrow, *xsrow;                              // this lane's row of codes and scales
+    if constexpr (QK == kCodes) {
+        const int64_t src = JOB == kJobGateUp ? a.order[tile.row0 + r] / a.top_k : tile.row0 + r;
+        xrow = reinterpret_cast<const char *>(a.xq) + src * a.ldq;
+        xsrow = reinterpret_cast<const char *>(a.xs + src * a.lds);
+    } else {
+        xrow = tok + r * row_bytes(a.blocks);
+        xsrow = xrow + a.blocks * 128;
+    }
+    // (LDS rows hold whole blocks)
+    const int last_chunk = QK == kCodes ? a.K - 16 : a.blocks * kBlock - 16;
     const v4i *wsrc[S::FN];
     const float *wscale[S::FN];
 #pragma unroll
@@ -64,22 +149,34 @@ __global__ __launch_bounds__(S::THREADS) void block_mm_small_kernel(const BlockM
     }
 
     f32x4 acc[S::FN] = {};
-    for (int b0 = wk; b0 < a.blocks; b0 += S::WK * S::U) {
-        v4i w[S::U][S::FN][2], x[S::U][2];
-        float xs[S::U], sw[S::U][S::FN];
+    v4i w[S::U][S::FN][2];
+    float sw[S::U][S::FN];
+    // (blocks past the last read that one; their products are skipped)
+    auto weights = [&](int b0) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < S::U; ++u) {
             const int b = min(b0 + u * S::WK, a.blocks - 1);
 #pragma unroll
             for (int j = 0; j < S::FN; ++j) {
-                w[u][j][0] = wsrc[j][(int64_t)b * 128];
-                w[u][j][1] = wsrc[j][(int64_t)b * 128 + 64];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const v4i *p = wsrc[j] + (int64_t)b * 128 + h * 64;
+                    w[u][j][h] = S::NT ? __builtin_nontemporal_load(p) : *p;
+                }
                 sw[u][j] = wscale[j][b];
             }
+        }
+    };
+    auto products = [&](int b0) __attribute__((always_inline)) {
+        v4i x[S::U][2];
+        float xs[S::U];
+#pragma unroll
+        for (int u = 0; u < S::U; ++u) {
+            const int b = min(b0 + u * S::WK, a.blocks - 1);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                x[u][h] = *reinterpret_cast<const v4i *>(xrow + min(b * kBlock + (4 * h + sub) * 16, a.K - 16));
-            xs[u] = xsrow[b];
+                x[u][h] = *reinterpret_cast<const v4i *>(xrow + min(b * kBlock + (4 * h + sub) * 16, last_chunk));
+            xs[u] = *reinterpret_cast<const float *>(xsrow + b * 4);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -91,70 +188,247 @@ __global__ __launch_bounds__(S::THREADS) void block_mm_small_kernel(const BlockM
                 const f32x4 p = block_product(w[u][j], x[u]);
                 const float s = xs[u] * sw[u][j];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    acc[j][r] = __builtin_fmaf(p[r], s, acc[j][r]);
+                for (int k = 0; k < 4; ++k)
+                    acc[j][k] = __builtin_fmaf(p[k], s, acc[j][k]);
             }
         }
+    };
+    int b0 = wk;
+    if constexpr (QK != kCodes) {
+        // (of every wave, clamped into the weight: no wave skips the barrier)
+        weights(b0);
+        quantize_rows<S::THREADS, QK>(
+            a,
+            [&](int row) __attribute__((always_inline)) {
+                const int64_t src = JOB == kJobGateUp ? (tile.row0 + row) / a.top_k : tile.row0 + row;
+                return static_cast<const char *>(a.x) + src * a.ldx * quant_rule::Elem<QK>::BYTES;
+            },
+            tile.rows, JOB == kJobDense && tn == 0, tile.row0, tok);
+        __syncthreads();
+        products(b0);
+        b0 += S::WK * S::U;
+    }
+    for (; b0 < a.blocks; b0 += S::WK * S::U) {
+        weights(b0);
+        products(b0);
     }
 
-    if (wk > 0) {
+    // The partial sums along K meet in LDS: unit u of the fragments (a gate and
+    // its up fragment are one) is finished by wave u % WK of those that share
+    // the channels, which adds all their sums in the waves' order.
+    constexpr int STEP = JOB == kJobGateUp ? 2 : 1, UNITS = S::FN / STEP;
+    auto slot = [](int w, int unit) { return w - (w > unit % S::WK); };
 #pragma unroll
-        for (int j = 0; j < S::FN; ++j)
-            part[wk - 1][j][lane] = acc[j];
-    }
+    for (int q = 0; q < S::FN; ++q)
+        if (wk != q / STEP % S::WK)
+            part[wn][slot(wk, q / STEP)][q][lane] = acc[q];
     __syncthreads();
-    if (wk != 0)
-        return;
 #pragma unroll
-    for (int j = 0; j < S::FN; ++j)
+    for (int u = 0; u < UNITS; ++u) {
+        if (wk != u % S::WK)
+            continue;
+        f32x4 v[STEP];
 #pragma unroll
-        for (int w = 0; w < S::WK - 1; ++w)
-            acc[j] += part[w][j][lane];
-
-    // Register r of lane l is channel 4*(l/16) + r of the fragment, token l%16.
-    if (r16 >= tile.rows)
-        return;
-    if constexpr (JOB == kJobGateUp) {
+        for (int e = 0; e < STEP; ++e) {
+            const int q = u * STEP + e;
 #pragma unroll
-        for (int j = 0; j < S::FN; j += 2) {
-            const int col = 8 * (nb0 + j) + 4 * sub;
-            if (nb0 + j >= a.frags)                       // (the columns are a multiple of 16)
-                continue;
+            for (int o = 0; o < S::WK; ++o) {
+                const f32x4 one = o == u % S::WK ? acc[q] : part[wn][slot(o, u)][q][lane];
+                v[e] = o == 0 ? one : v[e] + one;
+            }
+        }
+        // Register k of lane l is channel 4*(l/16) + k of the fragment, token l%16.
+        const int nb = nb0 + u * STEP;
+        if (r16 >= tile.rows || nb >= a.frags)
+            continue;
+        if constexpr (JOB == kJobGateUp) {
             f32x4 h;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                h[r] = silu(acc[j][r]) * acc[j + 1][r];
-            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + (int64_t)row * a.ldo + col) = h;
+            for (int k = 0; k < 4; ++k)
+                h[k] = silu(v[0][k]) * v[1][k];
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + (int64_t)(tile.row0 + r16) * a.ldo + 8 * nb +
+                                       4 * sub) = h;
+        } else {
+            const int64_t orow = JOB == kJobDown ? a.order[tile.row0 + r16] : tile.row0 + r16;
+            if (16 * nb + 4 * sub < a.N)
+                store4<OUT>(a, orow, 16 * nb + 4 * sub, v[0]);
         }
-        return;
     }
-    const int64_t orow = JOB == kJobDown ? a.order[row] : row;
+}
+
+// The down products of a token's slots and their weighted sum in one launch,
+// for a few tokens: a workgroup takes 16 channels of a token's output, its
+// waves the (slot, part of K) pairs in turn, so that the sum over slots is the
+// one over waves. Its slots' inner rows (fp32) are quantized first, as above.
+constexpr int kDirectWaves = 8, kDirectAhead = 8;
+template <int E>
+__global__ __launch_bounds__(64 * kDirectWaves) void down_direct_kernel(const BlockMmArgs a)
+{
+    __shared__ f32x4 part[kDirectWaves - 1][64];
+    extern __shared__ __attribute__((aligned(16))) char tok[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int sub = lane >> 4;
+    const int t = xcd_remap(blockIdx.x, a.M * a.frags);
+    const int token = t % a.M, nb = t / a.M, slot0 = token * a.top_k;
+    // Pairs: each slot's blocks in `parts` runs.
+    const int parts = max(1, kDirectWaves / a.top_k), run = (a.blocks + parts - 1) / parts;
+    const int pairs = a.top_k * parts;
+
+    v4i w[kDirectAhead][2];
+    float sw[kDirectAhead], weight = 0.0f;
+    int first = 0, end = 0;
+    const v4i *wsrc = nullptr;
+    const float *wscale = nullptr;
+    // The pair's weights (none for a slot without an expert).
+    auto begin = [&](int pair) __attribute__((always_inline)) {
+        const int j = pair / parts, id = pair < pairs ? a.ids[slot0 + j] : -1;
+        first = pair % parts * run;
+        end = id >= 0 && id < a.experts ? min(first + run, a.blocks) : 0;
+        if (first >= end)
+            return;
+        weight = a.weights[slot0 + j];
+        wsrc = reinterpret_cast<const v4i *>(a.wp + id * a.expert_bytes) + (int64_t)nb * a.blocks * 128 + lane;
+        wscale = a.ws + id * a.expert_scales + (int64_t)(nb >> 3) * a.blocks;
+    };
+    auto weights = [&](int b0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < S::FN; ++j) {
-        const int n = 16 * (nb0 + j) + 4 * sub;
-        if (n >= a.N)
+        for (int u = 0; u < kDirectAhead; ++u) {
+            const int b = min(b0 + u, end - 1);
+            w[u][0] = __builtin_nontemporal_load(wsrc + (int64_t)b * 128);
+            w[u][1] = __builtin_nontemporal_load(wsrc + (int64_t)b * 128 + 64);
+            sw[u] = wscale[b];
+        }
+    };
+    begin(wave);
+    if (first < end)
+        weights(first);
+    quantize_rows<64 * kDirectWaves, kF32>(
+        a,
+        [&](int row) __attribute__((always_inline)) {
+            return static_cast<const char *>(a.x) + (int64_t)(slot0 + row) * a.ldx * 4;
+        },
+        a.top_k, false, 0, tok);
+    __syncthreads();
+    f32x4 total = {};
+    for (int pair = wave; pair < pairs; pair += kDirectWaves) {
+        if (pair != wave)
+            begin(pair);
+        if (first >= end)
             continue;
-        store4<OUT>(a, orow, n, acc[j]);
+        const char *row = tok + pair / parts * row_bytes(a.blocks);
+        f32x4 acc = {};
+        for (int b0 = first; b0 < end; b0 += kDirectAhead) {
+            if (pair != wave || b0 != first)
+                weights(b0);
+#pragma unroll
+            for (int u = 0; u < kDirectAhead; ++u) {
+                if (b0 + u >= end)
+                    break;
+                v4i x[2];
+                x[0] = *reinterpret_cast<const v4i *>(row + (b0 + u) * kBlock + sub * 16);
+                x[1] = *reinterpret_cast<const v4i *>(row + (b0 + u) * kBlock + 64 + sub * 16);
+                const f32x4 p = block_product(w[u], x);
+                const float s = *reinterpret_cast<const float *>(row + a.blocks * 128 + (b0 + u) * 4) * sw[u];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    acc[k] = __builtin_fmaf(p[k], s, acc[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            total[k] = __builtin_fmaf(weight, acc[k], total[k]);
     }
+    if (wave > 0)
+        part[wave - 1][lane] = total;
+    __syncthreads();
+    if (wave != 0 || (lane & 15) != 0)
+        return;                                            // (all 16 columns of the product are the one token)
+#pragma unroll
+    for (int v = 0; v < kDirectWaves - 1; ++v)
+        total += part[v][lane];
+    const int64_t at = (int64_t)token * a.ldo + 16 * nb + 4 * sub;
+    if constexpr (E == kF32)
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = total;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+            make_uint2(pack2<E == kF16>(total[0], total[1]), pack2<E == kF16>(total[2], total[3]));
 }
 
 template <class S>
 constexpr BlockTileEntry entry(const char *name)
 {
-    return BlockTileEntry{name, S::BM, S::BN, S::THREADS, true,
-                          {block_mm_small_kernel<S, kJobDense, kOutBF16>, block_mm_small_kernel<S, kJobDense, kOutI32>,
-                           block_mm_small_kernel<S, kJobDense, kOutF16>},
-                          block_mm_small_kernel<S, kJobGateUp, kOutI32>, block_mm_small_kernel<S, kJobDown, kOutI32>};
+    return BlockTileEntry{
+        name, S::BM, S::BN, S::THREADS, true,
+        {block_mm_small_kernel<S, kJobDense, kOutBF16, kCodes>, block_mm_small_kernel<S, kJobDense, kOutI32, kCodes>,
+         block_mm_small_kernel<S, kJobDense, kOutF16, kCodes>},
+        block_mm_small_kernel<S, kJobGateUp, kOutI32, kCodes>, block_mm_small_kernel<S, kJobDown, kOutI32, kCodes>};
 }
 
-// 16 token rows x 16*FN channels / WK waves along K / U blocks at a time.
+// 16 token rows x 16*FN*WN channels / WN x WK waves / U blocks at a time.
 const BlockTileEntry kSmall[] = {
-    entry<Small<2, 8, 4>>("s16x32/k8/u4"),
+    entry<Small<2, 1, 8, 4, false>>("s16x32/n1k8/u4"),
+    entry<Small<2, 1, 8, 2, true>>("s16x32/n1k8/u2nt"),
+    entry<Small<2, 4, 2, 4, true>>("s16x128/n4k2/u4nt"),
 };
+
+// The quant in the same launch: of a layer's rows, and of slots' tokens.
+template <class S, int E>
+constexpr BlockMmKernel quant_kernel(int mode)
+{
+    return mode == kOutBF16  ? block_mm_small_kernel<S, kJobDense, kOutBF16, E>
+           : mode == kOutI32 ? block_mm_small_kernel<S, kJobDense, kOutI32, E>
+                             : block_mm_small_kernel<S, kJobDense, kOutF16, E>;
+}
+template <class S>
+BlockMmKernel quant_pick(int kind, int mode)
+{
+    return kind == kElemF32 ? quant_kernel<S, kF32>(mode) : kind == kElemF16 ? quant_kernel<S, kF16>(mode)
+                                                                             : quant_kernel<S, kBF16>(mode);
+}
+using Plain = Small<2, 1, 8, 4, false>;
+using Stream = Small<2, 1, 8, 2, true>;
 
 }  // namespace
 
 int fp8_block_small_count() { return (int)(sizeof(kSmall) / sizeof(kSmall[0])); }
 const BlockTileEntry &fp8_block_small(int i) { return kSmall[i]; }
+
+hipError_t launch_fp8_block_small_quant(BlockMmArgs a, int x_kind, int mode, int i, hipStream_t stream)
+{
+    const BlockTileEntry &e = kSmall[i];
+    const int64_t rows = std::min<int64_t>(a.M, e.bm);
+    if (i > 1 || ceil_div(rows * a.blocks * 16, e.threads) > kSlots)
+        return hipErrorNotSupported;
+    a.tiles_m = (int)ceil_div(a.M, e.bm);
+    const int64_t tiles = a.tiles_m * ceil_div(a.frags, e.bn / 16);
+    hipLaunchKernelGGL(i == 0 ? quant_pick<Plain>(x_kind, mode) : quant_pick<Stream>(x_kind, mode),
+                       dim3((unsigned)tiles), dim3(e.threads), (size_t)(rows * row_bytes(a.blocks)), stream, a);
+    return hipGetLastError();
+}
+
+bool fp8_block_direct_fits(int top_k, int64_t K, int64_t inner)
+{
+    return ceil_div(K, kBlock) * 16 <= kSlots * Stream::THREADS &&
+           top_k * ceil_div(inner, kBlock) * 16 <= kSlots * 64 * kDirectWaves;
+}
+
+hipError_t launch_fp8_block_direct(BlockMmArgs up, BlockMmArgs down, int x_kind, int tokens, hipStream_t stream)
+{
+    auto fn = x_kind == kElemF32   ? block_mm_small_kernel<Stream, kJobGateUp, kOutI32, kF32>
+              : x_kind == kElemF16 ? block_mm_small_kernel<Stream, kJobGateUp, kOutI32, kF16>
+                                   : block_mm_small_kernel<Stream, kJobGateUp, kOutI32, kBF16>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)(up.M * ceil_div(up.frags, Stream::BF))), dim3(Stream::THREADS),
+                       (size_t)row_bytes(up.blocks), stream, up);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess)
+        return err;
+    down.M = tokens;
+    auto last = x_kind == kElemF32   ? down_direct_kernel<kF32>
+                : x_kind == kElemF16 ? down_direct_kernel<kF16> : down_direct_kernel<kBF16>;
+    hipLaunchKernelGGL(last, dim3((unsigned)(tokens * down.frags)), dim3(64 * kDirectWaves),
+                       (size_t)(down.top_k * row_bytes(down.blocks)), stream, down);
+    return hipGetLastError();
+}
 
 }  // namespace w8a8
