@@ -21,37 +21,46 @@ namespace {
 
 using namespace fp8_block;
 
-constexpr int kThreads = 256, kPlanAhead = 4;
+// Threads of a workgroup and ids that each holds at a time: more where there are
+// many slots to go through. The ids of a run of kThreads * AHEAD slots are loaded
+// at once and stay in registers for both looks at them: beside the quantization's
+// loads a load takes microseconds (32768 slots, 64 experts: 28 us with 1024 x 4,
+// @@ with 1024 x 32).
+constexpr int kFewSlots = 4096, kFewThreads = 256, kFewAhead = 4, kManyThreads = 1024, kManyAhead = 32;
 
 // The plan of expert e by one workgroup: where its rows begin (the slots of
 // lower experts come first), its slots in ascending order, and its row tiles of
 // bm rows. Every workgroup counts all experts by itself (LDS counters: their
 // sums do not depend on the order), so that none waits for another. The last
 // one writes the number of row tiles behind them.
+template <int kThreads, int AHEAD>
 __device__ __forceinline__ void plan_expert(int e, const int *__restrict__ ids, int slots, int experts, int bm,
                                             int *__restrict__ order, BlockTile *__restrict__ tiles, int tiles_m)
 {
+    constexpr int WAVES = kThreads / 64, RUN = kThreads * AHEAD;
     __shared__ int count[kMaxExperts];
     __shared__ int sums[2];
-    __shared__ int in_wave[kPlanAhead][kThreads / 64];
-    const int t = threadIdx.x, wave = t >> 6;
+    __shared__ int in_wave[WAVES];
+    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
     for (int i = t; i < experts; i += kThreads)
         count[i] = 0;
     if (t < 2)
         sums[t] = 0;
     __syncthreads();
-    int id[kPlanAhead];
+    // Of a run, wave w has the ids from w * 64 * AHEAD on, in rows of 64.
+    const int mine0 = wave * 64 * AHEAD + lane;
+    int id[AHEAD];
     auto load = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int q = 0; q < kPlanAhead; ++q) {
-            const int i = i0 + q * kThreads + t;
+        for (int q = 0; q < AHEAD; ++q) {
+            const int i = i0 + mine0 + q * 64;
             id[q] = i < slots ? ids[i] : -1;
         }
     };
-    for (int i0 = 0; i0 < slots; i0 += kPlanAhead * kThreads) {
+    for (int i0 = 0; i0 < slots; i0 += RUN) {
         load(i0);
 #pragma unroll
-        for (int q = 0; q < kPlanAhead; ++q)
+        for (int q = 0; q < AHEAD; ++q)
             if (id[q] >= 0 && id[q] < experts)
                 atomicAdd(&count[id[q]], 1);
     }
@@ -74,36 +83,38 @@ __device__ __forceinline__ void plan_expert(int e, const int *__restrict__ ids, 
     if (rows == 0)
         return;
     int at = first;
-    for (int i0 = 0; i0 < slots; i0 += kPlanAhead * kThreads) {
-        if (slots > kPlanAhead * kThreads)                // (a single run is still in registers)
+    for (int i0 = 0; i0 < slots; i0 += RUN) {
+        if (slots > RUN)                                  // (a single run is still in registers)
             load(i0);
-        unsigned long long mask[kPlanAhead];
+        int hits = 0;
 #pragma unroll
-        for (int q = 0; q < kPlanAhead; ++q) {
-            mask[q] = __ballot(id[q] == e);
-            if ((t & 63) == 0)
-                in_wave[q][wave] = __popcll(mask[q]);
-        }
+        for (int q = 0; q < AHEAD; ++q)
+            hits += __popcll(__ballot(id[q] == e));
+        if (lane == 0)
+            in_wave[wave] = hits;
         __syncthreads();
+        int all = 0, place = at;
 #pragma unroll
-        for (int q = 0; q < kPlanAhead; ++q) {
-            int lower = 0, all = 0;
-#pragma unroll
-            for (int w = 0; w < kThreads / 64; ++w) {
-                lower += w < wave ? in_wave[q][w] : 0;
-                all += in_wave[q][w];
-            }
-            if (id[q] == e)
-                order[at + lower + __popcll(mask[q] & ((1ull << (t & 63)) - 1))] = i0 + q * kThreads + t;
-            at += all;
+        for (int w = 0; w < WAVES; ++w) {
+            const int n = in_wave[w];
+            all += n;
+            place += w < wave ? n : 0;
         }
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) {
+            const unsigned long long mask = __ballot(id[q] == e);
+            if (id[q] == e)
+                order[place + __popcll(mask & ((1ull << lane) - 1))] = i0 + mine0 + q * 64;
+            place += __popcll(mask);
+        }
+        at += all;
         __syncthreads();
     }
 }
 
 // The plan, one workgroup per expert, and beside it the quantization of the
 // tokens' rows: neither waits for the other.
-template <int E, int U>
+template <int E, int U, int kThreads, int AHEAD>
 __global__ __launch_bounds__(kThreads) void prepare_kernel(const int *__restrict__ ids, int slots, int experts, int bm,
                                                            int *__restrict__ order, BlockTile *__restrict__ tiles,
                                                            int tiles_m, const char *__restrict__ x, int64_t rows,
@@ -112,16 +123,22 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(const int *__restrict
                                                            int rpb)
 {
     if ((int)blockIdx.x < experts)
-        plan_expert(blockIdx.x, ids, slots, experts, bm, order, tiles, tiles_m);
+        plan_expert<kThreads, AHEAD>(blockIdx.x, ids, slots, experts, bm, order, tiles, tiles_m);
     else
-        quant_block_rows<E, U>(blockIdx.x - experts, x, rows, units, padded, ldx, q, ldq, s, lds, segs, rpb);
+        quant_block_rows<E, U>((int64_t)(blockIdx.x - experts) * (kThreads / 256) + threadIdx.x / 256,
+                               threadIdx.x % 256, x, rows, units, padded, ldx, q, ldq, s, lds, segs, rpb);
 }
 
-template <int E>
+template <int E, int N, int A>
 auto prepare_pick(int u)
 {
-    return u == 1 ? prepare_kernel<E, 1> : u == 2 ? prepare_kernel<E, 2>
-         : u == 3 ? prepare_kernel<E, 3> : prepare_kernel<E, 4>;
+    return u == 1 ? prepare_kernel<E, 1, N, A> : u == 2 ? prepare_kernel<E, 2, N, A>
+         : u == 3 ? prepare_kernel<E, 3, N, A> : prepare_kernel<E, 4, N, A>;
+}
+template <int E>
+auto prepare_pick(int u, bool many)
+{
+    return many ? prepare_pick<E, kManyThreads, kManyAhead>(u) : prepare_pick<E, kFewThreads, kFewAhead>(u);
 }
 
 // out[t] = sum over the token's slots of weight * y[slot], y fp32 rows or fp16
@@ -228,6 +245,12 @@ Path path_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
 // Row tiles of a launch, at most.
 int64_t most_tiles(int64_t slots, int experts, int bm) { return slots / bm + std::min<int64_t>(experts, slots); }
 
+int64_t grid_of(const BlockTileEntry &e, int64_t tiles_m, int64_t frags)
+{
+    const int64_t tiles_n = ceil_div(frags, e.bn / 16);
+    return e.small ? tiles_m * tiles_n : expert_grid(tiles_m, tiles_n);
+}
+
 Layout layout_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner, const Path &p)
 {
     Layout l;
@@ -269,8 +292,8 @@ bool experts_fit(int64_t tokens, int top_k, int experts, int64_t K, int64_t inne
     const int64_t step = tokens_at_once(tokens, top_k, K);
     const Path p = path_of(step, top_k, experts, K, inner);
     const int64_t tiles_m = most_tiles(step * top_k, experts, p.up->bm);
-    return mm_grid_fits(tiles_m * ceil_div(2 * inner, p.up->bn), p.up->threads) &&
-           mm_grid_fits(tiles_m * ceil_div(K, p.down->bn), p.down->threads);
+    return mm_grid_fits(grid_of(*p.up, tiles_m, fp8_block_frags(2 * inner, true)), p.up->threads) &&
+           mm_grid_fits(grid_of(*p.down, tiles_m, fp8_block_frags(K, false)), p.down->threads);
 }
 
 hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t stream)
@@ -340,10 +363,12 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         const int bm = p.up->bm, tiles_m = (int)most_tiles(slots, args.experts, bm);
         const int units = (int)(args.K / 8), padded = blocks * 16;
         const Cut c = cut_of(tokens, padded);
-        auto prepare = args.kind == kElemF32 ? prepare_pick<kF32>(c.u)
-                     : args.kind == kElemF16 ? prepare_pick<kF16>(c.u) : prepare_pick<kBF16>(c.u);
-        hipLaunchKernelGGL(prepare, dim3((unsigned)(args.experts + c.blocks)), dim3(kThreads), 0, stream, ids, slots,
-                           args.experts, bm, order, tiles, tiles_m, x, tokens, units, padded, args.ldx, xq, args.K, xs,
+        const bool many = slots > kFewSlots;
+        const int threads = many ? kManyThreads : kFewThreads;
+        auto prepare = args.kind == kElemF32 ? prepare_pick<kF32>(c.u, many)
+                     : args.kind == kElemF16 ? prepare_pick<kF16>(c.u, many) : prepare_pick<kBF16>(c.u, many);
+        hipLaunchKernelGGL(prepare, dim3((unsigned)(args.experts + ceil_div(c.blocks, threads / 256))), dim3(threads), 0,
+                           stream, ids, slots, args.experts, bm, order, tiles, tiles_m, x, tokens, units, padded, args.ldx, xq, args.K, xs,
                            scale_pitch(args.K), c.segs, c.rpb);
 
         up.tiles = down.tiles = tiles;
@@ -356,8 +381,8 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         up.out = p.small() ? static_cast<void *>(work + l.h) : hq;
         up.out_scale = hs;
         up.ld_out_scale = scale_pitch(args.inner);
-        hipLaunchKernelGGL(p.up->gate_up, dim3((unsigned)(tiles_m * ceil_div(up.frags, p.up->bn / 16))),
-                           dim3(p.up->threads), 0, stream, up);
+        hipLaunchKernelGGL(p.up->gate_up, dim3((unsigned)grid_of(*p.up, tiles_m, up.frags)), dim3(p.up->threads), 0,
+                           stream, up);
         if (p.small()) {
             err = launch_quant_fp8_block(work + l.h, kElemF32, slots, args.inner, args.inner, hq, args.inner, hs,
                                          scale_pitch(args.inner), stream);
@@ -372,8 +397,8 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         down.ldo = args.K;
         down.out_scale = ys;
         down.ld_out_scale = blocks;
-        hipLaunchKernelGGL(p.down->down, dim3((unsigned)(tiles_m * ceil_div(down.frags, p.down->bn / 16))),
-                           dim3(p.down->threads), 0, stream, down);
+        hipLaunchKernelGGL(p.down->down, dim3((unsigned)grid_of(*p.down, tiles_m, down.frags)), dim3(p.down->threads),
+                           0, stream, down);
 
         const int segs = (int)ceil_div(args.K, 2048);
         auto combine = args.kind == kElemF32 ? combine_pick<kF32>(!p.small())

@@ -20,6 +20,8 @@ struct RouteArgs {
     float scale;
     int *ids;                    // [tokens, top_k]
     float *weights;
+    int group_lanes;             // (set by launch_route)
+    unsigned size_inverse;
 };
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
 

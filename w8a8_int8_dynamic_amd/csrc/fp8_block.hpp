@@ -70,6 +70,18 @@ struct BlockMmArgs {
     int64_t expert_bytes, expert_scales;   // from one expert's weight and scales to the next's
 };
 
+// Tiles of an experts' launch that go to one XCD together: 4 row tiles by about 8
+// column tiles (`across` even groups of columns); and the workgroups that the
+// main kernel's launch over tiles_m x tiles_n tiles takes.
+constexpr int kExpertGroupM = 4, kExpertGroupN = 8, kExpertDeal = 768;
+inline int64_t expert_grid(int64_t tiles_m, int64_t tiles_n)
+{
+    const int64_t across = ceil_div(tiles_n, kExpertGroupN);
+    if (tiles_m * tiles_n < kExpertDeal)
+        return tiles_m * tiles_n;
+    return round_up(ceil_div(tiles_m, kExpertGroupM) * across, kXcds) * kExpertGroupM * ceil_div(tiles_n, across);
+}
+
 typedef void (*BlockMmKernel)(const BlockMmArgs);
 struct BlockTileEntry {
     const char *name;

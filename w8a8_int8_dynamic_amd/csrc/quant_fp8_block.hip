@@ -23,7 +23,7 @@ __global__ __launch_bounds__(256) void quant_fp8_block_kernel(const char *__rest
                                                               int64_t ldq, float *__restrict__ s, int64_t lds,
                                                               int segs, int rpb)
 {
-    quant_block_rows<E, U>(blockIdx.x, x, rows, units, padded, ldx, q, ldq, s, lds, segs, rpb);
+    quant_block_rows<E, U>(blockIdx.x, threadIdx.x, x, rows, units, padded, ldx, q, ldq, s, lds, segs, rpb);
 }
 
 // 8 codes a thread back to their values, rounded to the output's type.
@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256) void dequant_fp8_block_kernel(const uint8_t *_
                                                                 int64_t rows, int units, int padded,
                                                                 char *__restrict__ out, int64_t ldo, int segs, int rpb)
 {
-    const Place p = place_of(blockIdx.x, rows, padded, segs, rpb, 256 * U);
+    const Place p = place_of(blockIdx.x, threadIdx.x, rows, padded, segs, rpb, 256 * U);
     constexpr int BYTES = quant_rule::Elem<E>::BYTES;
     if (!p.valid)
         return;

@@ -15,29 +15,29 @@ struct Place {
     int unit0;
     bool valid;
 };
-__device__ __forceinline__ Place place_of(int64_t b, int64_t rows, int padded, int segs, int rpb, int per_block)
+__device__ __forceinline__ Place place_of(int64_t b, int t, int64_t rows, int padded, int segs, int rpb, int per_block)
 {
     Place p;
     if (rpb == 1) {
         p.row = b / segs;
-        p.unit0 = (int)(b - p.row * segs) * per_block + (int)threadIdx.x;
+        p.unit0 = (int)(b - p.row * segs) * per_block + t;
         p.valid = p.row < rows;
     } else {
-        const int r = (int)threadIdx.x / padded;
+        const int r = t / padded;
         p.row = b * rpb + r;
-        p.unit0 = (int)threadIdx.x - r * padded;
+        p.unit0 = t - r * padded;
         p.valid = r < rpb && p.row < rows;
     }
     return p;
 }
 
-// Workgroup b of 256 threads, U units (8 elements) each.
+// Thread t of workgroup b of 256 threads, U units (8 elements) each.
 template <int E, int U>
-__device__ __forceinline__ void quant_block_rows(int64_t b, const char *__restrict__ x, int64_t rows, int units,
+__device__ __forceinline__ void quant_block_rows(int64_t b, int t, const char *__restrict__ x, int64_t rows, int units,
                                                  int padded, int64_t ldx, uint8_t *__restrict__ q, int64_t ldq,
                                                  float *__restrict__ s, int64_t lds, int segs, int rpb)
 {
-    const Place p = place_of(b, rows, padded, segs, rpb, 256 * U);
+    const Place p = place_of(b, t, rows, padded, segs, rpb, 256 * U);
     constexpr int BYTES = quant_rule::Elem<E>::BYTES;
     uint4 lo[U], hi[U];
 #pragma unroll
@@ -50,8 +50,8 @@ __device__ __forceinline__ void quant_block_rows(int64_t b, const char *__restri
                 lo[i] = src[0];
                 hi[i] = src[1];
             } else {
-                const quant_rule::v4u t = __builtin_nontemporal_load(reinterpret_cast<const quant_rule::v4u *>(src));
-                lo[i] = make_uint4(t[0], t[1], t[2], t[3]);
+                const quant_rule::v4u v = __builtin_nontemporal_load(reinterpret_cast<const quant_rule::v4u *>(src));
+                lo[i] = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
     }

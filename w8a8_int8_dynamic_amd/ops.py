@@ -787,11 +787,13 @@ def fp8_block_dequant(xq: torch.Tensor, xs: torch.Tensor, dtype: torch.dtype = t
     if dtype not in _DTYPE:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
     M, K = _block_rows(xq, xs)
-    if xq.data_ptr() % 8 != 0 or _ld(xq) % 8 != 0:
+    at, ld = xq.data_ptr(), xq.stride(0) if M > 1 else K
+    if at % 8 != 0 or ld % 8 != 0:
         xq = _rows_aligned(xq, 16)
+        at, ld = xq.data_ptr(), _ld(xq)
     out = xq.new_empty((M, K), dtype=dtype)
-    _run(xq, "fp8_block_dequant", xq.data_ptr(), _ld(xq), xs.data_ptr(), _ld(xs), M, K, _DTYPE[dtype],
-         out.data_ptr(), K)
+    _run(xq, "fp8_block_dequant", at, ld, xs.data_ptr(), xs.stride(0) if M > 1 else xs.shape[1], M, K,
+         _DTYPE[dtype], out.data_ptr(), K)
     return out
 
 
