@@ -176,6 +176,22 @@ def test_experts(ops, dtype, t, e, top_k, k, inner):
     assert torch.equal(layer(x.to(DEV), ids.to(DEV), w.to(DEV)), y)
 
 
+@pytest.mark.parametrize("t,e,top_k,k,inner", [(1200, 36, 6, 784, 784), (1000, 32, 3, 784, 912), (1500, 64, 2, 1040, 784)])
+def test_experts_many_tiles(ops, t, e, top_k, k, inner):
+    """About 200, 94 and 47 rows an expert, of uneven shares, in more tiles than the card holds at once."""
+    parts, gv, dv = make(e, inner, k, t)
+    layer = layer_of(parts)
+    x = (rows(t, k, t + 1, torch.float32) * 0.3).to(torch.bfloat16)
+    ids, w = choose(t, e, top_k, 5, skew=0.5)
+    xv = ref.dequant(*ref.quant(x.float().numpy()))
+    exact, bound = ref.experts(xv, ids.numpy(), w.numpy(), gv, dv)
+    y = layer(x.to(DEV), ids.to(DEV), w.to(DEV))
+    check(y, exact, bound, torch.bfloat16, what=f"{t} {e}")
+    off = np.linalg.norm(y.double().cpu().numpy() - exact) / np.linalg.norm(exact)
+    assert off < 2.0 ** -6.5 + HALF[torch.bfloat16], off          # (as in test_experts)
+    assert torch.equal(layer(x.to(DEV), ids.to(DEV), w.to(DEV)), y)
+
+
 @pytest.mark.parametrize("t", [6, 200])
 def test_experts_any_ids(ops, t):
     """No expert (-1, or past the last), all slots one expert, the same expert twice, an order

@@ -209,6 +209,23 @@ def test_product_strides(ops, m, n, k):
                 assert (out[:, :at] == 7).all() and (out[:, at + n:] == 7).all()
 
 
+@pytest.mark.parametrize("k", [400, 656, 1040, 1168])
+def test_product_many_tiles(ops, k):
+    """More tiles than the card holds at once: rows have the values of smaller launches."""
+    m, n, step = 4400, 4250, 320
+    x, s = (dev(a) for a in codes(m, k, 7))
+    wq, ws = weights(n, k, 8)
+    packed, w = ops.fp8_block_prepack_weight(dev(wq)), dev(ws)
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(9)).to(torch.float16).to(DEV)
+    for tile in range(ops.fp8_block_tile_count()):
+        print(ops.fp8_block_tile_name(tile), flush=True)
+        for b, dtype in ((None, torch.float32), (None, torch.bfloat16), (bias, torch.float16)):
+            got = ops.fp8_block_scaled_mm(x, s, packed, w, n, b, dtype, tile=tile)
+            for at in range(0, m, step):
+                want = ops.fp8_block_scaled_mm(x[at:at + step], s[at:at + step], packed, w, n, b, dtype, tile=tile)
+                assert torch.equal(got[at:at + step], want), (tile, at)
+
+
 def test_product_keeps_to_its_rows(ops):
     """A row of NaN scales or NaN codes, or zero rows, changes no other row; zero
     weight blocks give zeros."""
