@@ -142,8 +142,10 @@ def test_experts_checks():
                 dict(dn=A + 8), dict(work=A + 128), dict(ids=A + 2), dict(w=A + 2), dict(gs=A + 2), dict(ds=A + 2)):
         assert experts(**bad) == ALIGN, bad
     most = _lib.W8A8_MAX_K
-    assert experts(K=most, inner=most, ldx=most, ldo=most, E=1024, T=8192, k=1) == SHAPE    # no launch holds it
-    assert L.fp8_block_experts_workspace_bytes(8192, most, most, 1024, 1) == 0
+    # The largest layer's launches all fit: a pass of up to 65536 slots and 2^30 codes, its rows twice.
+    for t, k in ((8192, 1), (2 ** 31 - 1, 64)):
+        size = L.fp8_block_experts_workspace_bytes(t, most, most, 1024, k)
+        assert 0 < size < 65536 * most * 8, (t, k)
     need = L.fp8_block_experts_workspace_bytes(4, 144, 80, 4, 2)
     assert need > 0 and experts(size=need - 1) == SHAPE
     assert L.fp8_block_experts_workspace_bytes(4, 136, 80, 4, 2) == 0

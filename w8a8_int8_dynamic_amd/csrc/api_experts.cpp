@@ -72,10 +72,8 @@ W8A8_API w8a8_status_t route_experts(const void *logits, int dtype, int64_t ld, 
 
 W8A8_API size_t fp8_block_experts_workspace_bytes(int64_t tokens, int64_t K, int64_t inner, int experts, int top_k)
 {
-    if (!experts_shape(tokens, K, inner, experts, top_k) ||
-        !w8a8::experts_fit(tokens, top_k, experts, K, inner))
-        return 0;
-    return w8a8::experts_workspace_bytes(tokens, top_k, experts, K, inner);
+    return experts_shape(tokens, K, inner, experts, top_k)
+               ? w8a8::experts_workspace_bytes(tokens, top_k, experts, K, inner) : 0;
 }
 
 W8A8_API w8a8_status_t fp8_block_experts(const w8a8_experts_t *layer, const void *x, int x_dtype, int64_t ldx,
@@ -93,8 +91,6 @@ W8A8_API w8a8_status_t fp8_block_experts(const w8a8_experts_t *layer, const void
         return fail(W8A8_ERR_SHAPE, "%s: tokens, K, inner, experts or top_k out of range", what);
     if (ldx < l.K || ldo < l.K)
         return fail(W8A8_ERR_SHAPE, "%s: leading dimension too small", what);
-    if (!w8a8::experts_fit(tokens, top_k, l.experts, l.K, l.inner))
-        return fail(W8A8_ERR_SHAPE, "%s: the shape needs more workgroups than one launch holds", what);
     if (tokens == 0)
         return ok();
     if (!x || !ids || !weights || !out || !workspace || !l.gate_up || !l.gate_up_scale || !l.down || !l.down_scale)

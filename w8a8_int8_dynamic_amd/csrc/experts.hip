@@ -25,7 +25,7 @@ using namespace fp8_block;
 // many slots to go through. The ids of a run of kThreads * AHEAD slots are loaded
 // at once and stay in registers for both looks at them: beside the quantization's
 // loads a load takes microseconds (32768 slots, 64 experts: 28 us with 1024 x 4,
-// @@ with 1024 x 32).
+// 17 with 1024 x 32).
 constexpr int kFewSlots = 4096, kFewThreads = 256, kFewAhead = 4, kManyThreads = 1024, kManyAhead = 32;
 
 // The plan of expert e by one workgroup: where its rows begin (the slots of
@@ -199,11 +199,6 @@ auto combine_pick(bool y16)
     return y16 ? combine_kernel<E, true> : combine_kernel<E, false>;
 }
 
-// Slots that are run without a plan, each with its expert's weights to itself:
-// the plan's launch costs about as much as reading a weight twice for one slot in
-// sixteen.
-constexpr int kDirectSlots = 16;
-
 // Tokens of one pass: what bounds the workspace and keeps every row offset of
 // the codes within 31 bits.
 int64_t tokens_at_once(int64_t tokens, int top_k, int64_t K)
@@ -227,24 +222,46 @@ struct Path {
     bool small() const { return up->small; }
 };
 
+// The choice, by what each side took (us, the whole layer; A: 64 experts, K 4096,
+// inner 1024, 4 a token; B: 24, 2064, 720, 3; C: 8, 4096, 2048):
+//   small-M tiles up to 10 rows an expert, on average, then the main kernel's:
+//     A at 8 rows 155 against 183, at 16 rows 218 against 175; B 41 : 45, 49 : 45.
+//     Of those 16 x 128, but 16 x 32 where K is long and column tiles are few: A at
+//     4 slots 8 tokens 70 against 74, at 64 slots 104 : 101, B 41 : 47;
+//   its 128 x 256 tile up to 104 rows, then 256 x 256:
+//     A at 64 rows 192 : 200, at 96 210 : 221, at 112 243 : 228, at 256 404 : 376;
+//     B at 96 59 : 64, at 128 72 : 67 (64 x 256 tiles gained 2 % at most, below 32);
+//   slots alone, without a plan, each with its expert's weights to itself, for up
+//   to four tokens and 24 slots, no more than there are experts (more would read
+//   weights twice): A, one token of 8 25.6 : 39.0, three of 8 56 : 63, eight of 1
+//   42.8 : 35.4; C, two of 8 58 : 48.
+constexpr int kSmallRows = 10, kHalfRows = 104, kDirectTokens = 4, kDirectSlots = 24;
+
 Path path_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
 {
     const int64_t slots = tokens * top_k, rows = slots / experts;   // rows of an expert, on average
     Path p{};
-    if (rows > 32) {
-        p.up = p.down = &fp8_block_main(rows > 128 ? 0 : rows > 64 ? 1 : 2);
+    if (rows > kSmallRows) {
+        p.up = p.down = &fp8_block_main(rows > kHalfRows ? 0 : 1);
         return p;
     }
-    p.direct = slots <= kDirectSlots && fp8_block_direct_fits(top_k, K, inner);
-    auto small = [](int64_t k) { return &fp8_block_small(k > 1024 ? 1 : 2); };
-    p.up = small(K);
-    p.down = small(inner);
+    p.direct = tokens <= kDirectTokens && slots <= std::min(kDirectSlots, experts) &&
+               fp8_block_direct_fits(top_k, K, inner);
+    // (of K, frags / 8 column tiles of an expert)
+    auto small = [&](int64_t k, int64_t frags) {
+        return &fp8_block_small(k > 1024 && std::min<int64_t>(slots, experts) * ceil_div(frags, 8) <= 512 ? 1 : 2);
+    };
+    p.up = small(K, fp8_block_frags(2 * inner, true));
+    p.down = small(inner, fp8_block_frags(K, false));
     return p;
 }
 
 // Row tiles of a launch, at most.
 int64_t most_tiles(int64_t slots, int experts, int bm) { return slots / bm + std::min<int64_t>(experts, slots); }
 
+// Workgroups of a product's launch: 3.5 million of 512 threads at most (a pass has
+// up to 65536 slots; 10 rows an expert on 16 x 128 tiles of 131056 rows of weights),
+// so that threads are counted in 32 bits.
 int64_t grid_of(const BlockTileEntry &e, int64_t tiles_m, int64_t frags)
 {
     const int64_t tiles_n = ceil_div(frags, e.bn / 16);
@@ -285,15 +302,6 @@ size_t experts_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t K
 {
     const int64_t step = tokens_at_once(tokens, top_k, K);
     return layout_of(step, top_k, experts, K, inner, path_of(step, top_k, experts, K, inner)).end;
-}
-
-bool experts_fit(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
-{
-    const int64_t step = tokens_at_once(tokens, top_k, K);
-    const Path p = path_of(step, top_k, experts, K, inner);
-    const int64_t tiles_m = most_tiles(step * top_k, experts, p.up->bm);
-    return mm_grid_fits(grid_of(*p.up, tiles_m, fp8_block_frags(2 * inner, true)), p.up->threads) &&
-           mm_grid_fits(grid_of(*p.down, tiles_m, fp8_block_frags(K, false)), p.down->threads);
 }
 
 hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t stream)

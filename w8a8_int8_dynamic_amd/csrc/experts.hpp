@@ -41,8 +41,6 @@ struct ExpertsArgs {
 };
 // Bytes of workspace for `tokens` tokens (0: out of range).
 size_t experts_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner);
-// Whether every launch of the call fits (mm_grid_fits).
-bool experts_fit(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner);
 hipError_t launch_experts(const ExpertsArgs &a, void *workspace, hipStream_t stream);
 
 }  // namespace w8a8

@@ -89,9 +89,8 @@ struct BlockTileEntry {
     bool small;
     BlockMmKernel dense[kOutKinds], gate_up, down;
 };
-int fp8_block_main_count();
+constexpr int kBlockMainTiles = 6, kBlockSmallTiles = 3;
 const BlockTileEntry &fp8_block_main(int i);
-int fp8_block_small_count();
 const BlockTileEntry &fp8_block_small(int i);
 // The quant of a.x (element kind x_kind) and small-M tile i in one launch;
 // hipErrorNotSupported (nothing launched) where a workgroup's rows are too many

@@ -4,7 +4,8 @@
 namespace w8a8 {
 namespace {
 
-// (a tile whose inner columns are one block)
+// The experts' kernels, for the tiles that they run on (whose inner columns are one
+// block).
 template <class T>
 constexpr BlockMmKernel gate_up()
 {
@@ -14,11 +15,10 @@ constexpr BlockMmKernel gate_up()
         return nullptr;
 }
 
-// (waves whose channels share a block)
 template <class T>
 constexpr BlockMmKernel down()
 {
-    if constexpr (8 % T::TN == 0)
+    if constexpr (T::BN == 256)
         return block_mm_kernel<T, kJobDown, kOutF16>;
     else
         return nullptr;
@@ -37,16 +37,15 @@ constexpr BlockTileEntry entry(const char *name)
 const BlockTileEntry kMain[] = {
     entry<BlockMain<256, 256, 2, 4, 2>>("256x256/m2n4/l2"),
     entry<BlockMain<128, 256, 2, 4, 3>>("128x256/m2n4/l3"),
-    entry<BlockMain<64, 256, 1, 4, 3>>("64x256/m1n4/l3"),
     entry<BlockMain<128, 192, 2, 4, 3>>("128x192/m2n4/l3"),
     entry<BlockMain<128, 128, 2, 4, 4>>("128x128/m2n4/l4"),
     entry<BlockMain<64, 128, 1, 4, 3>>("64x128/m1n4/l3"),
     entry<BlockMain<64, 64, 2, 2, 4>>("64x64/m2n2/l4"),
 };
+static_assert(sizeof(kMain) / sizeof(kMain[0]) == kBlockMainTiles, "tiles");
 
 }  // namespace
 
-int fp8_block_main_count() { return (int)(sizeof(kMain) / sizeof(kMain[0])); }
 const BlockTileEntry &fp8_block_main(int i) { return kMain[i]; }
 
 }  // namespace w8a8

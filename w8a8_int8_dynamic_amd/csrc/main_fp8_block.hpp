@@ -29,7 +29,7 @@
 //     way through the step); part B, the other rows, at the step's end. Each
 //     then has NS - 1/2 steps to land, where refilling whole stages leaves NS -
 //     1 (M8192 N4096 K12288, two stages of 64 KB, a step of 2048 matrix core
-//     cycles: 367 us so, @@ now).
+//     cycles: 367 us so, 354 now).
 //   - Token scales go through LDS too, 16 bytes (four blocks) a row at a time;
 //     the weight's are one or two numbers per wave and block, held by the lanes
 //     of a register for 64 blocks and read from there.
@@ -66,6 +66,7 @@ struct BlockMain {
     static constexpr int PITCH_Q = BN / 2 + 16;                  // staged row of codes (gated)
     static constexpr int TOPS = BM * PITCH_Q;                    // then WN block maxima per row
     static constexpr int LDS = cmax(cmax(RING, BM * PITCH), TOPS + WN * BM * 4);
+    static constexpr int WAVES = (2 * LDS <= 160 * 1024 ? 2 : 1) * NW / 4;   // on a SIMD
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0 &&
                       NS * LPW < 64, "tile");
     static_assert(TM % 2 == 0 && LX % 2 == 0 && BM % 64 == 0 && NW >= SX_UNITS && NW % 2 == 0 && NS <= 4,
@@ -102,7 +103,7 @@ __device__ __forceinline__ void expert_tile_of(int pid, int tiles_n, int &tm, in
 }
 
 template <class T, int JOB, int OUT>
-__global__ __launch_bounds__(T::THREADS, 2) void block_mm_kernel(const BlockMmArgs args)
+__global__ __launch_bounds__(T::THREADS, T::WAVES) void block_mm_kernel(const BlockMmArgs args)
 {
     __shared__ uint4 lds[T::LDS / 16];
     char *const shared = reinterpret_cast<char *>(lds);
@@ -438,12 +439,21 @@ __global__ __launch_bounds__(T::THREADS, 2) void block_mm_kernel(const BlockMmAr
         }
     } else {
         // 16-bit rows, staged in LDS and written whole, 16 bytes a lane (M4096
-        // N4096: 9 us of 8-byte stores from registers, @@ so). Down: fp16 under a
+        // N4096: 9 us of 8-byte stores from registers, 3.4 so). Down: fp16 under a
         // power of two per row and block of channels, so that a slot's row
         // costs half of fp32's bytes and a quarter of the 2^-9 that bf16 would
         // lose: |acc| <= 448 * 448 * 128 * the sum of its scales, brought below
         // 2^15; values 2^-29 of that bound and less leave fp16's normal range.
         constexpr bool F16 = OUT == kOutF16;
+        // Down: the slots of the wave's rows, then of the thread's pieces, are read
+        // ahead of the stores, which the compiler would else keep them behind (M
+        // 32768 rows of 64 experts, K 1024, N 4096: 234 us behind them, 214 now).
+        int slot_of[JOB == kJobDown ? TM : 1];
+        if constexpr (JOB == kJobDown) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                slot_of[i] = a.order[row0 + min(16 * (i * T::WM + wm) + r16, rows - 1)];
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int m = 16 * (i * T::WM + wm) + r16;
@@ -454,7 +464,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void block_mm_kernel(const BlockMmAr
                 const bool odd = !(top > 0x1p-100f && top < 0x1p126f);   // zero, not finite, or out of reach
                 down = odd ? 1.0f : __uint_as_float((u32)(127 - e) << 23);
                 if (sub == 0 && (wn * TN) % 8 == 0 && m < rows && wf < a.frags)
-                    a.out_scale[(int64_t)a.order[row0 + m] * a.ld_out_scale + (wf >> 3)] =
+                    a.out_scale[(int64_t)slot_of[i] * a.ld_out_scale + (wf >> 3)] =
                         odd ? 1.0f : __uint_as_float((u32)(127 + e) << 23);
             }
 #pragma unroll
@@ -475,15 +485,26 @@ __global__ __launch_bounds__(T::THREADS, 2) void block_mm_kernel(const BlockMmAr
                     make_uint2(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]));
             }
         }
-        __syncthreads();
         constexpr int P16 = T::BN / 8, RPP = T::THREADS / P16;   // pieces per row, rows per pass
-        const int c = threadIdx.x % P16, n = f0 * 16 + c * 8;
+        const int c = threadIdx.x % P16, first = threadIdx.x / P16, n = f0 * 16 + c * 8;
+        constexpr int PASSES = (T::BM + RPP - 1) / RPP;
+        int row_of[JOB == kJobDown ? PASSES : 1];
+        if constexpr (JOB == kJobDown) {
+#pragma unroll
+            for (int q = 0; q < PASSES; ++q)
+                row_of[q] = a.order[row0 + min(first + q * RPP, rows - 1)];
+        }
+        __syncthreads();
         uint16_t *out = static_cast<uint16_t *>(a.out) + n;
         if (n >= a.N)
             return;
         const bool whole = a.vec16 && n + 8 <= a.N;
-        for (int m = threadIdx.x / P16; m < rows; m += RPP) {
-            const int64_t orow = JOB == kJobDown ? a.order[row0 + m] : row0 + m;
+#pragma unroll
+        for (int q = 0; q < PASSES; ++q) {
+            const int m = first + q * RPP;
+            if (m >= rows)
+                break;
+            const int64_t orow = JOB == kJobDown ? row_of[q] : row0 + m;
             uint16_t *o = out + orow * a.ldo;
             const v4u v = *reinterpret_cast<const v4u *>(shared + m * T::PITCH + c * 16);
             if (whole) {

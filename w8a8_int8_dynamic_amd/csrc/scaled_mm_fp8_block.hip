@@ -16,7 +16,7 @@ namespace {
 // The rates (us) are fitted to the times of every tile on 473 shapes (M 1-8192, N
 // 512-12288, K 512-12288, weights from HBM) on MI355X, by
 // tests/probes/fp8_block_tile_grid.py; over them the chosen tile takes 1.1 % more
-// than the best on average, 28 % at most. Tiles without a cost are the experts'.
+// than the best on average, 28 % at most. A tile without a cost is the experts'.
 struct MainCost {
     int per_round;
     double fixed, block, round, weight, out;
@@ -24,7 +24,6 @@ struct MainCost {
 constexpr MainCost kMainCost[] = {
     {256, 1.412, 1.288, 4.905, 0.0, 0.163},        // 256x256
     {256, 2.98, 0.7625, 1.89, 0.0, 0.2407},        // 128x256
-    {0, 0, 0, 0, 0, 0},                            // 64x256
     {256, 3.84, 0.6822, 0.6553, 0.0, 0.2705},      // 128x192
     {256, 3.414, 0.5686, 0.8036, 0.0, 0.3086},     // 128x128
     {512, 3.421, 0.4418, 0.0, 0.008309, 0.4907},   // 64x128
@@ -39,6 +38,8 @@ constexpr SmallCost kSmallCost[] = {
     {16, 2.462, 5.044e-4, 1.407, 0.00877},         // s16x32/n1k8/u2nt
     {0, 0, 0, 0, 0},                               // s16x128/n4k2/u4nt
 };
+static_assert(sizeof(kMainCost) / sizeof(MainCost) == kBlockMainTiles &&
+                  sizeof(kSmallCost) / sizeof(SmallCost) == kBlockSmallTiles, "a cost per tile");
 constexpr int64_t kSmallRows = 256;
 
 double cost_of(int tile, int64_t M, int64_t N, int64_t K)
@@ -47,25 +48,22 @@ double cost_of(int tile, int64_t M, int64_t N, int64_t K)
     const double tiles = (double)(ceil_div(M, e.bm) * ceil_div(N, e.bn)), blocks = (double)ceil_div(K, 128);
     const double weight = (double)N * (double)K * 1e-6;
     if (e.small) {
-        const SmallCost &c = kSmallCost[tile - fp8_block_main_count()];
+        const SmallCost &c = kSmallCost[tile - kBlockMainTiles];
         if (M > kSmallRows || c.ahead == 0)
             return INFINITY;
         return c.fixed + c.work * tiles * blocks + c.chain * std::ceil(blocks / c.ahead) + c.weight * weight;
     }
     const MainCost &c = kMainCost[tile];
-    if (c.per_round == 0)
-        return INFINITY;
     return c.fixed + std::ceil(tiles / c.per_round) * (c.block * blocks + c.round) + c.weight * weight +
            c.out * (double)M * (double)N * 2e-6;
 }
 
 }  // namespace
 
-int fp8_block_tile_count() { return fp8_block_main_count() + fp8_block_small_count(); }
+int fp8_block_tile_count() { return kBlockMainTiles + kBlockSmallTiles; }
 const BlockTileEntry &fp8_block_tile(int tile)
 {
-    const int n = fp8_block_main_count();
-    return tile < n ? fp8_block_main(tile) : fp8_block_small(tile - n);
+    return tile < kBlockMainTiles ? fp8_block_main(tile) : fp8_block_small(tile - kBlockMainTiles);
 }
 
 int fp8_block_tile_auto(int64_t M, int64_t N, int64_t K)
@@ -84,8 +82,8 @@ int fp8_block_tile_auto(int64_t M, int64_t N, int64_t K)
 
 hipError_t launch_fp8_block_quant_mm(const BlockMmArgs &a, int x_kind, int mode, int tile, hipStream_t stream)
 {
-    const int n = fp8_block_main_count();
-    return tile < n ? hipErrorNotSupported : launch_fp8_block_small_quant(a, x_kind, mode, tile - n, stream);
+    return tile < kBlockMainTiles ? hipErrorNotSupported
+                                  : launch_fp8_block_small_quant(a, x_kind, mode, tile - kBlockMainTiles, stream);
 }
 
 hipError_t launch_fp8_block_mm(BlockMmArgs a, int mode, int tile, hipStream_t stream)

@@ -14,9 +14,11 @@
 // sums meet in LDS once at the end. The packed fragment is the MFMA's A operand
 // as stored, the token rows its B operand, so a lane holds runs of four
 // channels of one token.
-//   - WK = 8 where K has many blocks, WK = 2 beside WN = 4 where it has few: a
-//     wave with a single block waits for it and then for its neighbours (48
-//     tokens to 64 experts, K 1024: @@ us with WK = 8, @@ so).
+//   - WK = 8 for a layer, whose column tiles alone are few; WK = 2 beside WN = 4 for
+//     experts, whose tiles are many: a wave with a block or two waits for those
+//     and then for its neighbours (48 tokens, 8 of 64 experts each, N 4096, K
+//     1024: 90 us with WK = 8, 46 so; whole layer, K 4096, inner 1024, 4 of 64: 4
+//     tokens 51.6 and 48.9, 256 234 and 218).
 //   - NT: weights that one row tile reads pass the caches by (M1 N12288 K4096:
 //     11.7 us without, 10.3 so, 4.9 TB/s; below 16 MB, which the caches may
 //     hold, 4.6 without and 5.0 so).
@@ -358,11 +360,17 @@ __global__ __launch_bounds__(64 * kDirectWaves) void down_direct_kernel(const Bl
 template <class S>
 constexpr BlockTileEntry entry(const char *name)
 {
+    // (the experts run on the last two tiles)
+    BlockMmKernel up = nullptr, down = nullptr;
+    if constexpr (S::NT) {
+        up = block_mm_small_kernel<S, kJobGateUp, kOutI32, kCodes>;
+        down = block_mm_small_kernel<S, kJobDown, kOutI32, kCodes>;
+    }
     return BlockTileEntry{
         name, S::BM, S::BN, S::THREADS, true,
         {block_mm_small_kernel<S, kJobDense, kOutBF16, kCodes>, block_mm_small_kernel<S, kJobDense, kOutI32, kCodes>,
          block_mm_small_kernel<S, kJobDense, kOutF16, kCodes>},
-        block_mm_small_kernel<S, kJobGateUp, kOutI32, kCodes>, block_mm_small_kernel<S, kJobDown, kOutI32, kCodes>};
+        up, down};
 }
 
 // 16 token rows x 16*FN*WN channels / WN x WK waves / U blocks at a time.
@@ -371,6 +379,7 @@ const BlockTileEntry kSmall[] = {
     entry<Small<2, 1, 8, 2, true>>("s16x32/n1k8/u2nt"),
     entry<Small<2, 4, 2, 4, true>>("s16x128/n4k2/u4nt"),
 };
+static_assert(sizeof(kSmall) / sizeof(kSmall[0]) == kBlockSmallTiles, "tiles");
 
 // The quant in the same launch: of a layer's rows, and of slots' tokens.
 template <class S, int E>
@@ -391,7 +400,6 @@ using Stream = Small<2, 1, 8, 2, true>;
 
 }  // namespace
 
-int fp8_block_small_count() { return (int)(sizeof(kSmall) / sizeof(kSmall[0])); }
 const BlockTileEntry &fp8_block_small(int i) { return kSmall[i]; }
 
 hipError_t launch_fp8_block_small_quant(BlockMmArgs a, int x_kind, int mode, int i, hipStream_t stream)
