@@ -40,7 +40,8 @@ def scale_of(a):
     a = np.asarray(a, dtype=np.float32)
     live = ~(a < np.float32(2.0 ** -100))
     with np.errstate(all="ignore"):
-        return np.where(live, a / np.float32(448), np.float32(0)), np.where(live, np.float32(1) / a * np.float32(448), np.float32(0))
+        s, f = a / np.float32(448), np.float32(1) / a * np.float32(448)
+        return np.where(live, s, np.float32(0)), np.where(live, f, np.float32(0))
 
 
 def _blocked(x):
@@ -92,7 +93,8 @@ def product(x, w, k_total=None):
 
 
 def silu(v):
-    return v / (1 + np.exp(-v))
+    with np.errstate(over="ignore"):
+        return v / (1 + np.exp(-v))
 
 
 def gated(g, u, dg, du):

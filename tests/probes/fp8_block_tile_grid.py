@@ -119,9 +119,12 @@ def fit(path: str) -> int:
         at = [(terms(name, r["M"], r["N"], r["K"]), r["us"][name]) for r in grid if name in r["us"]]
         a = np.array([[v / us for v in t] for t, us in at])
         cost[name] = nnls(a, np.ones(len(a)))[0]
-        print(name, " ".join(f"{v:.4g}" for v in cost[name]), f"rms error {np.sqrt(np.mean((a @ cost[name] - 1) ** 2)):.3f}")
-    for what, choose in (("library", lambda r: r["auto"]),
-                         ("fitted", lambda r: min(r["us"], key=lambda t: np.dot(terms(t, r["M"], r["N"], r["K"]), cost[t])))):
+        off = np.sqrt(np.mean((a @ cost[name] - 1) ** 2))
+        print(name, " ".join(f"{v:.4g}" for v in cost[name]), f"rms error {off:.3f}")
+    def fitted(r):
+        return min(r["us"], key=lambda t: np.dot(terms(t, r["M"], r["N"], r["K"]), cost[t]))
+
+    for what, choose in (("library", lambda r: r["auto"]), ("fitted", fitted)):
         chosen = [r for r in grid if choose(r) in r["us"]]
         over = np.array([r["us"][choose(r)] / min(r["us"].values()) for r in chosen])
         print(f"{what} choice over the best of {len(chosen)} shapes: mean {over.mean():.4f}, largest {over.max():.3f}, "

@@ -44,7 +44,8 @@ def test_quant_checks():
         assert f(**{"ld" + rows: 143}) == SHAPE and f(ldq=143) == SHAPE and f(lds=1) == SHAPE
         assert f(M=0, q=None, s=None, **{rows: None}) == OK
         assert f(q=None) == NULL and f(s=None) == NULL and f(**{rows: None}) == NULL
-        assert f(**{rows: A + 8}) == ALIGN and f(**{"ld" + rows: 148}) == ALIGN and f(t=1, **{"ld" + rows: 146}) == ALIGN
+        assert f(**{rows: A + 8}) == ALIGN and f(**{"ld" + rows: 148}) == ALIGN
+        assert f(t=1, **{"ld" + rows: 146}) == ALIGN
         assert f(q=A + 4) == ALIGN and f(ldq=148) == ALIGN and f(s=A + 2) == ALIGN
         if NO_GPU:
             assert f() == DEVICE and f(t=1, **{"ld" + rows: 148}) == DEVICE
@@ -80,7 +81,8 @@ def test_mm_checks():
         for name in ("xq", "xs", "wp", "ws", "out"):
             assert f(**{name: None}) == NULL, name
         assert f(xq=A + 8) == ALIGN and f(ldq=152) == ALIGN and f(wp=A + 8) == ALIGN and f(ws=A + 2) == ALIGN
-        assert f(xs=A + 4) == ALIGN and f(lds=6) == ALIGN and f(out=A + 1) == ALIGN and f(out=A + 2, mode=1) == ALIGN and f(bias=A + 1) == ALIGN
+        assert f(xs=A + 4) == ALIGN and f(lds=6) == ALIGN and f(out=A + 1) == ALIGN
+        assert f(out=A + 2, mode=1) == ALIGN and f(bias=A + 1) == ALIGN
         n = 2 ** 31 - 1
         assert f(M=n, N=n, ldo=n) == SHAPE                  # no launch holds that many tiles
         none = dict(xq=None, xs=None, wp=None, ws=None, out=None)
@@ -131,7 +133,8 @@ def experts(gu=A, gs=A, dn=A, ds=A, K=144, inner=80, E=4, x=A, t=0, ldx=144, T=4
 def test_experts_checks():
     assert L.fp8_block_experts(None, A, 0, 144, 4, A, A, 2, A, 144, A, 1 << 40, None) == NULL
     assert experts(t=3) == MODE
-    for bad in (dict(T=-1), dict(K=136, ldx=136, ldo=136), dict(K=0), dict(inner=8), dict(inner=24), dict(E=0), dict(E=1025),
+    for bad in (dict(T=-1), dict(K=136, ldx=136, ldo=136), dict(K=0), dict(inner=8), dict(inner=24), dict(E=0),
+                dict(E=1025),
                 dict(k=0), dict(k=65), dict(K=BIG, ldx=BIG, ldo=BIG), dict(inner=BIG), dict(ldx=143), dict(ldo=143),
                 dict(T=2 ** 31)):
         assert experts(**bad) == SHAPE, bad

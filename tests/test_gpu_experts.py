@@ -45,7 +45,8 @@ def logits_of(t, e, seed, dtype=torch.float32):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("t,e,k", [(1, 1, 1), (1, 256, 8), (5, 8, 8), (33, 60, 6), (7, 64, 64), (9, 65, 3), (2, 1024, 16),
+@pytest.mark.parametrize("t,e,k", [(1, 1, 1), (1, 256, 8), (5, 8, 8), (33, 60, 6), (7, 64, 64), (9, 65, 3),
+                                   (2, 1024, 16),
                                    (130, 160, 6)])
 def test_route(ops, dtype, score, t, e, k):
     """Sixteen-bit logits have many equal ones in a row: ties go to the lowest index."""
@@ -56,7 +57,8 @@ def test_route(ops, dtype, score, t, e, k):
             same_route(ops, x, f"{t} {e} {b is None}", top_k=k, score=score, bias=b, renormalize=renormalize, scale=2.5)
 
 
-@pytest.mark.parametrize("groups,top_groups,e", [(8, 4, 256), (2, 1, 16), (64, 3, 128), (4, 4, 60), (3, 2, 99), (8, 1, 8)])
+@pytest.mark.parametrize("groups,top_groups,e", [(8, 4, 256), (2, 1, 16), (64, 3, 128), (4, 4, 60), (3, 2, 99),
+                                                 (8, 1, 8)])
 @pytest.mark.parametrize("group_top", [1, 2])
 def test_route_groups(ops, groups, top_groups, e, group_top):
     bias = 0.1 * torch.randn(e, generator=torch.Generator().manual_seed(1))
@@ -95,8 +97,8 @@ def test_route_masks(ops, score, groups):
     hard[5], hard[6] = -inf, float("nan")
     for b in (None, bias, hard):
         for renormalize in (True, False):
-            same_route(ops, x, f"{score} {groups} {b is None} {renormalize}", top_k=5, score=score, bias=b, groups=groups,
-                       top_groups=max(1, groups - 1), renormalize=renormalize)
+            same_route(ops, x, f"{score} {groups} {b is None} {renormalize}", top_k=5, score=score, bias=b,
+                       groups=groups, top_groups=max(1, groups - 1), renormalize=renormalize)
 
 
 def test_route_strides_streams_and_graph(ops):
@@ -176,7 +178,8 @@ def test_experts(ops, dtype, t, e, top_k, k, inner):
     assert torch.equal(layer(x.to(DEV), ids.to(DEV), w.to(DEV)), y)
 
 
-@pytest.mark.parametrize("t,e,top_k,k,inner", [(1200, 36, 6, 784, 784), (1000, 32, 3, 784, 912), (1500, 64, 2, 1040, 784)])
+@pytest.mark.parametrize("t,e,top_k,k,inner", [(1200, 36, 6, 784, 784), (1000, 32, 3, 784, 912),
+                                               (1500, 64, 2, 1040, 784)])
 def test_experts_many_tiles(ops, t, e, top_k, k, inner):
     """About 200, 94 and 47 rows an expert, of uneven shares, in more tiles than the card holds at once."""
     parts, gv, dv = make(e, inner, k, t)
@@ -220,6 +223,116 @@ def test_experts_any_ids(ops, t):
         assert torch.equal(f.bfloat16(), y)
 
 
+@pytest.mark.parametrize("t", [1, 20, 60, 500])
+def test_experts_large_values(ops, t):
+    """Inner rows up to about 1e36 and sums of scales past 2^103: results in fp32's range are there."""
+    e, top_k, k, inner = 4, 2, 272, 144
+    parts, gv, dv = make(e, inner, k, 15)
+    layer = layer_of(parts)
+    x = rows(t, k, 2, torch.float32).clamp(-4, 4) * 2.0 ** 58
+    ids, w = choose(t, e, top_k, 5)
+    exact, bound = ref.experts(ref.dequant(*ref.quant(x.numpy())), ids.numpy(), w.numpy(), gv, dv)
+    assert np.abs(exact).max() < 2.0 ** 126
+    y = ops.fp8_block_experts(x.to(DEV), ids.to(DEV), w.to(DEV), layer.gate_up, layer.gate_up_scale, layer.down,
+                              layer.down_scale, inner)
+    check(y, exact, bound, torch.float32)
+
+
+@pytest.mark.parametrize("t", [3, 5000])
+def test_experts_many_experts_and_choices(ops, t):
+    """1024 experts of one block each way; 64 choices a token."""
+    for e, top_k, k, inner in ((1024, 6, 128, 16), (70, 64, 144, 32)):
+        t1 = min(t, 300) if top_k == 64 else t
+        parts, gv, dv = make(e, inner, k, 17)
+        layer = layer_of(parts)
+        x = (rows(t1, k, t, torch.float32) * 0.3).to(torch.bfloat16)
+        ids, w = choose(t1, e, top_k, 5)
+        exact, bound = ref.experts(ref.dequant(*ref.quant(x.float().numpy())), ids.numpy(), w.numpy(), gv, dv)
+        check(layer(x.to(DEV), ids.to(DEV), w.to(DEV)), exact, bound, torch.bfloat16, what=f"{e} experts")
+
+
+def test_experts_passes(ops):
+    """More than 65536 slots go in passes: the tokens of each have the values of a call that is
+    one pass."""
+    e, top_k, k, inner, t = 24, 4, 144, 48, 20000
+    parts, _, _ = make(e, inner, k, 19)
+    layer = layer_of(parts)
+    x = (rows(t, k, 2, torch.float32) * 0.3).to(torch.bfloat16).to(DEV)
+    ids, w = (v.to(DEV) for v in choose(t, e, top_k, 5))
+    y, one = layer(x, ids, w), 65536 // top_k
+    assert torch.equal(y[:one], layer(x[:one], ids[:one], w[:one]))
+    assert torch.equal(y[t - one:], layer(x[t - one:], ids[t - one:], w[t - one:]))
+
+
+@pytest.mark.parametrize("t", [1, 300, 5000])
+def test_experts_weights_past_32_bits(ops, t):
+    """The last of experts whose weights end past 4 GiB, by three paths."""
+    e, k, inner = 264, 4096, 2048
+    g, u, dn = (weights(*s, 23 + j) for j, s in enumerate(((inner, k), (inner, k), (k, inner))))
+    gate_up = torch.zeros(e, 2 * inner, k, dtype=torch.uint8, device=DEV)
+    gate_up[-1] = dev(np.concatenate((g[0], u[0])))
+    down = torch.zeros(e, k, inner, dtype=torch.uint8, device=DEV)
+    down[-1] = dev(dn[0])
+    gs = torch.zeros(e, 2 * inner // 128, k // 128, device=DEV)
+    gs[-1] = dev(np.concatenate((g[1], u[1])))
+    ds = torch.zeros(e, k // 128, inner // 128, device=DEV)
+    ds[-1] = dev(dn[1])
+    from w8a8_int8_dynamic_amd import W8A8Experts
+    layer = W8A8Experts.from_quantized(gate_up, gs, down, ds)
+    assert layer.gate_up.numel() > 2 ** 32
+    x = (rows(t, k, 2, torch.float32) * 0.1).to(torch.bfloat16)
+    ids, w = torch.full((t, 1), e - 1, dtype=torch.int32), torch.ones(t, 1)
+    y = layer(x.to(DEV), ids.to(DEV), w.to(DEV))
+    some = [0, t // 2, t - 1]
+    exact, bound = ref.experts(ref.dequant(*ref.quant(x[some].float().numpy())), np.zeros((3, 1), np.int32),
+                               np.ones((3, 1), np.float32), [np.concatenate((ref.weight(*g), ref.weight(*u)))],
+                               [ref.weight(*dn)])
+    check(y[some], exact, bound, torch.bfloat16)
+
+
+def test_rows_past_32_bits(ops):
+    """Rows of logits, inputs and outputs 2 GiB apart."""
+    far, t, e, top_k, k, inner = 2 ** 30, 5, 60, 3, 144, 48
+    big = torch.empty(far * (t - 1) + 1024, dtype=torch.bfloat16, device=DEV)
+    logits = logits_of(t, e, 1, torch.bfloat16)
+    view = big.as_strided((t, e), (far, 1))
+    view.copy_(logits)
+    how = ops.Routing(top_k, score="sigmoid")
+    want, got = ops.route_experts(logits.to(DEV), how), ops.route_experts(view, how)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    parts, _, _ = make(4, inner, k, 21)
+    layer = layer_of(parts)
+    x = (rows(t, k, 2, torch.float32) * 0.3).to(torch.bfloat16).to(DEV)
+    view, out = big.as_strided((t, k), (far, 1)), big.as_strided((t, k), (far, 1), 512)
+    view.copy_(x)
+    for n, reps in ((t, 1), (t, 40)):
+        ids, w = (v.to(DEV) for v in choose(t * reps, 4, 2, 5))
+        ids, w = ids[:n], w[:n]
+        args = (layer.gate_up, layer.gate_up_scale, layer.down, layer.down_scale, inner)
+        ops.fp8_block_experts(view, ids, w, *args, out=out)
+        assert torch.equal(out, ops.fp8_block_experts(x, ids, w, *args))
+
+
+def test_experts_on_two_streams_at_once(ops):
+    e, top_k, k, inner = 6, 2, 272, 144
+    parts, _, _ = make(e, inner, k, 25)
+    layer = layer_of(parts)
+    streams, sets = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for n, t in enumerate((7, 400)):
+        x = (rows(t, k, n, torch.float32) * 0.3).to(torch.bfloat16).to(DEV)
+        ids, w = (v.to(DEV) for v in choose(t, e, top_k, n))
+        sets.append((x, ids, w, layer(x, ids, w)))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for n, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[n].append(layer(*sets[n][:3]))
+    torch.cuda.synchronize()
+    for n in range(2):
+        assert all(torch.equal(y, sets[n][3]) for y in got[n])
+
+
 def test_experts_rows_are_their_own(ops):
     """A token's result does not depend on the tokens beside it nor on which of them share its
     experts (within one path), and a token that is not finite harms no other."""
@@ -256,7 +369,8 @@ def test_experts_strides_and_shapes(ops):
         wide[:, at:at + k] = x
         assert torch.equal(layer(wide[:, at:at + k], ids, w), want)
     assert torch.equal(layer(x, ids.t().contiguous().t(), w.t().contiguous().t()), want)
-    assert torch.equal(layer(x.reshape(2, 3, 4, k), ids.reshape(2, 3, 4, 2), w.reshape(2, 3, 4, 2)), want.reshape(2, 3, 4, k))
+    got = layer(x.reshape(2, 3, 4, k), ids.reshape(2, 3, 4, 2), w.reshape(2, 3, 4, 2))
+    assert torch.equal(got, want.reshape(2, 3, 4, k))
     for at in (8, 3):
         out = torch.full((t, k + 24), 7.0, dtype=torch.bfloat16, device=DEV)
         ops.fp8_block_experts(x, ids, w, layer.gate_up, layer.gate_up_scale, layer.down, layer.down_scale, inner,
@@ -322,7 +436,8 @@ def test_from_float(ops):
     gate_up, down = torch.randn(e, 2 * inner, k, generator=g), torch.randn(e, k, inner, generator=g)
     for dtype in (torch.float32, torch.bfloat16, torch.float16):
         layer = W8A8Experts.from_float(gate_up.to(dtype).to(DEV), down.to(dtype).to(DEV))
-        q = [[ref.quant_weight(p.to(dtype).float().numpy()) for p in (a[:inner], a[inner:], b)] for a, b in zip(gate_up, down)]
+        q = [[ref.quant_weight(p.to(dtype).float().numpy()) for p in (a[:inner], a[inner:], b)]
+             for a, b in zip(gate_up, down)]
         other = layer_of([np.stack([np.concatenate((p[0][i], p[1][i])) for p in q]) if j == 0 else
                           np.stack([p[2][i] for p in q]) for j, i in ((0, 0), (0, 1), (1, 0), (1, 1))])
         for name in ("gate_up", "gate_up_scale", "down", "down_scale"):

@@ -186,6 +186,36 @@ def test_product_every_tile(ops, m, n, k):
             check(got, exact, bound, dtype, what=what)
 
 
+@pytest.mark.parametrize("m,n,k", [(70, 260, 8336), (3, 40, 131056)])
+def test_product_long_rows(ops, m, n, k):
+    """More than 64 blocks, and the most."""
+    test_product_every_tile(ops, m, n, k)
+
+
+def test_offsets_past_32_bits(ops):
+    """More than 2^32 codes, and results 2 GiB apart: the last rows are those of a small call."""
+    m, k = 270000, 16384
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device=DEV)
+    x[-3:] = rows(3, k, 1).to(DEV)
+    q, s = ops.fp8_quant_per_block(x)
+    q3, s3 = ops.fp8_quant_per_block(x[-3:].clone())
+    assert q.numel() > 2 ** 32 and torch.equal(q[-3:], q3) and torch.equal(s[-3:], s3)
+    assert torch.equal(ops.fp8_block_dequant(q, s)[-3:], ops.fp8_block_dequant(q3, s3))
+    del x
+    wq, ws = weights(80, k, 2)
+    packed, w = ops.fp8_block_prepack_weight(dev(wq)), dev(ws)
+    for tile in range(ops.fp8_block_tile_count()):
+        got = ops.fp8_block_scaled_mm(q, s, packed, w, 80, tile=tile)
+        assert torch.equal(got[-3:], ops.fp8_block_scaled_mm(q3, s3, packed, w, 80, tile=tile)), tile
+    far = 2 ** 30
+    out = torch.empty(far * 2 + 80, dtype=torch.bfloat16, device=DEV).as_strided((3, 80), (far, 1))
+    for tile in range(ops.fp8_block_tile_count()):
+        want = ops.fp8_block_scaled_mm(q3, s3, packed, w, 80, tile=tile)
+        out.zero_()
+        ops.fp8_block_scaled_mm(q3, s3, packed, w, 80, out=out, tile=tile)
+        assert torch.equal(out, want), tile
+
+
 @pytest.mark.parametrize("m,n,k", [(5, 70, 272), (140, 200, 400)])
 def test_product_strides(ops, m, n, k):
     """Rows of codes, scales and outputs further apart than they are long; what lies

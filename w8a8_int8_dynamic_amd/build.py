@@ -35,7 +35,8 @@ TIMELINE_SOURCE = "scaled_mm.hip"
 SOURCES = ["quant.hip", "prepack.hip", "scaled_mm.hip", "scaled_mm_fp8.hip", "skinny_mm.hip",
            "quant_fp4.hip", "scaled_mm_fp4.hip", "skinny_fp4.hip", "norm_rows_bf16.hip", "norm_rows_f16.hip",
            "norm_rows_f32_bf16.hip", "norm_rows_f32_f16.hip", "quant_fp8_block.hip", "scaled_mm_fp8_block.hip",
-           "main_fp8_block.hip", "small_fp8_block.hip", "routing.hip", "experts.hip", "api.cpp", "api_fp4.cpp", "api_norm.cpp",
+           "main_fp8_block.hip", "small_fp8_block.hip", "routing.hip", "experts.hip", "api.cpp", "api_fp4.cpp",
+           "api_norm.cpp",
            "api_fp8_block.cpp", "api_experts.cpp"]
 ARCH = "gfx950"
 

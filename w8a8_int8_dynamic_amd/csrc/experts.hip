@@ -160,14 +160,15 @@ __global__ __launch_bounds__(256) void combine_kernel(const void *__restrict__ y
         const int id = ids[slot];
         if (id < 0 || id >= experts)
             continue;
-        float w = weights[slot], v[8];
+        const float w = weights[slot];
+        float v[8];
         if constexpr (Y16) {
-            w *= y_scale[slot * ld_scale + col / kBlock];
+            const float s = y_scale[slot * ld_scale + col / kBlock];
             const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(y) + slot * K + col);
             const u32 d[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int r = 0; r < 8; ++r)
-                v[r] = quant_rule::f16_to_float(d[r >> 1] >> (16 * (r & 1)));
+                v[r] = quant_rule::f16_to_float(d[r >> 1] >> (16 * (r & 1))) * s;   // (exact)
         } else {
             const f32x4 *q = reinterpret_cast<const f32x4 *>(static_cast<const float *>(y) + slot * K + col);
             const f32x4 lo = q[0], hi = q[1];
@@ -375,9 +376,9 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         const int threads = many ? kManyThreads : kFewThreads;
         auto prepare = args.kind == kElemF32 ? prepare_pick<kF32>(c.u, many)
                      : args.kind == kElemF16 ? prepare_pick<kF16>(c.u, many) : prepare_pick<kBF16>(c.u, many);
-        hipLaunchKernelGGL(prepare, dim3((unsigned)(args.experts + ceil_div(c.blocks, threads / 256))), dim3(threads), 0,
-                           stream, ids, slots, args.experts, bm, order, tiles, tiles_m, x, tokens, units, padded, args.ldx, xq, args.K, xs,
-                           scale_pitch(args.K), c.segs, c.rpb);
+        hipLaunchKernelGGL(prepare, dim3((unsigned)(args.experts + ceil_div(c.blocks, threads / 256))), dim3(threads),
+                           0, stream, ids, slots, args.experts, bm, order, tiles, tiles_m, x, tokens, units, padded,
+                           args.ldx, xq, args.K, xs, scale_pitch(args.K), c.segs, c.rpb);
 
         up.tiles = down.tiles = tiles;
         up.tiles_m = down.tiles_m = tiles_m;

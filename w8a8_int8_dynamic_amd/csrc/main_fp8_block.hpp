@@ -441,9 +441,10 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES) void block_mm_kernel(const Bl
         // 16-bit rows, staged in LDS and written whole, 16 bytes a lane (M4096
         // N4096: 9 us of 8-byte stores from registers, 3.4 so). Down: fp16 under a
         // power of two per row and block of channels, so that a slot's row
-        // costs half of fp32's bytes and a quarter of the 2^-9 that bf16 would
-        // lose: |acc| <= 448 * 448 * 128 * the sum of its scales, brought below
-        // 2^15; values 2^-29 of that bound and less leave fp16's normal range.
+        // costs half of fp32's bytes and an eighth of the 2^-8 that bf16 would
+        // lose: |acc| <= 448 * 448 * 128 * the sum of its scales < 2^25 times that,
+        // brought below 2^15; values below about 2^-28 of that leave fp16's normal
+        // range.
         constexpr bool F16 = OUT == kOutF16;
         // Down: the slots of the wave's rows, then of the thread's pieces, are read
         // ahead of the stores, which the compiler would else keep them behind (M
@@ -459,13 +460,12 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES) void block_mm_kernel(const Bl
             const int m = 16 * (i * T::WM + wm) + r16;
             float down = 1.0f;
             if constexpr (JOB == kJobDown) {
-                const float top = bound[i] * (448.0f * 448.0f * 128.0f);
-                const int e = (int)((__float_as_uint(top) >> 23) & 255u) - 126 - 15;   // top < 2^(e + 15)
-                const bool odd = !(top > 0x1p-100f && top < 0x1p126f);   // zero, not finite, or out of reach
-                down = odd ? 1.0f : __uint_as_float((u32)(127 - e) << 23);
+                // bound < 2^(e - 10), or else |acc| < 2^128 (and what is not finite stays so)
+                const int e = min((int)((__float_as_uint(bound[i]) >> 23) & 255u) - 126 + 10, 113);
+                down = __uint_as_float((u32)(127 - e) << 23);
                 if (sub == 0 && (wn * TN) % 8 == 0 && m < rows && wf < a.frags)
                     a.out_scale[(int64_t)slot_of[i] * a.ld_out_scale + (wf >> 3)] =
-                        odd ? 1.0f : __uint_as_float((u32)(127 + e) << 23);
+                        __uint_as_float((u32)(127 + e) << 23);
             }
 #pragma unroll
             for (int j = 0; j < TN; ++j) {

@@ -26,7 +26,8 @@ __all__ = ["quant_per_token", "quant_per_channel", "prepack_weight", "quant_prep
            "fp4_tile_auto", "fp8_quant_per_block", "fp8_block_dequant", "fp8_block_prepack_weight",
            "fp8_block_quant_prepack_weight", "fp8_block_unpack_weight", "fp8_block_scaled_mm",
            "fp8_block_quant_scaled_mm", "fp8_block_tile_count", "fp8_block_tile_name", "fp8_block_tile_auto",
-           "Routing", "route_experts", "fp8_block_experts", "Norm", "norm", "norm_quant_per_token", "fp8_norm_quant_per_token", "gated_residual",
+           "Routing", "route_experts", "fp8_block_experts", "Norm", "norm",
+           "norm_quant_per_token", "fp8_norm_quant_per_token", "gated_residual",
            "gated_residual_norm", "gated_residual_norm_quant", "fp8_gated_residual_norm_quant"]
 
 
