@@ -429,6 +429,15 @@ def test_together(ops, t):
         assert torch.equal(block(xs[i]), want[i]), i
 
 
+def test_no_tokens(ops):
+    parts, _, _ = make(4, 48, 144, 27)
+    layer = layer_of(parts, routing=ops.Routing(2))
+    for lead in ((0,), (3, 0)):
+        x = torch.empty(*lead, 144, dtype=torch.bfloat16, device=DEV)
+        y = layer.forward_logits(x, torch.empty(*lead, 4, device=DEV))
+        assert y.shape == x.shape and y.dtype == x.dtype
+
+
 def test_from_float(ops):
     from w8a8_int8_dynamic_amd import W8A8Experts
     e, k, inner = 3, 272, 144

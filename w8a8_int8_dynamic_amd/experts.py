@@ -103,8 +103,8 @@ class W8A8Experts(torch.nn.Module):
             raise ValueError(f"logits must be {(*x.shape[:-1], self.experts)}, got {tuple(logits.shape)}")
         logits = logits.reshape(-1, self.experts)
         ids, weights = ops.route_experts(logits if logits.stride(-1) == 1 else logits.contiguous(), self.routing)
-        lead = x.shape[:-1]
-        return self.forward(x, ids.reshape(*lead, -1), weights.reshape(*lead, -1))
+        shape = (*x.shape[:-1], self.routing.top_k)
+        return self.forward(x, ids.reshape(shape), weights.reshape(shape))
 
     def extra_repr(self) -> str:
         return f"in_features={self.in_features}, inner={self.inner}, experts={self.experts}"
