@@ -36,6 +36,12 @@
 // Experts: the token tiles of a run that is shorter than BM rows are not
 // computed (they alternate between the two waves of a SIMD, so that what is
 // left out is left out of both).
+// Measured, M8192 N4096 K12288: 344 us, 2.4 PFLOP/s, the matrix cores busy 66 %
+// of the cycles at 1.85 GHz: power bounds it (the same instructions from
+// registers alone, on random codes, hold 1.8 GHz). A form whose workgroups stay
+// on their CU, load the next tile's first stages under a tile's last steps and
+// do not wait for its stores took 354-360 us there, and as long as this one for
+// 32768 rows of 64 experts; so a workgroup has one tile.
 // Ragged tails: rows past the last read that one again, fragments past the
 // weight its last (their results are not stored); k-chunks past K read the
 // row's last chunk, which meets zero weights.

@@ -7,7 +7,8 @@
 // exchanges give the block's maximum, and its code words are contiguous too.
 // A workgroup takes U x 256 such units of one row, or several whole rows where
 // a row is shorter than that. Rows whose last block is part full keep their
-// units in whole blocks (idle lanes count as zeros).
+// units in whole blocks (idle lanes count as zeros). M8192 K12288 bf16: 50 us,
+// 6.0 TB/s; the inverse 44 us, 6.9 (part of the codes are still in the caches).
 #include <algorithm>
 
 #include "quant_fp8_block.hpp"

@@ -20,7 +20,7 @@
 // and a step of the selection compares only the lanes' best, and the scores of
 // the chosen are computed again at the end, one lane each, instead of being
 // carried along. 256 experts in 8 groups, 8 chosen: 8192 tokens 14.9 us, one
-// token 6.0 (with exchanges through LDS, all of a lane's choices compared at
+// token 5.6 (with exchanges through LDS, all of a lane's choices compared at
 // every step and the library's exponential: 31 and 10 us).
 #include "experts.hpp"
 #include "quant_rule.hpp"

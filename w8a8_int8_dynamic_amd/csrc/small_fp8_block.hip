@@ -22,6 +22,8 @@
 //   - NT: weights that one row tile reads pass the caches by (M1 N12288 K4096:
 //     11.7 us without, 10.3 so, 4.9 TB/s; below 16 MB, which the caches may
 //     hold, 4.6 without and 5.0 so).
+//     Experts, 48 tokens to 8 of 64, K 4096, inner 1024: gated products 84 us, 6.4
+//     TB/s, down 44 us, 6.1.
 //   - QK: the rows come as floats. Every workgroup quantizes them into LDS
 //     while its first weights are on their way, 8 elements a thread at a time
 //     (they are few and sit in L2); the workgroups of the first channels write
