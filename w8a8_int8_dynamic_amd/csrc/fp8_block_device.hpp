@@ -19,6 +19,36 @@ __device__ __forceinline__ f32x4 block_product(const v4i (&w)[2], const v4i (&x)
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ww, xx, f32x4{}, 0, 0, 0, 127, 0, 127);
 }
 
+// The same of FN fragments with exact products: both operands as bf16 values,
+// which hold an e4m3 value exactly, eight k of a lane at a time.
+__device__ __forceinline__ v8bf widen(u32 lo, u32 hi)
+{
+    v8bf o{};
+#if defined(__HIP_DEVICE_COMPILE__)
+    const bf16x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false),
+                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true),
+                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false),
+                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        o[i] = p[i >> 1][i & 1];
+#endif
+    return o;
+}
+template <int FN>
+__device__ __forceinline__ void wide_products(const v4i (&w)[FN][2], const v4i (&x)[2], f32x4 (&p)[FN])
+{
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const v8bf xw = widen((u32)x[g >> 1][(g & 1) * 2], (u32)x[g >> 1][(g & 1) * 2 + 1]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                widen((u32)w[j][g >> 1][(g & 1) * 2], (u32)w[j][g >> 1][(g & 1) * 2 + 1]), xw,
+                g == 0 ? f32x4{} : p[j], 0, 0, 0);
+    }
+}
+
 // Scale row of packed fragment nb.
 template <int JOB>
 __device__ __forceinline__ int scale_row(int nb, int half_scales)

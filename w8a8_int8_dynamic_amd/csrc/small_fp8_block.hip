@@ -47,6 +47,7 @@ struct Small {
     static constexpr int BM = 16, BF = FN * WN, BN = 16 * BF, THREADS = 64 * WN * WK;
 };
 
+constexpr int cmin(int a, int b) { return a < b ? a : b; }
 constexpr int kCodes = -1;       // QK: codes and scales made before
 constexpr int kSlots = 4;        // units of 8 elements that a thread quantizes, at most
 
@@ -98,7 +99,7 @@ __device__ __forceinline__ void quantize_rows(const BlockMmArgs &a, Source &&sou
 }
 
 template <class S, int JOB, int OUT, int QK>
-__global__ __launch_bounds__(S::THREADS) void block_mm_small_kernel(const BlockMmArgs a)
+__global__ __launch_bounds__(S::THREADS, JOB == kJobGateUp || S::WN == 4 ? 4 : 1) void block_mm_small_kernel(const BlockMmArgs a)
 {
     __shared__ f32x4 part[S::WN][S::WK - 1][S::FN][64];
     extern __shared__ __attribute__((aligned(16))) char tok[];   // QK: the quantized rows
@@ -127,6 +128,8 @@ __global__ __launch_bounds__(S::THREADS) void block_mm_small_kernel(const BlockM
         tn = t / tiles_m;
         tile = JOB == kJobDense ? BlockTile{0, tm * S::BM, min(S::BM, a.M - tm * S::BM)} : a.tiles[tm];
     }
+    tile = BlockTile{__builtin_amdgcn_readfirstlane(tile.expert), __builtin_amdgcn_readfirstlane(tile.row0),
+                     __builtin_amdgcn_readfirstlane(tile.rows)};
     const int nb0 = tn * S::BF + wn * S::FN;
     const uint8_t *wp = a.wp + tile.expert * a.expert_bytes;
     const float *ws = a.ws + tile.expert * a.expert_scales;
@@ -171,29 +174,43 @@ __global__ __launch_bounds__(S::THREADS) void block_mm_small_kernel(const BlockM
             }
         }
     };
+    // Token operands: of all U blocks at a time, or where bf16 operands need the
+    // registers of two.
+    constexpr int AT = JOB == kJobGateUp ? cmin(S::U, 2) : S::U;
     auto products = [&](int b0) __attribute__((always_inline)) {
-        v4i x[S::U][2];
-        float xs[S::U];
-#pragma unroll
-        for (int u = 0; u < S::U; ++u) {
+        v4i x[AT][2];
+        float xs[AT];
+        auto tokens = [&](int u) __attribute__((always_inline)) {
             const int b = min(b0 + u * S::WK, a.blocks - 1);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                x[u][h] = *reinterpret_cast<const v4i *>(xrow + min(b * kBlock + (4 * h + sub) * 16, last_chunk));
-            xs[u] = *reinterpret_cast<const float *>(xsrow + b * 4);
-        }
+                x[u % AT][h] = *reinterpret_cast<const v4i *>(xrow + min(b * kBlock + (4 * h + sub) * 16, last_chunk));
+            xs[u % AT] = *reinterpret_cast<const float *>(xsrow + b * 4);
+        };
+#pragma unroll
+        for (int u = 0; u < AT; ++u)
+            tokens(u);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < S::U; ++u) {
             if (b0 + u * S::WK >= a.blocks)
                 break;
+            f32x4 p[S::FN];
+            if constexpr (JOB == kJobGateUp)
+                wide_products(w[u], x[u % AT], p);
 #pragma unroll
             for (int j = 0; j < S::FN; ++j) {
-                const f32x4 p = block_product(w[u][j], x[u]);
-                const float s = xs[u] * sw[u][j];
+                if constexpr (JOB != kJobGateUp)
+                    p[j] = block_product(w[u][j], x[u]);
+                const float s = xs[u % AT] * sw[u][j];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    acc[j][k] = __builtin_fmaf(p[k], s, acc[j][k]);
+                    acc[j][k] = __builtin_fmaf(p[j][k], s, acc[j][k]);
+            }
+            if constexpr (JOB == kJobGateUp) {
+                __builtin_amdgcn_sched_barrier(0);        // (one block's bf16 operands at a time)
+                if (u + AT < S::U)
+                    tokens(u + AT);
             }
         }
     };
