@@ -24,6 +24,12 @@
 //     hold, 4.6 without and 5.0 so).
 //     Experts, 48 tokens to 8 of 64, K 4096, inner 1024: gated products 84 us, 6.4
 //     TB/s, down 44 us, 6.1.
+//   - Gated products are summed from bf16 values, without the e4m3 instruction's
+//     error: an inner element near the border of two codes falls to either side by
+//     it, a step of 2^-3. The matrix cores wait for the weights anyway (48 tokens
+//     as above 144 us from e4m3, 146 so; outputs 1.6-2.8e-3 of their norm from the
+//     elementwise form's, and 4e-4 so). The main kernel, which computes the time
+//     it takes, keeps e4m3: 128-row tiles lost 5-20 % by it.
 //   - QK: the rows come as floats. Every workgroup quantizes them into LDS
 //     while its first weights are on their way, 8 elements a thread at a time
 //     (they are few and sit in L2); the workgroups of the first channels write
@@ -98,8 +104,10 @@ __device__ __forceinline__ void quantize_rows(const BlockMmArgs &a, Source &&sou
     }
 }
 
+// (four waves to a SIMD where the registers' limit would else leave three)
 template <class S, int JOB, int OUT, int QK>
-__global__ __launch_bounds__(S::THREADS, JOB == kJobGateUp || S::WN == 4 ? 4 : 1) void block_mm_small_kernel(const BlockMmArgs a)
+__global__ __launch_bounds__(S::THREADS, JOB == kJobGateUp || S::WN == 4 ? 4 : 1) void
+block_mm_small_kernel(const BlockMmArgs a)
 {
     __shared__ f32x4 part[S::WN][S::WK - 1][S::FN][64];
     extern __shared__ __attribute__((aligned(16))) char tok[];   // QK: the quantized rows
