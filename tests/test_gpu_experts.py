@@ -178,6 +178,21 @@ def test_experts(ops, dtype, t, e, top_k, k, inner):
     assert torch.equal(layer(x.to(DEV), ids.to(DEV), w.to(DEV)), y)
 
 
+@pytest.mark.parametrize("t,e,top_k,k,inner", [(48, 2, 1, 16, 16), (45, 3, 1, 128, 128), (90, 5, 2, 528, 208),
+                                               (60, 4, 2, 640, 1040), (50, 2, 1, 1168, 144), (100, 8, 4, 272, 528),
+                                               (64, 4, 1, 8208, 32), (30, 1, 1, 1040, 272), (130, 7, 2, 2064, 720)])
+def test_experts_of_a_few_dozen_rows(ops, t, e, top_k, k, inner):
+    parts, gv, dv = make(e, inner, k, t + 1)
+    layer = layer_of(parts)
+    for skew in (0.0, 1.5):
+        x = (rows(t, k, t + 1, torch.float32) * 0.3).to(torch.bfloat16)
+        ids, w = choose(t, e, top_k, 3, skew=skew)
+        exact, bound = ref.experts(ref.dequant(*ref.quant(x.float().numpy())), ids.numpy(), w.numpy(), gv, dv)
+        y = layer(x.to(DEV), ids.to(DEV), w.to(DEV))
+        check(y, exact, bound, torch.bfloat16, what=f"{t} {e} {skew}")
+        assert torch.equal(layer(x.to(DEV), ids.to(DEV), w.to(DEV)), y)
+
+
 @pytest.mark.parametrize("t,e,top_k,k,inner", [(1200, 36, 6, 784, 784), (1000, 32, 3, 784, 912),
                                                (1500, 64, 2, 1040, 784)])
 def test_experts_many_tiles(ops, t, e, top_k, k, inner):
