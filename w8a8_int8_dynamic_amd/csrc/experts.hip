@@ -219,6 +219,7 @@ struct Layout {
 // main kernel or of the small-M one (those of the up and the down products).
 struct Path {
     bool direct;
+    int bm;                      // rows of a tile, at most
     const BlockTileEntry *up, *down;
     bool small() const { return up->small; }
 };
@@ -226,17 +227,21 @@ struct Path {
 // The choice, by what each side took (us, the whole layer; A: 64 experts, K 4096,
 // inner 1024, 4 a token; B: 24, 2064, 720, 3; C: 8, 4096, 2048):
 //   small-M tiles up to 10 rows an expert, on average, then the main kernel's:
-//     A at 8 rows 155 against 183, at 16 rows 218 against 175; B 41 : 45, 49 : 45.
+//     A at 8 rows 155 against 183, at 16 rows 218 against 186; B 41 : 45, 49 : 49.
 //     Of those 16 x 128, but 16 x 32 where K is long and column tiles are few: A at
 //     4 slots 8 tokens 70 against 74, at 64 slots 104 : 101, B 41 : 47;
 //   its 128 x 256 tile up to 104 rows, then 256 x 256:
 //     A at 64 rows 192 : 200, at 96 210 : 221, at 112 243 : 228, at 256 404 : 376;
 //     B at 96 59 : 64, at 128 72 : 67 (64 x 256 tiles gained 2 % at most, below 32);
+//     of it, 64 rows at a time up to 32 rows, so that popular experts' gated
+//     products are exact too (main_fp8_block.hpp; 568 tokens, 1 of 23, K 144, inner
+//     736: 24.4 : 24.9). Beyond, the tiles more cost: 42 rows of uneven shares 55 :
+//     51, A at 48 rows 235 : 195;
 //   slots alone, without a plan, each with its expert's weights to itself, for up
 //   to four tokens and 24 slots, no more than there are experts (more would read
 //   weights twice): A, one token of 8 25.6 : 39.0, three of 8 56 : 63, eight of 1
 //   42.8 : 35.4; C, two of 8 58 : 48.
-constexpr int kSmallRows = 10, kHalfRows = 104, kDirectTokens = 4, kDirectSlots = 24;
+constexpr int kSmallRows = 10, kCutRows = 32, kHalfRows = 104, kDirectTokens = 4, kDirectSlots = 24;
 
 Path path_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
 {
@@ -244,6 +249,7 @@ Path path_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
     Path p{};
     if (rows > kSmallRows) {
         p.up = p.down = &fp8_block_main(rows > kHalfRows ? 0 : 1);
+        p.bm = rows > kCutRows ? p.up->bm : 64;
         return p;
     }
     p.direct = tokens <= kDirectTokens && slots <= std::min(kDirectSlots, experts) &&
@@ -254,6 +260,7 @@ Path path_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
     };
     p.up = small(K, fp8_block_frags(2 * inner, true));
     p.down = small(inner, fp8_block_frags(K, false));
+    p.bm = p.up->bm;
     return p;
 }
 
@@ -288,7 +295,7 @@ Layout layout_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inne
     l.xq = take(tokens * K);
     l.xs = take(tokens * scale_pitch(K) * 4);
     l.order = take(slots * 4);
-    l.tiles = take((most_tiles(slots, experts, p.up->bm) + 1) * (int64_t)sizeof(BlockTile));
+    l.tiles = take((most_tiles(slots, experts, p.bm) + 1) * (int64_t)sizeof(BlockTile));
     l.hq = take(slots * inner);
     l.hs = take(slots * scale_pitch(inner) * 4);
     l.y = take(slots * K * (small ? 4 : 2));
@@ -369,7 +376,7 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         float *ys = reinterpret_cast<float *>(work + l.ys);
         int *order = reinterpret_cast<int *>(work + l.order);
         BlockTile *tiles = reinterpret_cast<BlockTile *>(work + l.tiles);
-        const int bm = p.up->bm, tiles_m = (int)most_tiles(slots, args.experts, bm);
+        const int bm = p.bm, tiles_m = (int)most_tiles(slots, args.experts, bm);
         const int units = (int)(args.K / 8), padded = blocks * 16;
         const Cut c = cut_of(tokens, padded);
         const bool many = slots > kFewSlots;

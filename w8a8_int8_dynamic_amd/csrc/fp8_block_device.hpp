@@ -35,17 +35,20 @@ __device__ __forceinline__ v8bf widen(u32 lo, u32 hi)
 #endif
     return o;
 }
+// Eight k of a lane, part g of 4.
+__device__ __forceinline__ v8bf widen(const v4i (&v)[2], int g)
+{
+    return widen((u32)v[g >> 1][(g & 1) * 2], (u32)v[g >> 1][(g & 1) * 2 + 1]);
+}
 template <int FN>
 __device__ __forceinline__ void wide_products(const v4i (&w)[FN][2], const v4i (&x)[2], f32x4 (&p)[FN])
 {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        const v8bf xw = widen((u32)x[g >> 1][(g & 1) * 2], (u32)x[g >> 1][(g & 1) * 2 + 1]);
+        const v8bf xw = widen(x, g);
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-            p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                widen((u32)w[j][g >> 1][(g & 1) * 2], (u32)w[j][g >> 1][(g & 1) * 2 + 1]), xw,
-                g == 0 ? f32x4{} : p[j], 0, 0, 0);
+            p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w[j], g), xw, g == 0 ? f32x4{} : p[j], 0, 0, 0);
     }
 }
 

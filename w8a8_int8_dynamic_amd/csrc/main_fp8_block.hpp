@@ -35,7 +35,10 @@
 //     of a register for 64 blocks and read from there.
 // Experts: the token tiles of a run that is shorter than BM rows are not
 // computed (they alternate between the two waves of a SIMD, so that what is
-// left out is left out of both).
+// left out is left out of both). The 128-row tile's gated products of up to 64 rows,
+// whose time the loads take, are summed from bf16 values, for the reason in
+// small_fp8_block.hip (64 experts of 16 to 48 rows, K 4096, inner 1024 174-186 us from e4m3,
+// 180-195 so; 333 tokens, 3 of 24 50 and 51).
 // Measured, M8192 N4096 K12288: 344 us, 2.4 PFLOP/s, the matrix cores busy 66 %
 // of the cycles at 1.85 GHz: power bounds it (the same instructions from
 // registers alone, on random codes, hold 1.8 GHz). A form whose workgroups stay
@@ -277,6 +280,8 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES) void block_mm_kernel(const Bl
     auto loop = [&](auto live_c) __attribute__((always_inline)) {
         constexpr int LIVE = decltype(live_c)::value;
         static_assert(LIVE % 2 == 0, "products and scales alternate across steps too");
+        constexpr bool WIDE = JOB == kJobGateUp && TM == 4 && LIVE == 2;   // products from bf16 values
+        v8bf wide[WIDE ? TN : 1][4];
         float sc[2][2] = {};                              // scales of the products in p
 #pragma unroll
         for (int j = 0; j < TN; ++j)
@@ -338,9 +343,26 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES) void block_mm_kernel(const Bl
                 sc[i & 1][1] = TWO ? sx[i & 1] * sw[1] : 0.0f;
                 if constexpr (JOB == kJobDown)
                     bound[i] += __builtin_fabsf(sc[i & 1][0]);
+                if constexpr (WIDE) {
+                    if constexpr (i == 0)
+#pragma unroll
+                        for (int j = 0; j < TN; ++j)
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+                                wide[j][g] = widen(w[j], g);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const v8bf xw = widen(x[i & 1], g);
+#pragma unroll
+                        for (int j = 0; j < TN; ++j)
+                            p[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                wide[j][g], xw, g == 0 ? f32x4{} : p[i & 1][j], 0, 0, 0);
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
-                    p[i & 1][j] = block_product(w[j], x[i & 1]);
+                    if constexpr (!WIDE)
+                        p[i & 1][j] = block_product(w[j], x[i & 1]);
                     if constexpr (LAST)
                         read_w(stn, j);
                 }
@@ -348,7 +370,7 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES) void block_mm_kernel(const Bl
                 // Behind each MFMA the previous tile's multiply-adds (the first
                 // tile's: the last one's of the step before).
                 add(std::integral_constant<int, i == 0 ? LIVE - 1 : i - 1>{});
-                static_for<TN>([&](auto) __attribute__((always_inline)) {
+                static_for<WIDE ? 0 : TN>([&](auto) __attribute__((always_inline)) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);            // MFMA
                     __builtin_amdgcn_sched_group_barrier(0x020, PER, 0);          // VMEM read
                     __builtin_amdgcn_sched_group_barrier(0x100, LAST ? 2 : 1, 0); // DS read
