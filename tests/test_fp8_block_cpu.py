@@ -215,3 +215,38 @@ def test_refusals():
     for shape in ((), (1,), (17,), (1, 16)):
         with pytest.raises(ValueError, match="bias"):
             W8A8Linear(packed, torch.zeros(1, 1), 16, 64, torch.zeros(shape), "fp8_block")
+
+
+def overlapping_weights(k=48):
+    """Weights [N, K] and [E, N, K] whose rows lie anywhere but one pitch apart, by name."""
+    base = torch.arange(8 * 32 * k, dtype=torch.float32).remainder(251)
+    row = base[:k].view(1, k)
+    return {
+        "one row expanded": row.expand(32, k),
+        "one row expanded to experts": row.view(1, 1, k).expand(3, 32, k),
+        "one matrix expanded to experts": base[:32 * k].view(1, 32, k).expand(3, 32, k),
+        "an expert's row expanded": base[:3 * k].view(3, 1, k).expand(3, 32, k),
+        "sliding window": base.as_strided((32, k), (16, 1)),
+        "sliding windows of experts": base.as_strided((3, 32, k), (32 * 16, 16, 1)),
+        "experts of one row, overlapping": base.as_strided((3, 1, k), (16, 1, 1)),
+        "experts of one row, apart": base.as_strided((3, 1, k), (64, 7, 1)),
+        "experts of one row, the same": row.view(1, 1, k).expand(3, 1, k),
+        "one row": base.as_strided((1, k), (3, 1)),
+        "one expert": base.as_strided((1, 32, k), (5, k + 16, 1)),
+        "pitch": base.as_strided((32, k), (k + 16, 1)),
+        "pitch of experts": base.as_strided((3, 32, k), (32 * (k + 16), k + 16, 1)),
+        "gaps between experts": base.as_strided((3, 32, k), (32 * k + 16, k, 1)),
+        "columns": base[:32 * k].view(k, 32).t(),
+    }
+
+
+@pytest.mark.parametrize("name", list(overlapping_weights()))
+def test_weight_pitch(name):
+    """The pitch that a weight is handed over with leads to its own elements, inside its own memory."""
+    w = overlapping_weights()[name]
+    m, ld = ops._matrices(w)
+    n, k = w.shape[-2:]
+    rows = w.numel() // k
+    assert ld >= k and (rows - 1) * ld + k <= m.untyped_storage().nbytes() // 4 - m.storage_offset()
+    assert torch.equal(m.as_strided((rows, k), (ld, 1)), w.reshape(rows, k))
+    assert (m is w) == (name in ("one row", "one expert", "pitch", "pitch of experts", "experts of one row, apart"))

@@ -395,3 +395,23 @@ def test_python_refusals(ops):
         layer(torch.zeros(2, k, device=DEV))
     with pytest.raises(ValueError):
         layer(torch.zeros(2, k + 16, dtype=torch.bfloat16, device=DEV))
+
+
+def test_weights_of_any_strides(ops):
+    """Rows that are one row of memory, overlap, or lie further apart: packed as their contiguous copies are."""
+    from tests.test_fp8_block_cpu import overlapping_weights
+    for name, w in overlapping_weights().items():
+        print(name, flush=True)
+        full = w.contiguous().to(DEV)
+        for dtype in (torch.uint8, torch.float32, torch.bfloat16):
+            flat = torch.empty(0, dtype=torch.float32).set_(w.untyped_storage()).to(dtype).to(DEV)
+            view = flat.as_strided(w.shape, w.stride(), w.storage_offset())
+            assert torch.equal(view.float(), full)
+            for gated in (False, True) if w.shape[-2] == 32 else (False,):
+                if dtype == torch.uint8:
+                    assert torch.equal(ops.fp8_block_prepack_weight(view, gated),
+                                       ops.fp8_block_prepack_weight(full.to(dtype), gated))
+                else:
+                    got = ops.fp8_block_quant_prepack_weight(view, gated)
+                    want = ops.fp8_block_quant_prepack_weight(full.to(dtype), gated)
+                    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -798,9 +798,20 @@ def fp8_block_dequant(xq: torch.Tensor, xs: torch.Tensor, dtype: torch.dtype = t
     return out
 
 
-def _block_weights(w: torch.Tensor, name: str, gated: bool) -> Tuple[torch.Tensor, int, int, int]:
-    """(w, E, N, K) of a weight [N, K], or of experts' weights [E, N, K]; rows contiguous,
-    one matrix behind the other."""
+def _matrices(w: torch.Tensor) -> Tuple[torch.Tensor, int]:
+    """w [N, K] or [E, N, K] and the pitch of its rows, one matrix behind the other; a
+    copy where the strides are no such pitch, or rows overlap (those of an expanded
+    tensor are one row of memory)."""
+    N, K = w.shape[-2:]
+    E = w.shape[0] if w.dim() == 3 else 1
+    ld = w.stride(-2) if N > 1 else w.stride(0) if E > 1 else K
+    if w.stride(-1) != 1 or ld < K or (E > 1 and w.stride(0) != N * ld):
+        return w.clone(memory_format=torch.contiguous_format), K
+    return w, ld
+
+
+def _block_weights(w: torch.Tensor, name: str, gated: bool) -> Tuple[torch.Tensor, int, int, int, int]:
+    """(w, its row pitch, E, N, K) of a weight [N, K], or of experts' weights [E, N, K]."""
     if not w.is_cuda:
         raise ValueError(f"{name} must be a device tensor, got {w.device}")
     if w.dim() not in (2, 3):
@@ -811,9 +822,8 @@ def _block_weights(w: torch.Tensor, name: str, gated: bool) -> Tuple[torch.Tenso
     if N < 1 or E < 1 or (gated and N % 32 != 0):
         raise ValueError(f"{name}: no packed form of shape {tuple(w.shape)}"
                          f"{' (gated: N must be a multiple of 32)' if gated else ''}")
-    if w.stride(-1) != 1 or (w.dim() == 3 and w.stride(0) != N * w.stride(1)):
-        w = w.contiguous()
-    return w, E, N, K
+    w, ld = _matrices(w)
+    return w, ld, E, N, K
 
 
 def _block_packed(E: int, N: int, K: int, ref: torch.Tensor) -> torch.Tensor:
@@ -833,14 +843,10 @@ def fp8_block_prepack_weight(wq: torch.Tensor, gated: bool = False) -> torch.Ten
     as many up rows (the first weight of fp8_block_experts)."""
     if wq.dtype != torch.uint8:
         raise TypeError(f"wq must be torch.uint8, got {wq.dtype}")
-    wq, E, N, K = _block_weights(wq, "wq", gated)
+    wq, ld, E, N, K = _block_weights(wq, "wq", gated)
     packed = _block_packed(E, N, K, wq)
-    _run(wq, "fp8_block_prepack_weight", wq.data_ptr(), _row_pitch(wq), E, N, K, int(gated), packed.data_ptr())
+    _run(wq, "fp8_block_prepack_weight", wq.data_ptr(), ld, E, N, K, int(gated), packed.data_ptr())
     return packed
-
-
-def _row_pitch(w: torch.Tensor) -> int:
-    return max(w.stride(-2), w.shape[-1])
 
 
 def fp8_block_quant_prepack_weight(w: torch.Tensor, gated: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -849,14 +855,14 @@ def fp8_block_quant_prepack_weight(w: torch.Tensor, gated: bool = False) -> Tupl
     expert, and of a gated weight [2*ceil(N/2/128), ceil(K/128)])."""
     if w.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"w must be bfloat16 or float32, got {w.dtype}")
-    w, E, N, K = _block_weights(w, "w", gated)
+    w, ld, E, N, K = _block_weights(w, "w", gated)
     f32 = w.dtype == torch.float32
-    if w.data_ptr() % 16 != 0 or _row_pitch(w) % (4 if f32 else 8) != 0:
-        w = w.clone(memory_format=torch.contiguous_format)
+    if w.data_ptr() % 16 != 0 or ld % (4 if f32 else 8) != 0:
+        w, ld = w.clone(memory_format=torch.contiguous_format), K
     packed = _block_packed(E, N, K, w)
     shape = (_block_scale_rows(N, gated), _blocks_of(K))
     ws = w.new_empty(shape if w.dim() == 2 else (E, *shape), dtype=torch.float32)
-    _run(w, "fp8_block_quant_prepack_weight", w.data_ptr(), 0 if f32 else 1, _row_pitch(w), E, N, K, int(gated),
+    _run(w, "fp8_block_quant_prepack_weight", w.data_ptr(), 0 if f32 else 1, ld, E, N, K, int(gated),
          packed.data_ptr(), ws.data_ptr())
     return packed, ws
 
