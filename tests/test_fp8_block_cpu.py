@@ -250,3 +250,26 @@ def test_weight_pitch(name):
     assert ld >= k and (rows - 1) * ld + k <= m.untyped_storage().nbytes() // 4 - m.storage_offset()
     assert torch.equal(m.as_strided((rows, k), (ld, 1)), w.reshape(rows, k))
     assert (m is w) == (name in ("one row", "one expert", "pitch", "pitch of experts", "experts of one row, apart"))
+
+
+def overlapping_logits(e=24):
+    """Logits [8, e] whose rows are one row of memory, overlap, or lie further apart, by name."""
+    base = torch.randn(8 * 64, generator=torch.Generator().manual_seed(5))
+    return {"expanded": base[:e].expand(8, e), "overlapping": base.as_strided((8, e), (e - 1, 1)),
+            "pitch": base.as_strided((8, e), (e + 8, 1)), "contiguous": base[:8 * e].view(8, e),
+            "one": base.as_strided((1, e), (3, 1)), "one expert": base[:1].expand(8, 1),
+            "one expert, apart": base.as_strided((8, 1), (5, 7))}
+
+
+@pytest.mark.parametrize("name", list(overlapping_logits()))
+def test_logits_pitch(name, monkeypatch):
+    """The pitch that logits are handed over with leads to their own elements, inside their own memory."""
+    x = overlapping_logits()[name]
+    calls = []
+    monkeypatch.setattr(ops, "_float_rows", lambda t, _: (1, *t.shape, t.stride(0) if t.shape[0] > 1 else t.shape[1]))
+    monkeypatch.setattr(ops, "_run", lambda t, entry, at, kind, ld, *rest: calls.append((t, entry, at, ld)))
+    ops.route_experts(x, ops.Routing(1))
+    (t, entry, at, ld), = calls
+    assert entry == "route_experts" and at == t.data_ptr() and ld >= x.shape[1]
+    assert (t.shape[0] - 1) * ld + t.shape[1] <= t.untyped_storage().nbytes() // 4 - t.storage_offset()
+    assert torch.equal(t.as_strided(t.shape, (ld, 1)), x)

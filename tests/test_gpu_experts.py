@@ -501,3 +501,16 @@ def test_python_refusals(ops):
         layer_of([parts[0][:, :-16], parts[1], parts[2], parts[3]])
     with pytest.raises(ValueError):
         layer_of([parts[0], parts[1][:, :-1], parts[2], parts[3]])
+
+
+def test_route_logits_of_any_strides(ops):
+    """Rows that are one row of memory, overlap, or lie further apart are routed as their contiguous copies are."""
+    from tests.test_fp8_block_cpu import overlapping_logits
+    for name, x in overlapping_logits().items():
+        print(name, flush=True)
+        flat = torch.empty(0).set_(x.untyped_storage()).to(DEV)
+        view = flat.as_strided(x.shape, x.stride(), x.storage_offset())
+        for score in ("softmax", "sigmoid"):
+            how = ops.Routing(min(4, x.shape[1]), score)
+            got, want = ops.route_experts(view, how), ops.route_experts(x.contiguous().to(DEV), how)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), name

@@ -1008,11 +1008,13 @@ def route_experts(logits: torch.Tensor, routing: Routing) -> Tuple[torch.Tensor,
         raise ValueError(f"bias must be contiguous fp32 [{E}] on {logits.device}")
     if r.top_k < 1:
         raise ValueError(f"top_k must be at least 1, got {r.top_k}")
+    if ld < E:                                         # rows overlap, as those of an expanded tensor do
+        logits, ld = logits.contiguous(), E
     ids = logits.new_empty((T, r.top_k), dtype=torch.int32)
     weights = logits.new_empty((T, r.top_k), dtype=torch.float32)
     how = _lib.ROUTING_STRUCT.pack(0 if bias is None else bias.data_ptr(), score, r.top_k, r.groups, r.top_groups,
                                    r.group_top, int(r.renormalize), r.scale)
-    _run(logits, "route_experts", logits.data_ptr(), t, max(ld, E), T, E, how, ids.data_ptr(), weights.data_ptr())
+    _run(logits, "route_experts", logits.data_ptr(), t, ld, T, E, how, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
