@@ -514,3 +514,31 @@ def test_route_logits_of_any_strides(ops):
             how = ops.Routing(min(4, x.shape[1]), score)
             got, want = ops.route_experts(view, how), ops.route_experts(x.contiguous().to(DEV), how)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), name
+
+
+# Rows an expert on average, of each path but the slots alone: small tiles, rows cut at 64, 128-row and 256-row
+# tiles; of uneven shares, so that tiles of every fill are met.
+@pytest.mark.parametrize("rows_each", [6, 10, 11, 24, 32, 33, 40, 70, 100, 104, 105, 150])
+def test_experts_rows_whatever_their_place(ops, rows_each):
+    """A token's result depends neither on its place among its expert's rows nor on how many others the expert
+    has, on every path: all tokens in other orders, and with the other half of the tokens elsewhere."""
+    e, top_k, k, inner = 6, 2, 656, 272
+    t = rows_each * e // top_k
+    parts, _, _ = make(e, inner, k, 31)
+    layer = layer_of(parts)
+    x = (rows(t, k, 2, torch.float32) * 0.3).to(torch.bfloat16).to(DEV)
+    ids, w = (v.to(DEV) for v in choose(t, e, top_k, 5, skew=0.7))
+    counts = torch.bincount(ids.flatten().long().cpu(), minlength=e).tolist()
+    print(counts, flush=True)
+    want = layer(x, ids, w)
+    g = torch.Generator().manual_seed(3)
+    for _ in range(4):
+        perm = torch.randperm(t, generator=g).to(DEV)
+        assert torch.equal(layer(x[perm], ids[perm], w[perm]), want[perm])
+    half = torch.arange(t, device=DEV) % 2 == 0
+    for turn in range(1, e):
+        other = torch.where(half.unsqueeze(1), ids, (ids + turn) % e)
+        assert torch.equal(layer(x, other, w)[half], want[half])
+    none = torch.where(half.unsqueeze(1), ids, -1)
+    got = layer(x, none, w)
+    assert torch.equal(got[half], want[half]) and (got[~half] == 0).all()

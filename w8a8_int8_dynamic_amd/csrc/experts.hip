@@ -221,6 +221,7 @@ struct Path {
     bool direct;
     int bm;                      // rows of a tile, at most
     const BlockTileEntry *up, *down;
+    BlockMmKernel gate_up;
     bool small() const { return up->small; }
 };
 
@@ -233,15 +234,15 @@ struct Path {
 //   its 128 x 256 tile up to 104 rows, then 256 x 256:
 //     A at 64 rows 192 : 200, at 96 210 : 221, at 112 243 : 228, at 256 404 : 376;
 //     B at 96 59 : 64, at 128 72 : 67 (64 x 256 tiles gained 2 % at most, below 32);
-//     of it, 64 rows at a time up to 32 rows, so that popular experts' gated
-//     products are exact too (main_fp8_block.hpp; 568 tokens, 1 of 23, K 144, inner
-//     736: 24.4 : 24.9). Beyond, the tiles more cost: 42 rows of uneven shares 55 :
-//     51, A at 48 rows 235 : 195;
+//     of it, kCutRows rows at a time and with exact gated products (main_fp8_block.hpp) up to
+//     32 rows. Against whole tiles of e4m3 products that costs, at 24 rows of uneven
+//     shares, B 50 : 47, A 222 : 184, C 69 : 62; exact whole tiles would at 41 rows, B 58
+//     : 51, A 252 : 215, C 84 : 65, and at 64, B 65 : 56, A 278 : 225, C 86 : 67;
 //   slots alone, without a plan, each with its expert's weights to itself, for up
 //   to four tokens and 24 slots, no more than there are experts (more would read
 //   weights twice): A, one token of 8 25.6 : 39.0, three of 8 56 : 63, eight of 1
 //   42.8 : 35.4; C, two of 8 58 : 48.
-constexpr int kSmallRows = 10, kCutRows = 32, kHalfRows = 104, kDirectTokens = 4, kDirectSlots = 24;
+constexpr int kSmallRows = 10, kExactRows = 32, kHalfRows = 104, kDirectTokens = 4, kDirectSlots = 24;
 
 Path path_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
 {
@@ -249,7 +250,9 @@ Path path_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
     Path p{};
     if (rows > kSmallRows) {
         p.up = p.down = &fp8_block_main(rows > kHalfRows ? 0 : 1);
-        p.bm = rows > kCutRows ? p.up->bm : 64;
+        const bool cut = rows <= kExactRows;
+        p.bm = cut ? kCutRows : p.up->bm;
+        p.gate_up = cut ? p.up->gate_up_cut : p.up->gate_up;
         return p;
     }
     p.direct = tokens <= kDirectTokens && slots <= std::min(kDirectSlots, experts) &&
@@ -261,6 +264,7 @@ Path path_of(int64_t tokens, int top_k, int experts, int64_t K, int64_t inner)
     p.up = small(K, fp8_block_frags(2 * inner, true));
     p.down = small(inner, fp8_block_frags(K, false));
     p.bm = p.up->bm;
+    p.gate_up = p.up->gate_up;
     return p;
 }
 
@@ -397,7 +401,7 @@ hipError_t launch_experts(const ExpertsArgs &args, void *workspace, hipStream_t 
         up.out = p.small() ? static_cast<void *>(work + l.h) : hq;
         up.out_scale = hs;
         up.ld_out_scale = scale_pitch(args.inner);
-        hipLaunchKernelGGL(p.up->gate_up, dim3((unsigned)grid_of(*p.up, tiles_m, up.frags)), dim3(p.up->threads), 0,
+        hipLaunchKernelGGL(p.gate_up, dim3((unsigned)grid_of(*p.up, tiles_m, up.frags)), dim3(p.up->threads), 0,
                            stream, up);
         if (p.small()) {
             err = launch_quant_fp8_block(work + l.h, kElemF32, slots, args.inner, args.inner, hq, args.inner, hs,

@@ -87,8 +87,10 @@ struct BlockTileEntry {
     const char *name;
     int bm, bn, threads;
     bool small;
-    BlockMmKernel dense[kOutKinds], gate_up, down;
+    BlockMmKernel dense[kOutKinds], gate_up, down, gate_up_cut;
 };
+// Rows of a tile of gate_up_cut's launches, at most.
+constexpr int kCutRows = 64;
 constexpr int kBlockMainTiles = 6, kBlockSmallTiles = 3;
 const BlockTileEntry &fp8_block_main(int i);
 const BlockTileEntry &fp8_block_small(int i);

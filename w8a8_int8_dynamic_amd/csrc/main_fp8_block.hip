@@ -15,6 +15,16 @@ constexpr BlockMmKernel gate_up()
         return nullptr;
 }
 
+// The same of tiles of at most kCutRows rows, exact.
+template <class T>
+constexpr BlockMmKernel gate_up_cut()
+{
+    if constexpr (T::BN == 256 && T::BM == 128)
+        return block_mm_kernel<T, kJobGateUp, kOutI32, true>;
+    else
+        return nullptr;
+}
+
 template <class T>
 constexpr BlockMmKernel down()
 {
@@ -30,7 +40,7 @@ constexpr BlockTileEntry entry(const char *name)
     return BlockTileEntry{name, T::BM, T::BN, T::THREADS, false,
                           {block_mm_kernel<T, kJobDense, kOutBF16>, block_mm_kernel<T, kJobDense, kOutI32>,
                            block_mm_kernel<T, kJobDense, kOutF16>},
-                          gate_up<T>(), down<T>()};
+                          gate_up<T>(), down<T>(), gate_up_cut<T>()};
 }
 
 // token rows x channels / wave rows and columns / LDS stages

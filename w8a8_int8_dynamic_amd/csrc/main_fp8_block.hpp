@@ -35,10 +35,14 @@
 //     of a register for 64 blocks and read from there.
 // Experts: the token tiles of a run that is shorter than BM rows are not
 // computed (they alternate between the two waves of a SIMD, so that what is
-// left out is left out of both). The 128-row tile's gated products of up to 64 rows,
-// whose time the loads take, are summed from bf16 values, for the reason in
-// small_fp8_block.hip (64 experts of 16 to 48 rows, K 4096, inner 1024 174-186 us from e4m3,
-// 180-195 so; 333 tokens, 3 of 24 50 and 51).
+// left out is left out of both). Launches whose rows are cut at 64 sum gated
+// products from bf16 values, for the reason in small_fp8_block.hip; that is the
+// launch's choice, so that a row's result hangs neither on the rows beside it nor
+// on its place among them. Outputs of bf16 are then off 64 bits by 1.67e-3 of their
+// norm, of which bf16's own rounding is 1.66e-3, and 1.8-2.8e-3 from e4m3 (ten inputs
+// each of 333 tokens, 3 of 24, and of 60 rows an expert). The matrix cores take twice
+// the time and every wave converts both operands; what that costs a layer stands with
+// the thresholds (experts.hip).
 // Measured, M8192 N4096 K12288: 344 us, 2.4 PFLOP/s, the matrix cores busy 66 %
 // of the cycles at 1.85 GHz: power bounds it (the same instructions from
 // registers alone, on random codes, hold 1.8 GHz). A form whose workgroups stay
@@ -111,7 +115,9 @@ __device__ __forceinline__ void expert_tile_of(int pid, int tiles_n, int &tm, in
     tn = group % across * columns + within / kExpertGroupM;
 }
 
-template <class T, int JOB, int OUT>
+// WIDE: gated products from bf16 values, exact, of a launch whose tiles hold at
+// most kCutRows rows.
+template <class T, int JOB, int OUT, bool WIDE = false>
 __global__ __launch_bounds__(T::THREADS, T::WAVES) void block_mm_kernel(const BlockMmArgs args)
 {
     __shared__ uint4 lds[T::LDS / 16];
@@ -280,7 +286,6 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES) void block_mm_kernel(const Bl
     auto loop = [&](auto live_c) __attribute__((always_inline)) {
         constexpr int LIVE = decltype(live_c)::value;
         static_assert(LIVE % 2 == 0, "products and scales alternate across steps too");
-        constexpr bool WIDE = JOB == kJobGateUp && TM == 4 && LIVE == 2;   // products from bf16 values
         v8bf wide[WIDE ? TN : 1][4];
         float sc[2][2] = {};                              // scales of the products in p
 #pragma unroll
@@ -389,10 +394,11 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES) void block_mm_kernel(const Bl
         // on. Computed in whole quarters of the wave's tiles, each with a loop
         // of its own.
         constexpr int Q = TM >= 8 ? TM / 4 : 2;
+        static_assert(!WIDE || (JOB == kJobGateUp && kCutRows == 16 * T::WM * Q), "a cut tile's rows are one loop's");
         const int live = ((rows + 15) / 16 - wm + T::WM - 1) / T::WM;
-        static_for<TM / Q>([&](auto I) __attribute__((always_inline)) {
+        static_for<WIDE ? 1 : TM / Q>([&](auto I) __attribute__((always_inline)) {
             constexpr int n = decltype(I)::value;
-            if (n == 0 ? live <= Q : live > n * Q && live <= (n + 1) * Q)
+            if (n == 0 ? WIDE || live <= Q : live > n * Q && live <= (n + 1) * Q)
                 loop(std::integral_constant<int, (n + 1) * Q>{});
         });
     }

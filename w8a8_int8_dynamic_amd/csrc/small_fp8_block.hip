@@ -28,8 +28,8 @@
 //     error: an inner element near the border of two codes falls to either side by
 //     it, a step of 2^-3. The matrix cores wait for the weights anyway (48 tokens
 //     as above 144 us from e4m3, 146 so; outputs 1.6-2.8e-3 of their norm from the
-//     elementwise form's, and 4e-4 so). The main kernel keeps e4m3 in tiles of
-//     more than 64 rows, which compute the time they take: 80 rows lost 20 % by it.
+//     elementwise form's, and 4e-4 so). The main kernel does so
+//     in launches of few rows an expert, and keeps e4m3 in the others (experts.hip).
 //   - QK: the rows come as floats. Every workgroup quantizes them into LDS
 //     while its first weights are on their way, 8 elements a thread at a time
 //     (they are few and sit in L2); the workgroups of the first channels write
