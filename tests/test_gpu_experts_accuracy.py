@@ -39,6 +39,35 @@ def outputs(ops, layer, x, ids, w):
     return f.double().cpu().numpy()
 
 
+def values(kind, n, k, r):
+    """Codes of rows that are random codes, normal values, or normal values with some columns 20 times as large."""
+    if kind == "codes":
+        q = r.integers(0, 256, (n, k), dtype=np.uint8)
+        return np.where((q & 127) == 127, q ^ 1, q).astype(np.uint8)
+    return ref.quant(r.standard_normal((n, k)) * np.where(r.random(k) < (0.02 if kind == "outliers" else 0), 20, 1))[0]
+
+
+@pytest.mark.parametrize("kind", ["codes", "normal", "outliers"])
+def test_instruction(ops, kind):
+    """Sums of every tile are the instruction's as tests/experts_reference.py follows it, to fp32's rounding
+    of their 16 groups a block, the blocks and the scales' products; and so far from exact ones as csrc/
+    fp8_block_device.hpp says."""
+    m, n, k = 70, 144, 656
+    r = np.random.default_rng(9)
+    xq, wq = values(kind, m, k, r), values("codes" if kind == "codes" else "normal", n, k, r)
+    xs = (2.0 ** r.uniform(-9, -5, (m, ref.blocks_of(k)))).astype(np.float32)
+    ws = (2.0 ** r.uniform(-12, -8, (ref.blocks_of(n), ref.blocks_of(k)))).astype(np.float32)
+    want, x, w = tight.instruction_product(xq, xs, wq, ws, DEV), ref.dequant(xq, xs), ref.weight(wq, ws)
+    bound = (16 + ref.blocks_of(k) + 4) * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)
+    packed = ops.fp8_block_prepack_weight(dev(wq))
+    for tile in range(ops.fp8_block_tile_count()):
+        y = ops.fp8_block_scaled_mm(dev(xq), dev(xs), packed, dev(ws), n, out_dtype=torch.float32, tile=tile)
+        assert (np.abs(y.double().cpu().numpy() - want) <= bound).all(), ops.fp8_block_tile_name(tile)
+    off = np.sqrt(np.mean((want - x @ w.T) ** 2 / ((x ** 2) @ (w ** 2).T)))
+    print(f"{kind}: {off:.2g} of the sums' rms", flush=True)
+    assert off < 2.0 ** -13
+
+
 def held(y, x, ids, w, parts, exact):
     """Outputs y are near enough to the definition, in norm and elementwise."""
     want, bound = tight.experts(x.float().numpy(), ids, w, parts, exact, device=DEV)
