@@ -273,3 +273,12 @@ def test_logits_pitch(name, monkeypatch):
     assert entry == "route_experts" and at == t.data_ptr() and ld >= x.shape[1]
     assert (t.shape[0] - 1) * ld + t.shape[1] <= t.untyped_storage().nbytes() // 4 - t.storage_offset()
     assert torch.equal(t.as_strided(t.shape, (ld, 1)), x)
+
+
+def test_routing_divides_by_a_product():
+    """csrc/routing.hip's group of an expert, expert * ceil(2^20 / size) >> 20, is expert / size for every size of a
+    group and every expert that a lane may hold."""
+    expert = np.arange(1024, dtype=np.uint32)
+    for size in range(1, 1025):
+        inverse = np.uint32(((1 << 20) + size - 1) // size)
+        assert np.array_equal((expert * inverse) >> np.uint32(20), expert // size), size

@@ -327,7 +327,8 @@ hipError_t launch_route(const RouteArgs &args, hipStream_t stream)
     // Lanes of a group: a power of two, at most a row of 16, and all groups' within the token's.
     for (a.group_lanes = 16; a.group_lanes * a.groups > k.lanes; a.group_lanes /= 2)
         ;
-    // expert / size for experts below 1024: the product's error is below expert * size / 2^20 < 1 / size
+    // expert / size for experts below 1024: size_inverse is less than 1 above 2^20 / size, so the quotient is
+    // less than expert / 2^20 too large, which is below 1 / size (expert * size < 2^20): it reaches no next whole.
     const int size = a.experts / a.groups;
     a.size_inverse = ((1u << 20) + size - 1) / size;
     const size_t lds = a.groups > 1 ? (size_t)tokens * (a.experts + a.groups) * 8 : 0;
