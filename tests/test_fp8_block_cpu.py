@@ -282,3 +282,16 @@ def test_routing_divides_by_a_product():
     for size in range(1, 1025):
         inverse = np.uint32(((1 << 20) + size - 1) // size)
         assert np.array_equal((expert * inverse) >> np.uint32(20), expert // size), size
+
+
+def test_block_scales_are_checked_as_fp32():
+    from w8a8_int8_dynamic_amd.linear import _block_scales
+    for bad in (torch.full((1, 2), 1e39, dtype=torch.float64), torch.full((1, 2), float("nan")),
+                torch.full((1, 2), float("inf"), dtype=torch.bfloat16)):
+        with pytest.raises(ValueError, match="finite"):
+            _block_scales(bad, (1, 2))
+    with pytest.raises(ValueError, match="shape"):
+        _block_scales(torch.ones(2, 1), (1, 2))
+    for dtype in (torch.float64, torch.bfloat16):
+        ws = _block_scales(torch.full((2, 3), 0.5, dtype=dtype).t(), (3, 2))
+        assert ws.dtype == torch.float32 and ws.is_contiguous() and (ws == 0.5).all()

@@ -27,9 +27,10 @@ def _block_scales(ws: torch.Tensor, shape: Sequence[int]) -> torch.Tensor:
     """Block scales [*shape] as contiguous fp32, checked."""
     if ws.shape != tuple(shape):
         raise ValueError(f"weight scales must have shape {tuple(shape)}, got {tuple(ws.shape)}")
-    if not torch.isfinite(ws).all():
+    ws = ws.to(torch.float32).contiguous()
+    if not torch.isfinite(ws).all():                   # (fp64 scales may lie past fp32's range)
         raise ValueError("weight scales must be finite")
-    return ws.to(torch.float32).contiguous()
+    return ws
 
 
 class W8A8Linear(torch.nn.Module):
