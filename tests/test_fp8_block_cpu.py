@@ -295,3 +295,25 @@ def test_block_scales_are_checked_as_fp32():
     for dtype in (torch.float64, torch.bfloat16):
         ws = _block_scales(torch.full((2, 3), 0.5, dtype=dtype).t(), (3, 2))
         assert ws.dtype == torch.float32 and ws.is_contiguous() and (ws == 0.5).all()
+
+
+def test_experts_forward_takes_ids_of_its_tokens(monkeypatch):
+    """ids and weights stand beside x's leading dimensions, or are of the flattened tokens; others are
+    refused, also where they hold as many tokens."""
+    got = []
+    monkeypatch.setattr(ops, "fp8_block_experts", lambda x, ids, w, *_: got.append((ids, w)) or x)
+    part = torch.zeros(1)
+    layer = W8A8Experts(part, torch.zeros(4, 1, 1), part, part, 16, 48)
+    x = torch.zeros(2, 3, 48, dtype=torch.bfloat16)
+    ids = torch.arange(12, dtype=torch.int32).view(2, 3, 2)
+    w = ids.float()
+    for i, v in ((ids, w), (ids.view(6, 2), w.view(6, 2))):
+        assert layer(x, i, v).shape == x.shape
+        assert torch.equal(got[-1][0], ids.view(6, 2)) and torch.equal(got[-1][1], w.view(6, 2))
+    assert layer(x[0, 0], ids[0, 0], w[0, 0]).shape == (48,) and got[-1][0].shape == (1, 2)
+    before = len(got)
+    for i, v in ((ids.view(3, 2, 2), w.view(3, 2, 2)), (ids, w.view(3, 2, 2)), (ids, w.view(6, 2)),
+                 (ids.view(1, 6, 2), w.view(1, 6, 2)), (ids.flatten(), w.flatten())):
+        with pytest.raises(ValueError, match="ids and weights"):
+            layer(x, i, v)
+    assert len(got) == before

@@ -79,8 +79,8 @@ class W8A8Experts(torch.nn.Module):
         return cls(*quant(gate_up, True), *quant(down, False), inner, K, routing)
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor) -> torch.Tensor:
-        """x [..., K] (bf16 or fp16), ids int32 and weights fp32 [..., top_k] (an id outside
-        [0, E) stands for no expert) -> [..., K] in x's type."""
+        """x [..., K] (bf16 or fp16), ids int32 and weights fp32 [..., top_k], or of the flattened
+        tokens [T, top_k] (an id outside [0, E) stands for no expert) -> [..., K] in x's type."""
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
         if x.dtype != torch.bfloat16 and x.dtype != torch.float16:
@@ -90,6 +90,9 @@ class W8A8Experts(torch.nn.Module):
         if x2.stride(-1) != 1:
             x2 = x2.contiguous()
         if not flat:
+            if ids.shape != weights.shape or (ids.shape[:-1] != x.shape[:-1] and ids.dim() != 2):
+                raise ValueError(f"ids and weights must be [..., top_k] beside x {tuple(x.shape)}, got "
+                                 f"{tuple(ids.shape)} and {tuple(weights.shape)}")
             ids, weights = ids.reshape(-1, ids.shape[-1]), weights.reshape(-1, weights.shape[-1])
         y = ops.fp8_block_experts(x2, ids, weights, self.gate_up, self.gate_up_scale, self.down, self.down_scale,
                                   self.inner)
