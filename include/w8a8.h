@@ -704,15 +704,17 @@ typedef struct w8a8_experts {
  *   h_j = silu(gate_e x) * (up_e x)   in fp32, silu(v) = v / (1 + e^-v)
  *   out_t = sum over j of w_j * down_e q(h_j)   in fp32, rounded once
  * where x and h pass through fp8_quant_per_block's codes. x [tokens, ldx] and
- * out [tokens, ldo] in x_dtype; ids and weights [tokens, top_k]. With more
- * than 10 slots (tokens times top_k) an expert, the products down_e q(h_j) wait
- * for the sum as fp16 under a power of two per 128 columns (2^-11 of their
- * value at most, or 2^-38 of what the scales bound them by), otherwise in fp32.
- * With more than 32 slots an expert, the gated products are summed by the e4m3
- * matrix instruction, as fp8_block_scaled_mm's are, otherwise from exact products
- * in fp32. The sizes alone decide between such forms: a token's result depends on
- * the number of tokens, but not on what the others hold or choose, nor on its
- * place among them.
+ * out [tokens, ldo] in x_dtype; ids and weights [tokens, top_k].
+ * Two forms hang on n, the slots (tokens times top_k) over the experts, rounded
+ * down (slots without an expert count; more than 65536 slots, or 2^30 elements of
+ * x, go in passes of as many, and n is a pass's):
+ *   n > 10: the products down_e q(h_j) wait for the sum as fp16 under a power of
+ *     two per 128 columns (2^-11 of their value at most, or 2^-38 of what the
+ *     scales bound them by), otherwise in fp32;
+ *   n > 32: the gated products are summed by the e4m3 matrix instruction, as
+ *     fp8_block_scaled_mm's are, otherwise from exact products in fp32.
+ * So a token's result depends on how many tokens there are, but not on what the
+ * others hold or choose, nor on its place among them.
  * Requirements: tokens >= 0 (0 is a no-op); K and inner multiples of 16 in
  * [16, W8A8_MAX_K]; top_k 1 .. 64; rows of x and out 16-byte aligned (ld a
  * multiple of 8, of 4 for fp32); the workspace 256-byte aligned and as long as

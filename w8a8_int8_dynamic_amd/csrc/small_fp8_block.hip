@@ -21,7 +21,9 @@
 //     tokens 51.6 and 48.9, 256 234 and 218).
 //   - NT: weights that one row tile reads pass the caches by (M1 N12288 K4096:
 //     11.7 us without, 10.3 so, 4.9 TB/s; below 16 MB, which the caches may
-//     hold, 4.6 without and 5.0 so).
+//     hold, 4.6 without and 5.0 so). Experts' tiles always do: an expert with several
+//     row tiles has them side by side on one XCD, which read its weights together
+//     (64 experts, K 4096, inner 1024, 160 tokens of 4: 166 us spread, 95 all to four).
 //     Experts, 48 tokens to 8 of 64, K 4096, inner 1024: gated products 84 us, 6.4
 //     TB/s, down 44 us, 6.1.
 //   - Gated products are summed from bf16 values, without the e4m3 instruction's
