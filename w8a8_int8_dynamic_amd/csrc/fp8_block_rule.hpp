@@ -5,9 +5,9 @@
 //   else scale = fl32(a/448), q = e4m3(clamp(fl32(x * f), +-448)),
 //        f = fl32(448 * fl32(1/a))
 // (quant_rule.hpp's e4m3 rule with a block in place of a row, and the factor by
-// way of the reciprocal, as it is commonly written: f differs from fl32(448/a) in
-// its last bit for some a, which moves elements that lie halfway between two
-// codes). A block that holds an infinity or NaN gets a scale that is not finite.
+// way of the reciprocal, as tensor libraries compute a constant over a tensor: f
+// differs from fl32(448/a) in its last bit for some a, which moves elements that
+// lie halfway between two codes). A block that holds an infinity or NaN gets a scale that is not finite.
 //
 // Packed weights: fragment F[nb][kb] (kb fastest) is 16 channels x 128 k, 2048
 // bytes; unit 16*c + r (16 bytes) holds k 128*kb + 16*c .. +15 of channel 16*nb
