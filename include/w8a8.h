@@ -566,7 +566,7 @@ int w8a8_fp4_tile_auto(int64_t M, int64_t N, int64_t K);
  * and scales x_scale [M, lds] (ceil(K/128) a row). A block that holds an
  * infinity or NaN gets a scale that is not finite.
  * fp8_block_dequant - codes and scales back to the values they stand for,
- * code * scale rounded once to out_dtype.
+ * code * scale in fp32, rounded to out_dtype.
  * Requirements: M >= 0 (0 is a no-op); rows of x and out 16-byte aligned (ld
  * a multiple of 8, of 4 for fp32); codes 8-byte aligned, ldq a multiple of 8.
  */

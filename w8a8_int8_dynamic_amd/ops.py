@@ -784,7 +784,7 @@ def fp8_quant_per_block(x: torch.Tensor, xq: Optional[torch.Tensor] = None,
 
 
 def fp8_block_dequant(xq: torch.Tensor, xs: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
-    """The values [M, K] that e4m3 codes and block scales stand for, rounded once to dtype."""
+    """The values [M, K] that e4m3 codes and block scales stand for: code * scale in fp32, rounded to dtype."""
     if dtype not in _DTYPE:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
     M, K = _block_rows(xq, xs)
