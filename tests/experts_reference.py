@@ -147,7 +147,9 @@ def crossings(g, u, dg, du):
     errors of standard deviations dg and du: the mean error (0.8 of its standard deviation, which holds the
     sums', the block maximum's and the fp32 steps' shares) over the codes' distance."""
     h = ref.silu(g) * u
-    slope = (1 + np.exp(-g) * (1 + g)) / (1 + np.exp(-g)) ** 2
+    with np.errstate(over="ignore"):
+        part = 1 / (1 + np.exp(-g))
+    slope = part * (1 + g * (1 - part))
     off = np.sqrt((slope * u * dg) ** 2 + (ref.silu(g) * du) ** 2 + (h * 2.0 ** -22) ** 2)
     b, o = ref._blocked(h), ref._blocked(off)
     top = np.abs(b).argmax(-1)[..., None]
