@@ -58,6 +58,9 @@ CASES = {
     "a hundred rows": (300, 9, 3, 400, 272),
     "many rows": (400, 6, 2, 656, 272),                    # 256-row tiles
     "long rows, many": (260, 2, 1, 2064, 272),
+    "1024 experts": (300, 1024, 6, 256, 48),
+    "64 choices, few rows": (10, 70, 64, 272, 80),
+    "64 choices": (150, 70, 64, 144, 48),
 }
 
 

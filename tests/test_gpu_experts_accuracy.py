@@ -9,7 +9,7 @@ import torch
 
 from tests import block_reference as ref
 from tests import experts_reference as tight
-from tests.test_experts_accuracy_cpu import CASES, INNER_CASES, case_of, inner_case_of
+from tests.test_experts_accuracy_cpu import CASES, INNER_CASES, case_of, inner_case_of, make, rows
 from tests.test_gpu_fp8_block import DEV, dev
 
 pytestmark = pytest.mark.gpu
@@ -169,3 +169,21 @@ def test_outputs_of_concentrated_choices(ops, t, skew):
     layer = layer_of(parts)
     for i in (ids, np.zeros_like(ids), np.full_like(ids, e - 1)):
         held(outputs(ops, layer, x, i, w), x, i, w, parts, True)
+
+
+@pytest.mark.parametrize("t", [1, 300, 5000, 9000, 30000])
+def test_outputs_of_weights_past_32_bits(ops, t):
+    """All tokens to the last of 264 experts, whose weights end past 4 GiB, on each path; three tokens' outputs."""
+    from w8a8_int8_dynamic_amd import W8A8Experts
+    e, k, inner = 264, 4096, 2048
+    r = np.random.default_rng(t)
+    one = make(1, inner, k, r)
+    parts = [torch.zeros(e, *p.shape[1:], dtype=torch.from_numpy(p).dtype, device=DEV) for p in one]
+    for p, last in zip(parts, one):
+        p[-1] = dev(last[0])
+    layer = W8A8Experts.from_quantized(*parts)
+    assert layer.gate_up.numel() > 2 ** 32
+    x = torch.from_numpy(rows(t, k, r).astype(np.float32)).to(torch.bfloat16)
+    y = outputs(ops, layer, x, np.full((t, 1), e - 1, np.int32), np.ones((t, 1), np.float32))
+    some = [0, t // 2, t - 1]
+    held(y[some], x[some], np.zeros((3, 1), np.int32), np.ones((3, 1), np.float32), one, tight.is_exact(t, 1, e))
